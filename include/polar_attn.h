@@ -64,7 +64,9 @@ typedef enum {
     POLAR_ERR_TIMEOUT = 5,     /* device: a bounded wait ran out */
     POLAR_ERR_CUDA = 6,        /* a CUDA runtime call failed */
     POLAR_ERR_BAD_SEQLEN = 7,  /* device: seqlen outside [1, max_pages*64] */
-    POLAR_ERR_BAD_SLOT = 8     /* device: memory state slot >= num_slots (polar_gdelta.h) */
+    POLAR_ERR_BAD_SLOT = 8,    /* device: memory state slot >= num_slots (polar_gdelta.h), or
+                                  a source row out of range (polar_cache.h) */
+    POLAR_ERR_NO_PAGES = 9     /* device: the page pool ran out (polar_cache.h) */
 } polar_status_t;
 
 typedef enum { POLAR_BF16 = 0, POLAR_FP32 = 1 } polar_dtype_t;
@@ -313,6 +315,86 @@ polar_status_t polar_attn_decode_paged_chunk(const void *q, const void *kv_pages
                                              const float *u, const polar_params_t *params,
                                              void *out, float *neff_out, void *workspace,
                                              size_t ws_bytes, void *stream);
+
+/*
+ * Decode for a tree of drafted tokens (speculative verification with several
+ * candidate continuations): node t of a sequence sees every cached position
+ * and the drafted nodes that its mask names.  The drafted keys and values are
+ * dense arguments and are not in the cache; once a path is accepted, its rows
+ * go there with polar_attn_cache_append (polar_cache.h).
+ *
+ *  q          [num_seqs, tree, Hq, 64] dtype, device
+ *  k, v       [num_seqs, tree, Hkv, 64] dtype, device: the drafted nodes' rows
+ *  tree_mask  [num_seqs, tree] uint64, device (8-byte aligned): bit j of node
+ *             t's word: node t sees node j (a node that sees itself has its own
+ *             bit set).  Bits at or past the sequence's node count are ignored.
+ *  tree_lens  [num_seqs] int32, device: nodes of each sequence, 0 .. tree, or
+ *             NULL: `tree` nodes each.  Rows at or past it are neither read nor
+ *             written.
+ *  tree       1 .. 64 (else POLAR_ERR_UNSUPPORTED)
+ *  seqlens    [num_seqs] int32, device: cached tokens, 0 .. 64 * max_pages
+ *             (the drafted nodes are not counted)
+ *  out        [num_seqs, tree, Hq, 64] dtype, device
+ *  neff_out   [num_seqs, tree, Hq] float32, device (may be NULL)
+ *  other arguments as polar_attn_decode_paged.
+ *
+ * n, and with it the length temperature and the null floor, is the number of
+ * keys that the node sees: seqlen + the mask's bits.  A node that sees nothing
+ * gets out = 0 and n_eff = 0.  What a node does not see does not enter its
+ * row, not even values that are not finite.  A chain (bits 0 .. t of node t)
+ * computes what polar_attn_decode_paged_chunk does once its rows are cached.
+ * params->window must be 0 (POLAR_ERR_UNSUPPORTED).  Errors as
+ * polar_attn_decode_paged; a length or node count out of range records
+ * POLAR_ERR_BAD_SEQLEN and the sequence is skipped.
+ */
+size_t polar_attn_decode_tree_workspace_size(int num_seqs, int max_pages, int tree,
+                                             const polar_params_t *params);
+
+polar_status_t polar_attn_decode_paged_tree(const void *q, const void *k, const void *v,
+                                            const uint64_t *tree_mask, const int32_t *tree_lens,
+                                            int tree, const void *kv_pages, int num_pages,
+                                            const int32_t *page_table, int max_pages,
+                                            const int32_t *seqlens, int num_seqs, const float *u,
+                                            const polar_params_t *params, void *out,
+                                            float *neff_out, void *workspace, size_t ws_bytes,
+                                            void *stream);
+
+/*
+ * Decode over selected pages: each (sequence, kv head) reads at most `keep`
+ * pages of its cache, chosen by a score on the pages' key bounds, so that a
+ * long context costs its bounds (256 bytes a page and head) and `keep` pages.
+ *
+ *  q         [num_seqs, Hq, 64] dtype, device
+ *  bounds    [num_pages, Hkv, 2, 64] dtype, device: smallest and largest key of
+ *            each dimension per page (polar_attn_cache_append keeps them)
+ *  keep      pages per (sequence, kv head), >= 1
+ *  selected_out [num_seqs, Hkv, keep] int32, device (may be NULL): the logical
+ *            pages read, ascending, then -1
+ *  other arguments as polar_attn_decode_paged.
+ *
+ * score(page) = max over the group's query heads of
+ *               sum_d max(q_d lo_d, q_d hi_d)
+ *
+ * the largest product a key within the bounds can have, summed in 64 bits and
+ * rounded to float32 once.  The page of the newest token is always read; the
+ * others by score, the lower page first on a tie, a NaN score above all
+ * others.  A sequence of at most `keep` pages is read whole and the row equals
+ * polar_attn_decode_paged's.  The row is the mixing step over the positions of
+ * the selected pages: n, and with it the length temperature and the null
+ * floor, is their number.  params->window must be 0 (POLAR_ERR_UNSUPPORTED).
+ * Errors as polar_attn_decode_paged (a sequence out of range leaves its
+ * selected pages unwritten too).
+ */
+size_t polar_attn_decode_sparse_workspace_size(int num_seqs, int max_pages, int keep,
+                                               const polar_params_t *params);
+
+polar_status_t polar_attn_decode_paged_sparse(const void *q, const void *kv_pages,
+                                              const void *bounds, int num_pages,
+                                              const int32_t *page_table, int max_pages,
+                                              const int32_t *seqlens, int num_seqs, int keep,
+                                              const float *u, const polar_params_t *params,
+                                              void *out, float *neff_out, int32_t *selected_out,
+                                              void *workspace, size_t ws_bytes, void *stream);
 
 /* Bytes of device staging that polar_attn_decode_paged_host needs. */
 size_t polar_attn_decode_staging_size(int num_seqs, int max_pages, const polar_params_t *params);

@@ -1,4 +1,4 @@
-// api.cu -- the C ABI declared in include/polar_attn.h: argument validation,
+// api.cu -- the C ABI declared in include/polar_attn.h and its sisters: argument validation,
 // the per-device status word, tensor-map encoding and dispatch to the kernels.
 #include <atomic>
 #include <cmath>
@@ -8,6 +8,7 @@
 #include <cudaTypedefs.h>
 
 #include "polar_attn_selftest.h"
+#include "polar_cache.h"
 #include "polar_common.cuh"
 #include "polar_gdelta.h"
 #include "polar_internal.h"
@@ -128,6 +129,39 @@ polar_status_t check_decode_chunk(const polar_params_t *p, int num_seqs, int max
     return POLAR_OK;
 }
 
+// Tree and page-selecting decode: unwindowed.
+polar_status_t check_decode_tree(const polar_params_t *p, int num_seqs, int max_pages, int tree) {
+    polar_status_t st = check_decode(p, num_seqs, max_pages);
+    if (st != POLAR_OK) return st;
+    if (p->window != 0) return POLAR_ERR_UNSUPPORTED;
+    if (tree < 1) return POLAR_ERR_INVALID_ARG;
+    if (tree > kMaxTree) return POLAR_ERR_UNSUPPORTED;
+    return POLAR_OK;
+}
+
+polar_status_t check_decode_sparse(const polar_params_t *p, int num_seqs, int max_pages, int keep) {
+    polar_status_t st = check_decode(p, num_seqs, max_pages);
+    if (st != POLAR_OK) return st;
+    if (p->window != 0) return POLAR_ERR_UNSUPPORTED;
+    if (keep < 1) return POLAR_ERR_INVALID_ARG;
+    return POLAR_OK;
+}
+
+bool bad_pool(int num_pages, int Hkv) {
+    return num_pages < 1 || static_cast<long long>(num_pages) * 2 * Hkv * kPage > (1ll << 31) - 1;
+}
+
+// The paged cache: the pool's shape and the rows' tables.
+polar_status_t check_cache(const polar_cache_t *c, int num_seqs) {
+    if (!c) return POLAR_ERR_INVALID_ARG;
+    if (c->head_dim != kHeadDim) return POLAR_ERR_UNSUPPORTED;
+    if (c->dtype != POLAR_BF16 && c->dtype != POLAR_FP32) return POLAR_ERR_INVALID_ARG;
+    if (c->dtype != POLAR_BF16) return POLAR_ERR_UNSUPPORTED;
+    if (c->Hkv < 1 || c->Hkv > 32767 || bad_pool(c->num_pages, c->Hkv)) return POLAR_ERR_INVALID_ARG;
+    if (num_seqs < 0 || num_seqs > 65535) return POLAR_ERR_INVALID_ARG;
+    return POLAR_OK;
+}
+
 // Memory channel: shape and flag checks shared by prefill and step.
 polar_status_t check_gdelta(const polar_gdelta_params_t *p) {
     if (!p) return POLAR_ERR_INVALID_ARG;
@@ -149,6 +183,34 @@ polar_status_t check_gdelta_prefill(const polar_gdelta_params_t *p) {
 }
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The pool's pointers, and the rows' where there are rows.
+polar_status_t check_cache_ptrs(const polar_cache_t *c, const int32_t *table, int max_pages,
+                                const int32_t *lens, int num_seqs) {
+    if (max_pages < 1 || static_cast<long long>(max_pages) * kPage > (1ll << 31) - 1)
+        return POLAR_ERR_INVALID_ARG;
+    if (!c->kv_pages || !aligned16(c->kv_pages) || (c->bounds && !aligned16(c->bounds)) ||
+        (c->refs && !aligned4(c->refs)))
+        return POLAR_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!table || !lens || !aligned4(table) || !aligned4(lens)))
+        return POLAR_ERR_INVALID_ARG;
+    return POLAR_OK;
+}
+
+CacheLaunch make_cache(const polar_cache_t *c, const int32_t *table, int max_pages,
+                       const int32_t *lens, int num_seqs, int *status, void *stream) {
+    CacheLaunch a;
+    a.kv = c->kv_pages; a.bounds = c->bounds; a.refs = c->refs; a.num_pages = c->num_pages;
+    a.Hkv = c->Hkv; a.table = const_cast<int32_t *>(table); a.max_pages = max_pages;
+    a.lens = const_cast<int32_t *>(lens); a.num_seqs = num_seqs; a.workspace = nullptr;
+    a.status = status; a.stream = static_cast<cudaStream_t>(stream);
+    return a;
+}
+
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
 
 polar_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? POLAR_OK : POLAR_ERR_CUDA; }
 
@@ -596,6 +658,184 @@ polar_status_t polar_attn_decode_paged_chunk(const void *q, const void *kv_pages
     return from_cuda(launch_decode(a));
 }
 
+size_t polar_attn_decode_tree_workspace_size(int num_seqs, int max_pages, int tree,
+                                             const polar_params_t *p) {
+    if (check_decode_tree(p, num_seqs, max_pages, tree) != POLAR_OK) return 0;
+    return tree_workspace_bytes(num_seqs, max_pages, tree, p->Hq, p->Hkv);
+}
+
+polar_status_t polar_attn_decode_paged_tree(const void *q, const void *k, const void *v,
+                                            const uint64_t *tree_mask, const int32_t *tree_lens,
+                                            int tree, const void *kv_pages, int num_pages,
+                                            const int32_t *page_table, int max_pages,
+                                            const int32_t *seqlens, int num_seqs, const float *u,
+                                            const polar_params_t *p, void *out, float *neff_out,
+                                            void *workspace, size_t ws_bytes, void *stream) {
+    polar_status_t st = check_decode_tree(p, num_seqs, max_pages, tree);
+    if (st != POLAR_OK) return st;
+    if (num_seqs == 0) return POLAR_OK;
+    if (bad_pool(num_pages, p->Hkv)) return POLAR_ERR_INVALID_ARG;
+    if (!q || !k || !v || !tree_mask || !kv_pages || !page_table || !seqlens || !u || !out ||
+        !workspace)
+        return POLAR_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(kv_pages) || !aligned16(u) ||
+        !aligned16(out) || !aligned16(workspace) || !aligned4(page_table) || !aligned4(seqlens) ||
+        (tree_lens && !aligned4(tree_lens)) || (neff_out && !aligned4(neff_out)) ||
+        (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
+        return POLAR_ERR_INVALID_ARG;
+    if (ws_bytes < tree_workspace_bytes(num_seqs, max_pages, tree, p->Hq, p->Hkv))
+        return POLAR_ERR_WORKSPACE;
+    int *status = status_ptr();
+    if (!status) return POLAR_ERR_CUDA;
+    TreeLaunch a;
+    a.q = q; a.k = k; a.v = v; a.mask = tree_mask; a.tree_lens = tree_lens; a.tree = tree;
+    a.kv_pages = kv_pages; a.num_pages = num_pages; a.page_table = page_table;
+    a.max_pages = max_pages; a.seqlens = seqlens; a.num_seqs = num_seqs; a.u = u; a.out = out;
+    a.neff = neff_out; a.Hq = p->Hq; a.Hkv = p->Hkv; a.s = p->logit_scale; a.alpha = p->alpha;
+    a.beta = p->beta; a.L = p->L_train; a.workspace = workspace; a.status = status;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return from_cuda(launch_decode_tree(a));
+}
+
+size_t polar_attn_decode_sparse_workspace_size(int num_seqs, int max_pages, int keep,
+                                               const polar_params_t *p) {
+    if (check_decode_sparse(p, num_seqs, max_pages, keep) != POLAR_OK) return 0;
+    return sparse_workspace_bytes(num_seqs, max_pages, keep, p->Hq, p->Hkv);
+}
+
+polar_status_t polar_attn_decode_paged_sparse(const void *q, const void *kv_pages,
+                                              const void *bounds, int num_pages,
+                                              const int32_t *page_table, int max_pages,
+                                              const int32_t *seqlens, int num_seqs, int keep,
+                                              const float *u, const polar_params_t *p, void *out,
+                                              float *neff_out, int32_t *selected_out,
+                                              void *workspace, size_t ws_bytes, void *stream) {
+    polar_status_t st = check_decode_sparse(p, num_seqs, max_pages, keep);
+    if (st != POLAR_OK) return st;
+    if (num_seqs == 0) return POLAR_OK;
+    if (bad_pool(num_pages, p->Hkv)) return POLAR_ERR_INVALID_ARG;
+    if (!q || !kv_pages || !bounds || !page_table || !seqlens || !u || !out || !workspace)
+        return POLAR_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(kv_pages) || !aligned16(bounds) || !aligned16(u) ||
+        !aligned16(out) || !aligned16(workspace) || !aligned4(page_table) || !aligned4(seqlens) ||
+        (neff_out && !aligned4(neff_out)) || (selected_out && !aligned4(selected_out)))
+        return POLAR_ERR_INVALID_ARG;
+    if (ws_bytes < sparse_workspace_bytes(num_seqs, max_pages, keep, p->Hq, p->Hkv))
+        return POLAR_ERR_WORKSPACE;
+    int *status = status_ptr();
+    if (!status) return POLAR_ERR_CUDA;
+    SparseLaunch a;
+    a.q = q; a.kv_pages = kv_pages; a.bounds = bounds; a.num_pages = num_pages;
+    a.page_table = page_table; a.max_pages = max_pages; a.seqlens = seqlens;
+    a.num_seqs = num_seqs; a.keep = keep; a.u = u; a.out = out; a.neff = neff_out;
+    a.selected = selected_out; a.Hq = p->Hq; a.Hkv = p->Hkv; a.s = p->logit_scale;
+    a.alpha = p->alpha; a.beta = p->beta; a.L = p->L_train; a.workspace = workspace;
+    a.status = status; a.stream = static_cast<cudaStream_t>(stream);
+    return from_cuda(launch_decode_sparse(a));
+}
+
+size_t polar_attn_cache_workspace_size(const polar_cache_t *c, int num_seqs) {
+    if (check_cache(c, num_seqs) != POLAR_OK) return 0;
+    return cache_workspace_bytes(c->num_pages, num_seqs);
+}
+
+polar_status_t polar_attn_cache_reserve(const polar_cache_t *c, int32_t *page_table, int max_pages,
+                                        int32_t *seqlens, const int32_t *grow, int num_seqs,
+                                        int32_t *granted, void *workspace, size_t ws_bytes,
+                                        void *stream) {
+    polar_status_t st = check_cache(c, num_seqs);
+    if (st != POLAR_OK) return st;
+    if (num_seqs == 0) return POLAR_OK;
+    st = check_cache_ptrs(c, page_table, max_pages, seqlens, num_seqs);
+    if (st != POLAR_OK) return st;
+    if (!c->refs || !grow || !granted || !workspace || !aligned4(grow) || !aligned4(granted) ||
+        !aligned16(workspace))
+        return POLAR_ERR_INVALID_ARG;
+    if (ws_bytes < cache_workspace_bytes(c->num_pages, num_seqs)) return POLAR_ERR_WORKSPACE;
+    int *status = status_ptr();
+    if (!status) return POLAR_ERR_CUDA;
+    CacheLaunch a = make_cache(c, page_table, max_pages, seqlens, num_seqs, status, stream);
+    a.workspace = workspace;
+    return from_cuda(launch_cache_reserve(a, grow, granted));
+}
+
+polar_status_t polar_attn_cache_append(const polar_cache_t *c, const void *k, const void *v,
+                                       int src_tokens, const int32_t *pick, int tokens,
+                                       const int32_t *counts, const int32_t *page_table,
+                                       int max_pages, const int32_t *seqlens, int num_seqs,
+                                       void *stream) {
+    polar_status_t st = check_cache(c, num_seqs);
+    if (st != POLAR_OK) return st;
+    if (tokens < 0 || src_tokens < 0 || (!pick && tokens > src_tokens)) return POLAR_ERR_INVALID_ARG;
+    if (num_seqs == 0 || tokens == 0) return POLAR_OK;
+    st = check_cache_ptrs(c, page_table, max_pages, seqlens, num_seqs);
+    if (st != POLAR_OK) return st;
+    if (!k || !v || !aligned16(k) || !aligned16(v) || (pick && !aligned4(pick)) ||
+        (counts && !aligned4(counts)))
+        return POLAR_ERR_INVALID_ARG;
+    int *status = status_ptr();
+    if (!status) return POLAR_ERR_CUDA;
+    return from_cuda(launch_cache_append(
+        make_cache(c, page_table, max_pages, seqlens, num_seqs, status, stream), k, v, src_tokens,
+        pick, tokens, counts));
+}
+
+polar_status_t polar_attn_cache_fork(const polar_cache_t *c, const int32_t *src_table,
+                                     const int32_t *src_lens, int num_src,
+                                     const int32_t *src_rows, int num_dst, int32_t *dst_table,
+                                     int32_t *dst_lens, int max_pages, void *stream) {
+    polar_status_t st = check_cache(c, num_dst);
+    if (st != POLAR_OK) return st;
+    if (num_src < 0 || num_src > 65535) return POLAR_ERR_INVALID_ARG;
+    if (num_dst == 0) return POLAR_OK;
+    st = check_cache_ptrs(c, dst_table, max_pages, dst_lens, num_dst);
+    if (st == POLAR_OK) st = check_cache_ptrs(c, src_table, max_pages, src_lens, num_src);
+    if (st != POLAR_OK) return st;
+    if (!c->refs || !src_rows || !aligned4(src_rows)) return POLAR_ERR_INVALID_ARG;
+    const size_t row = static_cast<size_t>(max_pages) * 4;
+    if (overlap(src_table, num_src * row, dst_table, num_dst * row) ||
+        overlap(src_lens, static_cast<size_t>(num_src) * 4, dst_lens,
+                static_cast<size_t>(num_dst) * 4))
+        return POLAR_ERR_INVALID_ARG;
+    int *status = status_ptr();
+    if (!status) return POLAR_ERR_CUDA;
+    return from_cuda(launch_cache_fork(
+        make_cache(c, dst_table, max_pages, dst_lens, num_dst, status, stream), src_table,
+        src_lens, num_src, src_rows));
+}
+
+polar_status_t polar_attn_cache_free(const polar_cache_t *c, int32_t *page_table, int max_pages,
+                                     int32_t *seqlens, const int32_t *keep, int num_seqs,
+                                     void *stream) {
+    polar_status_t st = check_cache(c, num_seqs);
+    if (st != POLAR_OK) return st;
+    if (num_seqs == 0) return POLAR_OK;
+    st = check_cache_ptrs(c, page_table, max_pages, seqlens, num_seqs);
+    if (st != POLAR_OK) return st;
+    if (!c->refs || (keep && !aligned4(keep))) return POLAR_ERR_INVALID_ARG;
+    int *status = status_ptr();
+    if (!status) return POLAR_ERR_CUDA;
+    return from_cuda(launch_cache_free(
+        make_cache(c, page_table, max_pages, seqlens, num_seqs, status, stream), keep));
+}
+
+polar_status_t polar_attn_cache_compact(const polar_cache_t *c, int32_t *page_table, int max_pages,
+                                        const int32_t *seqlens, int num_seqs, int32_t *used,
+                                        void *workspace, size_t ws_bytes, void *stream) {
+    polar_status_t st = check_cache(c, num_seqs);
+    if (st != POLAR_OK) return st;
+    st = check_cache_ptrs(c, page_table, max_pages, seqlens, num_seqs);
+    if (st != POLAR_OK) return st;
+    if (!c->refs || !used || !workspace || !aligned4(used) || !aligned16(workspace))
+        return POLAR_ERR_INVALID_ARG;
+    if (ws_bytes < cache_workspace_bytes(c->num_pages, num_seqs)) return POLAR_ERR_WORKSPACE;
+    int *status = status_ptr();
+    if (!status) return POLAR_ERR_CUDA;
+    CacheLaunch a = make_cache(c, page_table, max_pages, seqlens, num_seqs, status, stream);
+    a.workspace = workspace;
+    return from_cuda(launch_cache_compact(a, used));
+}
+
 size_t polar_attn_decode_staging_size(int num_seqs, int max_pages, const polar_params_t *p) {
     if (check_decode(p, num_seqs, max_pages) != POLAR_OK) return 0;
     const size_t e = dtype_bytes(p->dtype);
@@ -678,7 +918,8 @@ const char *polar_attn_status_string(polar_status_t s) {
         case POLAR_ERR_TIMEOUT: return "a bounded device wait timed out";
         case POLAR_ERR_CUDA: return "CUDA runtime error";
         case POLAR_ERR_BAD_SEQLEN: return "sequence length outside [1, 64*max_pages]";
-        case POLAR_ERR_BAD_SLOT: return "memory state slot outside the state pool";
+        case POLAR_ERR_BAD_SLOT: return "memory state slot or source row out of range";
+        case POLAR_ERR_NO_PAGES: return "no free page left in the page pool";
     }
     return "unknown status";
 }

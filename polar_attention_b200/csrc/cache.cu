@@ -1,0 +1,587 @@
+// cache.cu -- the paged KV cache's own operations: growth with copy on write,
+// appending tokens with their pages' key bounds, forking and freeing rows, and
+// moving live pages together.  All state (tables, lengths, reference counts)
+// stays on the device.
+#include <algorithm>
+
+#include "polar_common.cuh"
+#include "polar_internal.h"
+
+namespace polar {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kChunkPages = 2048;      // reference counts per block of the compaction's plan
+constexpr int kRowVecs = kHeadDim / 8;  // 16-byte vectors of one key or value row
+
+__device__ __forceinline__ int pages_of(int len) { return (len + kPage - 1) / kPage; }
+
+// Inclusive sum over the block's threads; `scratch` holds one value per warp.
+// Returns this thread's inclusive prefix; *total gets the block's sum.
+template <typename T>
+__device__ __forceinline__ T block_scan(T x, T *scratch, T *total) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();  // scratch may still be read from the call before
+    if (lane == 31) scratch[w] = x;
+    __syncthreads();
+    T before = 0, sum = 0;
+    for (int i = 0; i < nw; ++i) {
+        const T s = scratch[i];
+        before += i < w ? s : 0;
+        sum += s;
+    }
+    *total = sum;
+    return x + before;
+}
+
+// ------------------------------------------------------------------ grow ---
+
+struct ReserveArgs {
+    int32_t *refs, *table, *lens, *granted;
+    const int32_t *grow;
+    int num_pages, max_pages, num_seqs;
+    // Workspace: per page the last growing row that writes it and how many
+    // do; the free pages found, in order; per row the end of its share of
+    // them, and the page copied for it (-1: none) with its destination.
+    int *owner, *sharers, *fresh, *end, *copy_src, *copy_dst, *copy_rows;
+    int *status;
+};
+
+// Plan of a growth step, one block: which rows copy their last page, how many
+// pages each row takes (a running sum over the rows), the lowest free ids (a
+// running count over the reference counts that stops once there are enough),
+// then the tables, counts and lengths.
+__global__ void __launch_bounds__(kPlanThreads) cache_reserve_plan_kernel(const ReserveArgs a) {
+    __shared__ int scratch[kPlanThreads / 32];
+    __shared__ long long wide[kPlanThreads / 32];
+    const int tid = threadIdx.x;
+
+    // A row's state before it grows; false: the row is passed over.
+    auto row = [&](int i, int *len, int *g, int *page) {
+        *len = a.lens[i];
+        *g = a.grow[i];
+        *page = -1;
+        const long long cap = static_cast<long long>(a.max_pages) * kPage;
+        if (*len < 0 || *len > cap || *g < 0 || *len + static_cast<long long>(*g) > cap) return 1;
+        if (*g > 0 && *len % kPage != 0) {
+            *page = a.table[static_cast<size_t>(i) * a.max_pages + *len / kPage];
+            if (*page < 0 || *page >= a.num_pages) return 2;
+        }
+        return 0;
+    };
+    auto for_rows = [&](auto &&f) {
+        for (int i = tid; i < a.num_seqs; i += kPlanThreads) f(i);
+    };
+    for_rows([&](int i) {
+        int len, g, page;
+        if (row(i, &len, &g, &page) == 0 && page >= 0 && a.refs[page] > 1) {
+            a.owner[page] = -1;
+            a.sharers[page] = 0;
+        }
+    });
+    __syncthreads();
+    for_rows([&](int i) {
+        int len, g, page;
+        if (row(i, &len, &g, &page) == 0 && page >= 0 && a.refs[page] > 1) {
+            atomicMax(&a.owner[page], i);
+            atomicAdd(&a.sharers[page], 1);
+        }
+    });
+    __syncthreads();
+
+    // Sums in 64 bits: many rows may ask for far more than the pool has.
+    long long asked = 0;
+    for (int i0 = 0; i0 < a.num_seqs; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        long long need = 0;
+        int copy = -1, rows = 0;
+        if (i < a.num_seqs) {
+            int len, g, page;
+            const int bad = row(i, &len, &g, &page);
+            if (bad) {
+                record_error(a.status, bad == 1 ? POLAR_ERR_BAD_SEQLEN : POLAR_ERR_BAD_PAGE);
+            } else {
+                need = pages_of(len + g) - pages_of(len);
+                if (page >= 0 && a.refs[page] > 1 &&
+                    !(a.sharers[page] == a.refs[page] && a.owner[page] == i)) {
+                    copy = page;
+                    rows = len % kPage;
+                    ++need;
+                }
+            }
+        }
+        long long total;
+        const long long end = asked + block_scan(need, wide, &total);
+        asked += total;
+        if (i < a.num_seqs) {
+            a.end[i] = static_cast<int>(min(end, 0x7fffffffll));
+            a.copy_src[i] = copy;
+            a.copy_rows[i] = rows;
+        }
+    }
+
+    const int need_all = static_cast<int>(min(asked, 0x7ffffffell));
+    int found = 0;
+    constexpr int kPer = 16;
+    for (int p0 = 0; p0 < a.num_pages && found < need_all; p0 += kPlanThreads * kPer) {
+        const int p = p0 + tid * kPer;
+        int r[kPer], mine = 0;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) r[e] = p + e < a.num_pages ? a.refs[p + e] : 1;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) mine += r[e] == 0;
+        int total;
+        int at = found + block_scan(mine, scratch, &total) - mine;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+            if (r[e] == 0) {
+                if (at < need_all) a.fresh[at] = p + e;
+                ++at;
+            }
+        found += total;
+    }
+    __syncthreads();
+
+    // A warp per row.
+    const int lane = tid & 31;
+    for (int i = tid >> 5; i < a.num_seqs; i += kPlanThreads / 32) {
+        int len, g, page;
+        const int bad = row(i, &len, &g, &page);
+        const bool served = !bad && a.end[i] <= found;
+        const int copy = a.copy_src[i];
+        const int have = bad ? 0 : pages_of(len);
+        const int extra = bad ? 0 : pages_of(len + g) - have;
+        const int first = a.end[i] - extra - (copy >= 0);
+        __syncwarp();
+        if (served) {
+            int32_t *pt = a.table + static_cast<size_t>(i) * a.max_pages;
+            for (int e = lane; e < extra; e += 32) {
+                const int id = a.fresh[first + (copy >= 0) + e];
+                pt[have + e] = id;
+                a.refs[id] = 1;
+            }
+            if (lane == 0 && copy >= 0) {
+                const int id = a.fresh[first];
+                pt[len / kPage] = id;
+                a.refs[id] = 1;
+                atomicSub(&a.refs[copy], 1);
+                a.copy_dst[i] = id;
+            }
+        }
+        if (lane == 0) {
+            if (!served || copy < 0) a.copy_dst[i] = -1;
+            if (!served && !bad && g > 0) record_error(a.status, POLAR_ERR_NO_PAGES);
+            a.granted[i] = served ? g : 0;
+            if (served) a.lens[i] = len + g;
+        }
+    }
+}
+
+// The copies of a growth step: block (row, K|V and head), the valid rows of
+// one 8 KB block; the first 2 * Hkv blocks of a row also copy the bounds.
+__global__ void __launch_bounds__(128)
+cache_reserve_copy_kernel(uint4 *__restrict__ kv, uint4 *__restrict__ bounds,
+                          const int *__restrict__ copy_src, const int *__restrict__ copy_dst,
+                          const int *__restrict__ copy_rows, int Hkv) {
+    const int i = blockIdx.x, blk = blockIdx.y;
+    const int dst = copy_dst[i];
+    if (dst < 0) return;
+    const int src = copy_src[i], vecs = copy_rows[i] * kRowVecs;
+    const size_t step = static_cast<size_t>(2) * Hkv;
+    const uint4 *from = kv + (src * step + blk) * (kPage * kRowVecs);
+    uint4 *to = kv + (dst * step + blk) * (kPage * kRowVecs);
+#pragma unroll 4
+    for (int e = threadIdx.x; e < vecs; e += 128) to[e] = from[e];
+    if (bounds && threadIdx.x < kRowVecs)
+        bounds[(dst * step + blk) * kRowVecs + threadIdx.x] =
+            bounds[(src * step + blk) * kRowVecs + threadIdx.x];
+}
+
+// ---------------------------------------------------------------- append ---
+
+struct AppendArgs {
+    const uint4 *k, *v;
+    uint4 *kv, *bounds;
+    const int32_t *refs, *pick, *counts, *table, *lens;
+    int src_tokens, tokens, num_pages, max_pages, Hkv;
+    int *status;
+};
+
+__device__ __forceinline__ uint32_t bmin2(uint32_t a, uint32_t b) {
+    __nv_bfloat162 r = __hmin2_nan(reinterpret_cast<__nv_bfloat162 &>(a),
+                                   reinterpret_cast<__nv_bfloat162 &>(b));
+    return reinterpret_cast<uint32_t &>(r);
+}
+__device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
+    __nv_bfloat162 r = __hmax2_nan(reinterpret_cast<__nv_bfloat162 &>(a),
+                                   reinterpret_cast<__nv_bfloat162 &>(b));
+    return reinterpret_cast<uint32_t &>(r);
+}
+__device__ __forceinline__ uint4 bmin8(uint4 a, uint4 b) {
+    return make_uint4(bmin2(a.x, b.x), bmin2(a.y, b.y), bmin2(a.z, b.z), bmin2(a.w, b.w));
+}
+__device__ __forceinline__ uint4 bmax8(uint4 a, uint4 b) {
+    return make_uint4(bmax2(a.x, b.x), bmax2(a.y, b.y), bmax2(a.z, b.z), bmax2(a.w, b.w));
+}
+__device__ __forceinline__ uint4 shfl8(uint4 a, int o) {
+    return make_uint4(__shfl_xor_sync(0xffffffffu, a.x, o), __shfl_xor_sync(0xffffffffu, a.y, o),
+                      __shfl_xor_sync(0xffffffffu, a.z, o), __shfl_xor_sync(0xffffffffu, a.w, o));
+}
+
+// Block (touched page of the row, kv head, row): thread (row r0 of 16, vector
+// c of 8) moves rows r0, r0 + 16, ... of the page.  Rows before the first new
+// token are read back where the bounds need them.
+__global__ void __launch_bounds__(128) cache_append_kernel(const AppendArgs a) {
+    __shared__ uint4 part[2][4][kRowVecs];
+    const int i = blockIdx.z, g = blockIdx.y;
+    const int len = a.lens[i], cnt = a.counts ? a.counts[i] : a.tokens;
+    if (cnt < 0 || cnt > a.tokens || len < cnt ||
+        len > static_cast<long long>(a.max_pages) * kPage) {
+        if (blockIdx.x == 0 && g == 0 && threadIdx.x == 0)
+            record_error(a.status, POLAR_ERR_BAD_SEQLEN);
+        return;
+    }
+    const int first = len - cnt;  // position of the first new token
+    const int lp = first / kPage + blockIdx.x;
+    if (cnt == 0 || lp >= pages_of(len)) return;
+    const int page = a.table[static_cast<size_t>(i) * a.max_pages + lp];
+    if (page < 0 || page >= a.num_pages || (a.refs && a.refs[page] != 1)) {
+        if (g == 0 && threadIdx.x == 0) record_error(a.status, POLAR_ERR_BAD_PAGE);
+        return;
+    }
+    const int lo = max(first - lp * kPage, 0), hi = min(len - lp * kPage, kPage);
+    const int c = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+    uint4 *kp = a.kv + (static_cast<size_t>(page) * 2 * a.Hkv + g) * (kPage * kRowVecs);
+    uint4 *vp = kp + static_cast<size_t>(a.Hkv) * (kPage * kRowVecs);
+
+    uint4 kx[4], vx[4];
+    bool write[4], have[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int r = r0 + 16 * e;
+        write[e] = r >= lo && r < hi;
+        have[e] = r < hi && (write[e] || a.bounds != nullptr);
+        kx[e] = vx[e] = make_uint4(0, 0, 0, 0);
+        if (write[e]) {
+            const int t = lp * kPage + r - first;
+            const int from = a.pick ? a.pick[static_cast<size_t>(i) * a.tokens + t] : t;
+            if (from < 0 || from >= a.src_tokens) {
+                record_error(a.status, POLAR_ERR_BAD_SLOT);
+                write[e] = false;  // the row stays as it is, and its key counts as it is
+            } else {
+                const size_t at =
+                    ((static_cast<size_t>(i) * a.src_tokens + from) * a.Hkv + g) * kRowVecs + c;
+                kx[e] = __ldg(a.k + at);
+                vx[e] = __ldg(a.v + at);
+            }
+        }
+        if (have[e] && !write[e] && a.bounds) kx[e] = kp[r * kRowVecs + c];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (write[e]) {
+            kp[(r0 + 16 * e) * kRowVecs + c] = kx[e];
+            vp[(r0 + 16 * e) * kRowVecs + c] = vx[e];
+        }
+    if (!a.bounds) return;
+    const uint32_t inf = 0x7f807f80u, ninf = 0xff80ff80u;
+    uint4 mn = make_uint4(inf, inf, inf, inf), mx = make_uint4(ninf, ninf, ninf, ninf);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (have[e]) {
+            mn = bmin8(mn, kx[e]);
+            mx = bmax8(mx, kx[e]);
+        }
+#pragma unroll
+    for (int o = 8; o <= 16; o <<= 1) {  // the warp's four rows of each vector
+        mn = bmin8(mn, shfl8(mn, o));
+        mx = bmax8(mx, shfl8(mx, o));
+    }
+    const int w = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) < kRowVecs) {
+        part[0][w][c] = mn;
+        part[1][w][c] = mx;
+    }
+    __syncthreads();
+    if (threadIdx.x < 2 * kRowVecs) {
+        const int which = threadIdx.x >> 3;
+        uint4 x = part[which][0][c];
+#pragma unroll
+        for (int k = 1; k < 4; ++k)
+            x = which ? bmax8(x, part[1][k][c]) : bmin8(x, part[0][k][c]);
+        a.bounds[(static_cast<size_t>(page) * a.Hkv + g) * 2 * kRowVecs + threadIdx.x] = x;
+    }
+}
+
+// ----------------------------------------------------------- fork, free ---
+
+__global__ void __launch_bounds__(256)
+cache_fork_kernel(int32_t *__restrict__ refs, int num_pages,
+                  const int32_t *__restrict__ src_table, const int32_t *__restrict__ src_lens,
+                  int num_src, const int32_t *__restrict__ src_rows,
+                  int32_t *__restrict__ dst_table, int32_t *__restrict__ dst_lens, int max_pages,
+                  int *status) {
+    const int i = blockIdx.y;
+    const bool says = blockIdx.x == 0 && threadIdx.x == 0;
+    const int src = src_rows[i];
+    if (src < 0) return;
+    if (src >= num_src) {
+        if (says) record_error(status, POLAR_ERR_BAD_SLOT);
+        return;
+    }
+    const int len = src_lens[src];
+    if (len < 0 || len > static_cast<long long>(max_pages) * kPage) {
+        if (says) record_error(status, POLAR_ERR_BAD_SEQLEN);
+        return;
+    }
+    if (says) dst_lens[i] = len;
+    const int n = pages_of(len);
+    for (int c = blockIdx.x * 256 + threadIdx.x; c < n; c += gridDim.x * 256) {
+        const int p = src_table[static_cast<size_t>(src) * max_pages + c];
+        dst_table[static_cast<size_t>(i) * max_pages + c] = p;
+        if (p >= 0 && p < num_pages)
+            atomicAdd(&refs[p], 1);
+        else
+            record_error(status, POLAR_ERR_BAD_PAGE);
+    }
+}
+
+// One block per row, so that the row's length is read by all its threads
+// before it changes.
+__global__ void __launch_bounds__(256)
+cache_free_kernel(int32_t *__restrict__ refs, int num_pages, int32_t *__restrict__ table,
+                  int max_pages, int32_t *__restrict__ lens, const int32_t *__restrict__ keep,
+                  int *status) {
+    const int i = blockIdx.x;
+    const int len = lens[i], kept = keep ? keep[i] : 0;
+    __syncthreads();
+    if (len < 0 || len > static_cast<long long>(max_pages) * kPage) {
+        if (threadIdx.x == 0) record_error(status, POLAR_ERR_BAD_SEQLEN);
+        return;
+    }
+    if (kept < 0 || kept >= len) return;
+    if (threadIdx.x == 0) lens[i] = kept;
+    int32_t *pt = table + static_cast<size_t>(i) * max_pages;
+    for (int c = pages_of(kept) + threadIdx.x; c < pages_of(len); c += 256) {
+        const int p = pt[c];
+        pt[c] = -1;
+        if (p < 0 || p >= num_pages) {
+            record_error(status, POLAR_ERR_BAD_PAGE);
+        } else if (atomicSub(&refs[p], 1) <= 0) {
+            atomicAdd(&refs[p], 1);
+            record_error(status, POLAR_ERR_BAD_PAGE);
+        }
+    }
+}
+
+// --------------------------------------------------------------- compact ---
+
+struct CompactArgs {
+    int32_t *refs, *table, *used;
+    const int32_t *lens;
+    uint4 *kv, *bounds;
+    int num_pages, max_pages, num_seqs, Hkv, chunks;
+    // Workspace: live pages per chunk of the counts; [0] pages that move, [1]
+    // live pages; per page its rank among the movers (-1: none); the movers
+    // and their places, by rank.
+    int *counts, *head, *rank, *src, *dst;
+    int *status;
+};
+
+__global__ void __launch_bounds__(256) cache_compact_count_kernel(const CompactArgs a) {
+    int live = 0;
+    const int p0 = blockIdx.x * kChunkPages;
+    for (int p = p0 + threadIdx.x; p < min(p0 + kChunkPages, a.num_pages); p += 256)
+        live += a.refs[p] > 0;
+    __shared__ int scratch[8];
+    int total;
+    block_scan(live, scratch, &total);
+    if (threadIdx.x == 0) a.counts[blockIdx.x] = total;
+}
+
+// With n live pages and L(x) live pages below id x: a live page p >= n is the
+// (L(p) - L(n))-th mover, a free id p < n the (p - L(p))-th place.
+__global__ void __launch_bounds__(256) cache_compact_plan_kernel(const CompactArgs a) {
+    __shared__ int scratch[8];
+    const int tid = threadIdx.x;
+    int mine = 0, all = 0;
+    for (int c = tid; c < a.chunks; c += 256) {
+        const int x = a.counts[c];
+        all += x;
+        mine += c < blockIdx.x ? x : 0;
+    }
+    int n, before;
+    block_scan(all, scratch, &n);
+    block_scan(mine, scratch, &before);
+    // L(n): the chunks below n's, and n's own chunk up to n.
+    const int cn = n / kChunkPages;
+    int below = 0;
+    for (int c = tid; c < cn; c += 256) below += a.counts[c];
+    for (int p = cn * kChunkPages + tid; p < n; p += 256) below += a.refs[p] > 0;
+    int live_below;
+    block_scan(below, scratch, &live_below);
+
+    constexpr int kPer = kChunkPages / 256;
+    const int p0 = blockIdx.x * kChunkPages + tid * kPer;
+    bool live[kPer];
+    int count = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        live[e] = p0 + e < a.num_pages && a.refs[p0 + e] > 0;
+        count += live[e];
+    }
+    int total;
+    int upto = before + block_scan(count, scratch, &total) - count;  // L(p0)
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        const int p = p0 + e;
+        if (p < a.num_pages) {
+            if (p < n) {
+                a.rank[p] = live[e] ? -2 : -1;  // -2: stays
+                if (!live[e]) a.dst[p - upto] = p;
+            } else {
+                a.rank[p] = live[e] ? upto - live_below : -1;
+                if (live[e]) a.src[upto - live_below] = p;
+            }
+        }
+        upto += live[e];
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+        a.head[0] = n - live_below;
+        a.used[0] = n;
+    }
+}
+
+// Copies the movers' blocks (8 KB units), then rewrites references and tables.
+__global__ void __launch_bounds__(256) cache_compact_move_kernel(const CompactArgs a) {
+    const int moves = a.head[0];
+    const int per = 2 * a.Hkv;  // 8 KB blocks of a page
+    const long long units = static_cast<long long>(moves) * per;
+    for (long long unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int k = static_cast<int>(unit / per), blk = static_cast<int>(unit % per);
+        const size_t s = static_cast<size_t>(a.src[k]) * per + blk;
+        const size_t d = static_cast<size_t>(a.dst[k]) * per + blk;
+        const uint4 *from = a.kv + s * (kPage * kRowVecs) + threadIdx.x;
+        uint4 *to = a.kv + d * (kPage * kRowVecs) + threadIdx.x;
+        const uint4 x = __ldg(from), y = __ldg(from + 256);
+        to[0] = x;
+        to[256] = y;
+        if (a.bounds && threadIdx.x < kRowVecs)
+            a.bounds[d * kRowVecs + threadIdx.x] = a.bounds[s * kRowVecs + threadIdx.x];
+        if (blk == 0 && threadIdx.x == 0) {
+            a.refs[a.dst[k]] = a.refs[a.src[k]];
+            a.refs[a.src[k]] = 0;
+        }
+    }
+    const long long entries = static_cast<long long>(a.num_seqs) * a.max_pages;
+    for (long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; e < entries;
+         e += static_cast<long long>(gridDim.x) * 256) {
+        const int i = static_cast<int>(e / a.max_pages), c = static_cast<int>(e % a.max_pages);
+        const int len = a.lens[i];
+        if (len < 0 || len > static_cast<long long>(a.max_pages) * kPage) {
+            if (c == 0) record_error(a.status, POLAR_ERR_BAD_SEQLEN);
+            continue;
+        }
+        if (c >= pages_of(len)) continue;
+        const int p = a.table[e];
+        const int r = p >= 0 && p < a.num_pages ? a.rank[p] : -1;
+        if (r == -1)
+            record_error(a.status, POLAR_ERR_BAD_PAGE);
+        else if (r >= 0)
+            a.table[e] = a.dst[r];
+    }
+}
+
+int chunk_count(int num_pages) { return (num_pages + kChunkPages - 1) / kChunkPages; }
+
+}  // namespace
+
+size_t cache_workspace_bytes(int num_pages, int num_seqs) {
+    // Three ints a page (reserve: owner, sharers, fresh; compact: rank, src,
+    // dst), four a row, the compaction's chunk counts and its head.
+    return (3 * static_cast<size_t>(num_pages) + 4 * static_cast<size_t>(num_seqs) +
+            chunk_count(num_pages) + 4) * sizeof(int);
+}
+
+cudaError_t launch_cache_reserve(const CacheLaunch &a, const int32_t *grow, int32_t *granted) {
+    int *ws = static_cast<int *>(a.workspace);
+    ReserveArgs r;
+    r.refs = a.refs; r.table = a.table; r.lens = a.lens; r.grow = grow; r.granted = granted;
+    r.num_pages = a.num_pages; r.max_pages = a.max_pages; r.num_seqs = a.num_seqs;
+    r.owner = ws; r.sharers = ws + a.num_pages; r.fresh = ws + 2 * static_cast<size_t>(a.num_pages);
+    int *rows = ws + 3 * static_cast<size_t>(a.num_pages);
+    r.end = rows; r.copy_src = rows + a.num_seqs;
+    r.copy_dst = rows + 2 * static_cast<size_t>(a.num_seqs);
+    r.copy_rows = rows + 3 * static_cast<size_t>(a.num_seqs);
+    r.status = a.status;
+    cache_reserve_plan_kernel<<<1, kPlanThreads, 0, a.stream>>>(r);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cache_reserve_copy_kernel<<<dim3(a.num_seqs, 2 * a.Hkv), 128, 0, a.stream>>>(
+        static_cast<uint4 *>(a.kv), static_cast<uint4 *>(a.bounds), r.copy_src, r.copy_dst,
+        r.copy_rows, a.Hkv);
+    count_launches(2);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_append(const CacheLaunch &a, const void *k, const void *v, int src_tokens,
+                                const int32_t *pick, int tokens, const int32_t *counts) {
+    AppendArgs p;
+    p.k = static_cast<const uint4 *>(k); p.v = static_cast<const uint4 *>(v);
+    p.kv = static_cast<uint4 *>(a.kv); p.bounds = static_cast<uint4 *>(a.bounds);
+    p.refs = a.refs; p.pick = pick; p.counts = counts; p.table = a.table; p.lens = a.lens;
+    p.src_tokens = src_tokens; p.tokens = tokens; p.num_pages = a.num_pages;
+    p.max_pages = a.max_pages; p.Hkv = a.Hkv; p.status = a.status;
+    // Pages that `tokens` new tokens can touch, from any offset in a page.
+    const int touched = static_cast<int>(
+        std::min<long long>(a.max_pages, (tokens - 1ll + kPage - 1) / kPage + 1));
+    cache_append_kernel<<<dim3(touched, a.Hkv, a.num_seqs), 128, 0, a.stream>>>(p);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_fork(const CacheLaunch &a, const int32_t *src_table,
+                              const int32_t *src_lens, int num_src, const int32_t *src_rows) {
+    const int blocks = std::min((a.max_pages + 255) / 256, 64);
+    cache_fork_kernel<<<dim3(blocks, a.num_seqs), 256, 0, a.stream>>>(
+        a.refs, a.num_pages, src_table, src_lens, num_src, src_rows, a.table, a.lens, a.max_pages,
+        a.status);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_free(const CacheLaunch &a, const int32_t *keep) {
+    cache_free_kernel<<<a.num_seqs, 256, 0, a.stream>>>(a.refs, a.num_pages, a.table, a.max_pages,
+                                                       a.lens, keep, a.status);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_compact(const CacheLaunch &a, int32_t *used) {
+    int *ws = static_cast<int *>(a.workspace);
+    CompactArgs c;
+    c.refs = a.refs; c.table = a.table; c.lens = a.lens; c.used = used;
+    c.kv = static_cast<uint4 *>(a.kv); c.bounds = static_cast<uint4 *>(a.bounds);
+    c.num_pages = a.num_pages; c.max_pages = a.max_pages; c.num_seqs = a.num_seqs; c.Hkv = a.Hkv;
+    c.chunks = chunk_count(a.num_pages);
+    c.rank = ws; c.src = ws + a.num_pages; c.dst = ws + 2 * static_cast<size_t>(a.num_pages);
+    c.counts = ws + 3 * static_cast<size_t>(a.num_pages);
+    c.head = c.counts + c.chunks;
+    c.status = a.status;
+    cache_compact_count_kernel<<<c.chunks, 256, 0, a.stream>>>(c);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cache_compact_plan_kernel<<<c.chunks, 256, 0, a.stream>>>(c);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cache_compact_move_kernel<<<148 * 8, 256, 0, a.stream>>>(c);
+    count_launches(3);
+    return cudaGetLastError();
+}
+
+}  // namespace polar

@@ -86,6 +86,62 @@ struct GdeltaStepLaunch {          // one decode token per sequence, in place
     cudaStream_t stream;
 };
 
+struct TreeLaunch {                // a tree of drafted tokens over the paged cache
+    const void *q;                 // [num_seqs, tree, Hq, 64]
+    const void *k, *v;             // drafted rows [num_seqs, tree, Hkv, 64]
+    const uint64_t *mask;          // [num_seqs, tree]
+    const int32_t *tree_lens;      // [num_seqs], or null: tree
+    int tree;
+    const void *kv_pages;
+    int num_pages;
+    const int32_t *page_table;
+    int max_pages;
+    const int32_t *seqlens;
+    int num_seqs;
+    const float *u;
+    void *out;
+    float *neff;
+    int Hq, Hkv;
+    float s, alpha, beta;
+    int L;
+    void *workspace;               // tree_workspace_bytes
+    int *status;
+    cudaStream_t stream;
+};
+
+struct SparseLaunch {              // decode over the pages that their bounds select
+    const void *q;                 // [num_seqs, Hq, 64]
+    const void *kv_pages, *bounds;
+    int num_pages;
+    const int32_t *page_table;
+    int max_pages;
+    const int32_t *seqlens;
+    int num_seqs, keep;
+    const float *u;
+    void *out;
+    float *neff;
+    int32_t *selected;             // [num_seqs, Hkv, keep], or null
+    int Hq, Hkv;
+    float s, alpha, beta;
+    int L;
+    void *workspace;               // sparse_workspace_bytes
+    int *status;
+    cudaStream_t stream;
+};
+
+struct CacheLaunch {               // the paged cache's own operations
+    void *kv, *bounds;             // bounds may be null
+    int32_t *refs;
+    int num_pages, Hkv;
+    int32_t *table;
+    int max_pages;
+    int32_t *lens;
+    int num_seqs;
+    void *workspace;               // cache_workspace_bytes (reserve, compact)
+    int *status;
+    cudaStream_t stream;
+};
+
 // Per-row coefficient record of the backward's bf16 path (fp32 words), written
 // by the rows pass for every row of the sequence padded to a multiple of 128
 // (rows past the end carry cl2 = c = 0 and nref = -inf, which give zero weights
@@ -135,6 +191,22 @@ cudaError_t launch_bwd_from_state(const BwdLaunch &l, const void *out, const flo
 cudaError_t launch_gdelta_prefill(const GdeltaLaunch &a);
 cudaError_t launch_gdelta_step(const GdeltaStepLaunch &a);
 size_t gdelta_workspace_bytes(int B, int T, int H);
+
+cudaError_t launch_decode_tree(const TreeLaunch &a);
+size_t tree_workspace_bytes(int num_seqs, int max_pages, int tree, int Hq, int Hkv);
+cudaError_t launch_decode_sparse(const SparseLaunch &a);
+size_t sparse_workspace_bytes(int num_seqs, int max_pages, int keep, int Hq, int Hkv);
+// Tensor map over the page pool's rows of 64 (box: one page's block of a head).
+bool page_pool_map(CUtensorMap *map, const void *kv_pages, int num_pages, int Hkv);
+
+cudaError_t launch_cache_reserve(const CacheLaunch &a, const int32_t *grow, int32_t *granted);
+cudaError_t launch_cache_append(const CacheLaunch &a, const void *k, const void *v, int src_tokens,
+                                const int32_t *pick, int tokens, const int32_t *counts);
+cudaError_t launch_cache_fork(const CacheLaunch &a, const int32_t *src_table,
+                              const int32_t *src_lens, int num_src, const int32_t *src_rows);
+cudaError_t launch_cache_free(const CacheLaunch &a, const int32_t *keep);
+cudaError_t launch_cache_compact(const CacheLaunch &a, int32_t *used);
+size_t cache_workspace_bytes(int num_pages, int num_seqs);
 
 // Key moments of causal prefill (fwd_moments.cu): one record of kMomFloats
 // fp32 (the 64 x 64 key Gram, then the 64 key sums) per (batch, kv head, full

@@ -1,5 +1,5 @@
-"""ctypes binding of libpolar_attn.so, the C ABI of include/polar_attn.h and
-include/polar_gdelta.h.
+"""ctypes binding of libpolar_attn.so, the C ABI of include/polar_attn.h,
+include/polar_gdelta.h and include/polar_cache.h.
 
 Argument marshalling only: torch tensors supply device memory and streams, and
 every step of the computation runs in the library's CUDA kernels.  There is no
@@ -8,6 +8,7 @@ CPU or PyTorch fallback; a missing or unloadable library raises at once.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -20,9 +21,10 @@ POLAR_BF16, POLAR_FP32 = 0, 1
 IMPLS = {"auto": 0, "simt": 1, "tc": 2}
 STATUS = {0: "POLAR_OK", 1: "POLAR_ERR_INVALID_ARG", 2: "POLAR_ERR_UNSUPPORTED",
           3: "POLAR_ERR_WORKSPACE", 4: "POLAR_ERR_BAD_PAGE", 5: "POLAR_ERR_TIMEOUT",
-          6: "POLAR_ERR_CUDA", 7: "POLAR_ERR_BAD_SEQLEN", 8: "POLAR_ERR_BAD_SLOT"}
+          6: "POLAR_ERR_CUDA", 7: "POLAR_ERR_BAD_SEQLEN", 8: "POLAR_ERR_BAD_SLOT",
+          9: "POLAR_ERR_NO_PAGES"}
 
-# Every entry point include/polar_attn.h and include/polar_gdelta.h declare.
+# Every entry point that the headers under include/ declare.
 EXPORTS = ["polar_attn_default_params", "polar_attn_fwd_workspace_size", "polar_attn_fwd",
            "polar_attn_fwd_ws",
            "polar_attn_fwd_staging_size",
@@ -35,7 +37,12 @@ EXPORTS = ["polar_attn_default_params", "polar_attn_fwd_workspace_size", "polar_
            "polar_gdelta_prefill_workspace_size", "polar_gdelta_prefill", "polar_gdelta_step",
            "polar_attn_selftest_timeout", "polar_attn_selftest_decode_per_head",
            "polar_attn_fwd_state_size", "polar_attn_fwd_train", "polar_attn_bwd_from_state",
-           "polar_attn_selftest_fwd_host_segments"]
+           "polar_attn_selftest_fwd_host_segments",
+           "polar_attn_decode_tree_workspace_size", "polar_attn_decode_paged_tree",
+           "polar_attn_decode_sparse_workspace_size", "polar_attn_decode_paged_sparse",
+           "polar_attn_cache_workspace_size", "polar_attn_cache_reserve",
+           "polar_attn_cache_append", "polar_attn_cache_fork", "polar_attn_cache_free",
+           "polar_attn_cache_compact"]
 
 
 class PolarError(RuntimeError):
@@ -58,6 +65,13 @@ class GdeltaParams(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
                 ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("zero_init", ctypes.c_int),
                 ("accumulate", ctypes.c_int)]
+
+
+class Cache(ctypes.Structure):
+    """polar_cache_t."""
+    _fields_ = [("kv_pages", ctypes.c_void_p), ("bounds", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
 _lib = None
@@ -115,6 +129,22 @@ def lib() -> ctypes.CDLL:
             L.polar_gdelta_prefill_workspace_size.restype = Z
             L.polar_gdelta_prefill.argtypes = [P, P, P, P, P, P, GP, P, P, Z, P]
             L.polar_gdelta_step.argtypes = [P, P, P, P, P, P, I, P, I, GP, P, P]
+            CP = ctypes.POINTER(Cache)
+            L.polar_attn_decode_tree_workspace_size.argtypes = [I, I, I, PP]
+            L.polar_attn_decode_tree_workspace_size.restype = Z
+            L.polar_attn_decode_paged_tree.argtypes = [P, P, P, P, P, I, P, I, P, I, P, I, P, PP,
+                                                       P, P, P, Z, P]
+            L.polar_attn_decode_sparse_workspace_size.argtypes = [I, I, I, PP]
+            L.polar_attn_decode_sparse_workspace_size.restype = Z
+            L.polar_attn_decode_paged_sparse.argtypes = [P, P, P, I, P, I, P, I, I, P, PP, P, P, P,
+                                                         P, Z, P]
+            L.polar_attn_cache_workspace_size.argtypes = [CP, I]
+            L.polar_attn_cache_workspace_size.restype = Z
+            L.polar_attn_cache_reserve.argtypes = [CP, P, I, P, P, I, P, P, Z, P]
+            L.polar_attn_cache_append.argtypes = [CP, P, P, I, P, I, P, P, I, P, I, P]
+            L.polar_attn_cache_fork.argtypes = [CP, P, P, I, P, I, P, P, I, P]
+            L.polar_attn_cache_free.argtypes = [CP, P, I, P, P, I, P]
+            L.polar_attn_cache_compact.argtypes = [CP, P, I, P, I, P, P, Z, P]
             L.polar_attn_get_status.argtypes = [P]
             L.polar_attn_status_string.argtypes = [I]
             L.polar_attn_status_string.restype = ctypes.c_char_p
@@ -125,7 +155,11 @@ def lib() -> ctypes.CDLL:
                          "polar_attn_decode_paged_chunk", "polar_attn_bwd",
                          "polar_gdelta_prefill", "polar_gdelta_step",
                          "polar_attn_selftest_timeout", "polar_attn_selftest_decode_per_head",
-                         "polar_attn_fwd_train", "polar_attn_bwd_from_state"):
+                         "polar_attn_fwd_train", "polar_attn_bwd_from_state",
+                         "polar_attn_decode_paged_tree", "polar_attn_decode_paged_sparse",
+                         "polar_attn_cache_reserve", "polar_attn_cache_append",
+                         "polar_attn_cache_fork", "polar_attn_cache_free",
+                         "polar_attn_cache_compact"):
                 getattr(L, name).restype = I
             _lib = L
     return _lib
@@ -508,6 +542,275 @@ def gdelta_step(q, k, v, alpha, beta, state_pool, slots, out=None, *, accumulate
                                    ctypes.byref(p), _ptr(out), _stream(stream)),
            "polar_gdelta_step")
     return out
+
+
+@functools.lru_cache(maxsize=64)
+def _decode_params(Hq, Hkv, D, dtype, s, alpha, L, beta):
+    """A polar_params_t of these values, and its pointer; never changed after."""
+    p = make_params(0, 0, Hq, Hkv, dtype, s, alpha, L, beta)
+    p.head_dim = D
+    return p, ctypes.pointer(p)
+
+
+class _Scope:
+    """A call on `device` and `stream` (None: the device's current stream):
+    what the call allocates belongs to that device and stream."""
+    __slots__ = ("device", "given", "stack")
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError("inputs must be contiguous CUDA tensors")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream of {stream.device} for tensors on {device}")
+        self.device, self.given, self.stack = device, stream, []
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.device.index:
+            self.stack.append(torch.cuda.device(self.device))
+        if self.given is not None:
+            self.stack.append(torch.cuda.stream(self.given))
+        for c in self.stack:
+            c.__enter__()
+        s = self.given if self.given is not None else torch.cuda.current_stream()
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.stack):
+            c.__exit__(*exc)
+
+
+def _need(name, t, dtype, shape, device):
+    """t's address, once it is a contiguous tensor of this type, shape and device."""
+    if t.dtype is dtype and t.device == device and t.is_contiguous() and tuple(t.shape) == shape:
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on {device}")
+    raise ValueError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
+
+
+def _need_or_none(name, t, dtype, shape, device):
+    return None if t is None else _need(name, t, dtype, shape, device)
+
+
+def _scratch(workspace, need, device):
+    """The workspace's address and size; a fresh one where the caller gave none."""
+    if workspace is None:
+        workspace = torch.empty(max(int(need), 16), device=device, dtype=torch.uint8)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _pool_shape(kv_pages, D):
+    if kv_pages.dim() != 5 or kv_pages.shape[1] != 2 or tuple(kv_pages.shape[3:]) != (64, D):
+        raise ValueError(f"kv_pages must be [pages, 2, Hkv, 64, {D}], not {tuple(kv_pages.shape)}")
+    return kv_pages.shape[0], kv_pages.shape[2]
+
+
+def decode_tree_workspace_size(num_seqs: int, max_pages: int, tree: int, Hq: int, Hkv: int) -> int:
+    _, pp = _decode_params(Hq, Hkv, 64, POLAR_BF16, 8.0, 0.3, 2048, 1.0)
+    return int(lib().polar_attn_decode_tree_workspace_size(num_seqs, max_pages, tree, pp))
+
+
+def decode_paged_tree(q, k, v, tree_mask, kv_pages, page_table, seqlens, u, out=None, neff=None,
+                      workspace=None, *, tree_lens=None, s=8.0, alpha=0.3, L=2048, beta=1.0,
+                      stream=None, want_neff=True):
+    """Decode for a tree of drafted tokens.  q [N,M,Hq,64], k and v [N,M,Hkv,64]
+    bf16: the drafted nodes, which are not in the cache; tree_mask [N,M] int64:
+    bit j of word t: node t sees node j; tree_lens [N] int32 (None: M nodes
+    each); kv_pages, page_table, u as decode_paged; seqlens [N] int32: cached
+    tokens, 0 and up.  Returns (out [N,M,Hq,64], neff [N,M,Hq]); rows at or past
+    a sequence's nodes are left as they are (unset where out is allocated
+    here)."""
+    N, M, Hq, D = q.shape
+    P_, Hkv = _pool_shape(kv_pages, D)
+    dev, bf16, i32, f32 = q.device, torch.bfloat16, torch.int32, torch.float32
+    max_pages = page_table.shape[1]
+    with _Scope(dev, stream) as st:
+        ptr = (_need("q", q, bf16, (N, M, Hq, D), dev), _need("k", k, bf16, (N, M, Hkv, D), dev),
+               _need("v", v, bf16, (N, M, Hkv, D), dev),
+               _need("tree_mask", tree_mask, torch.int64, (N, M), dev),
+               _need_or_none("tree_lens", tree_lens, i32, (N,), dev), M,
+               _need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, D), dev), P_,
+               _need("page_table", page_table, i32, (N, max_pages), dev), max_pages,
+               _need("seqlens", seqlens, i32, (N,), dev), N, _need("u", u, f32, (Hq, D), dev))
+        _, pp = _decode_params(Hq, Hkv, D, POLAR_BF16, s, alpha, L, beta)
+        if out is None:
+            out = torch.empty_like(q)
+        if neff is None and want_neff:
+            neff = torch.empty((N, M, Hq), device=dev, dtype=f32)
+        need = 0 if workspace is not None else \
+            lib().polar_attn_decode_tree_workspace_size(N, max_pages, M, pp)
+        workspace, wp, wb = _scratch(workspace, need, dev)
+        _check(lib().polar_attn_decode_paged_tree(
+            *ptr, pp, _need("out", out, bf16, (N, M, Hq, D), dev),
+            _need_or_none("neff", neff, f32, (N, M, Hq), dev), wp, wb, st),
+            "polar_attn_decode_paged_tree")
+    return out, neff
+
+
+def decode_sparse_workspace_size(num_seqs: int, max_pages: int, keep: int, Hq: int,
+                                 Hkv: int) -> int:
+    _, pp = _decode_params(Hq, Hkv, 64, POLAR_BF16, 8.0, 0.3, 2048, 1.0)
+    return int(lib().polar_attn_decode_sparse_workspace_size(num_seqs, max_pages, keep, pp))
+
+
+def decode_paged_sparse(q, kv_pages, bounds, page_table, seqlens, u, keep, out=None, neff=None,
+                        selected=None, workspace=None, *, s=8.0, alpha=0.3, L=2048, beta=1.0,
+                        stream=None, want_neff=True, want_selected=True):
+    """Decode over at most `keep` pages per (sequence, kv head), chosen by a
+    score on the pages' key bounds [P,Hkv,2,64] bf16 (smallest and largest key;
+    cache_append keeps them).  Other arguments as decode_paged.  Returns (out
+    [N,Hq,64], neff [N,Hq], selected [N,Hkv,keep] int32: the logical pages
+    read, ascending, then -1)."""
+    N, Hq, D = q.shape
+    P_, Hkv = _pool_shape(kv_pages, D)
+    keep = int(keep)
+    dev, bf16, i32, f32 = q.device, torch.bfloat16, torch.int32, torch.float32
+    max_pages = page_table.shape[1]
+    with _Scope(dev, stream) as st:
+        ptr = (_need("q", q, bf16, (N, Hq, D), dev),
+               _need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, D), dev),
+               _need("bounds", bounds, bf16, (P_, Hkv, 2, D), dev), P_,
+               _need("page_table", page_table, i32, (N, max_pages), dev), max_pages,
+               _need("seqlens", seqlens, i32, (N,), dev), N, keep,
+               _need("u", u, f32, (Hq, D), dev))
+        _, pp = _decode_params(Hq, Hkv, D, POLAR_BF16, s, alpha, L, beta)
+        if out is None:
+            out = torch.empty_like(q)
+        if neff is None and want_neff:
+            neff = torch.empty((N, Hq), device=dev, dtype=f32)
+        if selected is None and want_selected:
+            selected = torch.empty((N, Hkv, max(keep, 0)), device=dev, dtype=i32)
+        need = 0 if workspace is not None else \
+            lib().polar_attn_decode_sparse_workspace_size(N, max_pages, keep, pp)
+        workspace, wp, wb = _scratch(workspace, need, dev)
+        _check(lib().polar_attn_decode_paged_sparse(
+            *ptr, pp, _need("out", out, bf16, (N, Hq, D), dev),
+            _need_or_none("neff", neff, f32, (N, Hq), dev),
+            _need_or_none("selected", selected, i32, (N, Hkv, keep), dev), wp, wb, st),
+            "polar_attn_decode_paged_sparse")
+    return out, neff, selected
+
+
+class PageCache:
+    """A paged KV cache: the pool kv_pages [P,2,Hkv,64,64] bf16, the references
+    refs [P] int32 (page-table entries that name a page; 0: free; None for a
+    caller with an allocator of its own, who then only appends) and the pages'
+    key bounds [P,Hkv,2,64] bf16 (None: not kept).  Holds the tensors; page
+    tables and lengths are arguments of each call."""
+    __slots__ = ("kv_pages", "refs", "bounds", "_c", "_p")
+
+    def __init__(self, kv_pages, refs=None, bounds=None):
+        P_, Hkv = _pool_shape(kv_pages, 64)
+        dev, bf16 = kv_pages.device, torch.bfloat16
+        if dev.type != "cuda":
+            raise ValueError("inputs must be contiguous CUDA tensors")
+        self.kv_pages, self.refs, self.bounds = kv_pages, refs, bounds
+        self._c = Cache(_need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, 64), dev),
+                        _need_or_none("bounds", bounds, bf16, (P_, Hkv, 2, 64), dev),
+                        _need_or_none("refs", refs, torch.int32, (P_,), dev), P_, Hkv, 64,
+                        POLAR_BF16)
+        self._p = ctypes.pointer(self._c)
+
+
+def cache_workspace_size(cache: PageCache, num_seqs: int) -> int:
+    return int(lib().polar_attn_cache_workspace_size(cache._p, num_seqs))
+
+
+def _rows(cache, page_table, seqlens):
+    """(addresses and sizes of a page table and its lengths), rows, pages a row."""
+    dev, i32 = cache.kv_pages.device, torch.int32
+    N, max_pages = page_table.shape
+    return (_need("page_table", page_table, i32, (N, max_pages), dev),
+            _need("seqlens", seqlens, i32, (N,), dev), N, max_pages)
+
+
+def cache_reserve(cache: PageCache, page_table, seqlens, grow, granted=None, workspace=None, *,
+                  stream=None):
+    """Room for grow [N] int32 more tokens in each row: takes free pages (and
+    copies a shared last page) and grows page_table [N,max_pages] and seqlens
+    [N] (int32) in place.  Returns granted [N] int32: grow, or 0 from the first
+    row on that the pool cannot serve."""
+    dev, i32 = cache.kv_pages.device, torch.int32
+    with _Scope(dev, stream) as st:
+        table, lens, N, max_pages = _rows(cache, page_table, seqlens)
+        g = _need("grow", grow, i32, (N,), dev)
+        if granted is None:
+            granted = torch.empty_like(grow)
+        need = 0 if workspace is not None else cache_workspace_size(cache, N)
+        workspace, wp, wb = _scratch(workspace, need, dev)
+        _check(lib().polar_attn_cache_reserve(cache._p, table, max_pages, lens, g, N,
+                                              _need("granted", granted, i32, (N,), dev), wp, wb,
+                                              st), "polar_attn_cache_reserve")
+    return granted
+
+
+def cache_append(cache: PageCache, k, v, page_table, seqlens, counts=None, pick=None, *,
+                 stream=None):
+    """Writes the newest tokens of each row: token t < counts[n] (None: all) of
+    row n, from k, v [N,T,Hkv,64] row t (pick [N,C] int32: row pick[n,t]), to
+    position seqlens[n] - counts[n] + t; the touched pages' bounds are kept."""
+    dev, bf16, i32 = cache.kv_pages.device, torch.bfloat16, torch.int32
+    with _Scope(dev, stream) as st:
+        table, lens, N, max_pages = _rows(cache, page_table, seqlens)
+        if k.dim() != 4:
+            raise ValueError(f"k must be [N, T, Hkv, 64], not {tuple(k.shape)}")
+        T, Hkv = k.shape[1], cache._c.Hkv
+        C = T if pick is None else pick.shape[1]
+        _check(lib().polar_attn_cache_append(
+            cache._p, _need("k", k, bf16, (N, T, Hkv, 64), dev),
+            _need("v", v, bf16, (N, T, Hkv, 64), dev), T,
+            _need_or_none("pick", pick, i32, (N, C), dev), C,
+            _need_or_none("counts", counts, i32, (N,), dev), table, max_pages, lens, N, st),
+            "polar_attn_cache_append")
+
+
+def cache_fork(cache: PageCache, src_table, src_lens, src_rows, dst_table, dst_lens, *,
+               stream=None):
+    """Row i of dst_table, dst_lens becomes a copy of row src_rows[i] (int32) of
+    src_table, src_lens that shares its pages; a negative source leaves the row
+    alone.  The two tables may not overlap."""
+    dev, i32 = cache.kv_pages.device, torch.int32
+    with _Scope(dev, stream) as st:
+        src, slens, S, width = _rows(cache, src_table, src_lens)
+        dst, dlens, N, max_pages = _rows(cache, dst_table, dst_lens)
+        if width != max_pages:
+            raise ValueError("src_table and dst_table must be equally wide")
+        _check(lib().polar_attn_cache_fork(cache._p, src, slens, S,
+                                           _need("src_rows", src_rows, i32, (N,), dev), N, dst,
+                                           dlens, max_pages, st), "polar_attn_cache_fork")
+
+
+def cache_free(cache: PageCache, page_table, seqlens, keep=None, *, stream=None):
+    """Cuts each row to its first keep [N] int32 tokens (None: none; negative:
+    the row is left alone) and gives the pages behind them back, in place."""
+    dev = cache.kv_pages.device
+    with _Scope(dev, stream) as st:
+        table, lens, N, max_pages = _rows(cache, page_table, seqlens)
+        _check(lib().polar_attn_cache_free(
+            cache._p, table, max_pages, lens,
+            _need_or_none("keep", keep, torch.int32, (N,), dev), N, st), "polar_attn_cache_free")
+
+
+def cache_compact(cache: PageCache, page_table, seqlens, used=None, workspace=None, *,
+                  stream=None):
+    """Moves the live pages to the front of the pool and rewrites page_table (all
+    rows that name pages of this pool) in place.  Returns used [1] int32: the
+    number of live pages, which are pages 0 .. used - 1 afterwards."""
+    dev, i32 = cache.kv_pages.device, torch.int32
+    with _Scope(dev, stream) as st:
+        table, lens, N, max_pages = _rows(cache, page_table, seqlens)
+        if used is None:
+            used = torch.empty(1, device=dev, dtype=i32)
+        need = 0 if workspace is not None else cache_workspace_size(cache, N)
+        workspace, wp, wb = _scratch(workspace, need, dev)
+        _check(lib().polar_attn_cache_compact(cache._p, table, max_pages, lens, N,
+                                              _need("used", used, i32, (1,), dev), wp, wb, st),
+               "polar_attn_cache_compact")
+    return used
 
 
 def selftest_decode_per_head(q, kv_pages, page_table, seqlens, u, out=None, neff=None,
