@@ -4,6 +4,7 @@
 // stays on the device.
 #include <algorithm>
 
+#include "launch.cuh"
 #include "polar_common.cuh"
 #include "polar_internal.h"
 
@@ -41,76 +42,115 @@ __device__ __forceinline__ T block_scan(T x, T *scratch, T *total) {
 
 // ------------------------------------------------------------------ grow ---
 
+constexpr int kPlanRows = 1024;  // rows whose plan is held in shared memory
+
 struct ReserveArgs {
     int32_t *refs, *table, *lens, *granted;
     const int32_t *grow;
     int num_pages, max_pages, num_seqs;
-    // Workspace: per page the last growing row that writes it and how many
-    // do; the free pages found, in order; per row the end of its share of
-    // them, and the page copied for it (-1: none) with its destination.
-    int *owner, *sharers, *fresh, *end, *copy_src, *copy_dst, *copy_rows;
+    // Workspace: per page the last growing row that writes it and how many do;
+    // the free pages found, in order; per row the running sum of pages taken
+    // and the page that it copies (-1: none), used past kPlanRows; the copies'
+    // source, destination (-1: none) and rows.
+    int *owner, *sharers, *fresh, *end, *copy, *copy_src, *copy_dst, *copy_rows;
     int *status;
 };
 
-// Plan of a growth step, one block: which rows copy their last page, how many
-// pages each row takes (a running sum over the rows), the lowest free ids (a
-// running count over the reference counts that stops once there are enough),
-// then the tables, counts and lengths.
+// Plan of a growth step, one block.  Which rows copy their last page; how many
+// pages each row takes (a running sum over the rows); the lowest free ids (a
+// running count over the reference counts that stops once there are enough);
+// then every taken page finds its row by a search in the running sums.  What
+// bounds it is the chain of dependent loads, so the first stretch of reference
+// counts is on its way before the rows are looked at, and the passes over
+// shared pages run only where a last page is shared.
 __global__ void __launch_bounds__(kPlanThreads) cache_reserve_plan_kernel(const ReserveArgs a) {
     __shared__ int scratch[kPlanThreads / 32];
     __shared__ long long wide[kPlanThreads / 32];
-    const int tid = threadIdx.x;
+    __shared__ int s_end[kPlanRows], s_copy[kPlanRows];
+    const int tid = threadIdx.x, N = a.num_seqs;
+    int *const end_of = N <= kPlanRows ? s_end : a.end;
+    int *const copy_of = N <= kPlanRows ? s_copy : a.copy;
 
-    // A row's state before it grows; false: the row is passed over.
-    auto row = [&](int i, int *len, int *g, int *page) {
-        *len = a.lens[i];
-        *g = a.grow[i];
-        *page = -1;
+    constexpr int kPer = 16;
+    int r[kPer];
+    auto fetch = [&](int p) {  // reference counts of pages p .. p + 15; past the pool: taken
+        const bool whole = p + kPer <= a.num_pages &&
+                           (reinterpret_cast<uintptr_t>(a.refs) & 15u) == 0;
+#pragma unroll
+        for (int e = 0; e < kPer; e += 4) {
+            int4 x = make_int4(1, 1, 1, 1);
+            if (whole) {
+                x = *reinterpret_cast<const int4 *>(a.refs + p + e);
+            } else {
+                if (p + e < a.num_pages) x.x = a.refs[p + e];
+                if (p + e + 1 < a.num_pages) x.y = a.refs[p + e + 1];
+                if (p + e + 2 < a.num_pages) x.z = a.refs[p + e + 2];
+                if (p + e + 3 < a.num_pages) x.w = a.refs[p + e + 3];
+            }
+            r[e] = x.x; r[e + 1] = x.y; r[e + 2] = x.z; r[e + 3] = x.w;
+        }
+    };
+    fetch(tid * kPer);
+
+    // A row before it grows: its length, its growth and, where it has a partly
+    // filled last page to write, that page and its references.
+    struct Row {
+        int len, g, page, refs, bad;
+    };
+    auto row = [&](int i) {
+        Row x{a.lens[i], a.grow[i], -1, 0, 0};
         const long long cap = static_cast<long long>(a.max_pages) * kPage;
-        if (*len < 0 || *len > cap || *g < 0 || *len + static_cast<long long>(*g) > cap) return 1;
-        if (*g > 0 && *len % kPage != 0) {
-            *page = a.table[static_cast<size_t>(i) * a.max_pages + *len / kPage];
-            if (*page < 0 || *page >= a.num_pages) return 2;
+        if (x.len < 0 || x.len > cap || x.g < 0 || x.len + static_cast<long long>(x.g) > cap) {
+            x.bad = POLAR_ERR_BAD_SEQLEN;
+        } else if (x.g > 0 && x.len % kPage != 0) {
+            x.page = a.table[static_cast<size_t>(i) * a.max_pages + x.len / kPage];
+            if (x.page < 0 || x.page >= a.num_pages) {
+                x.bad = POLAR_ERR_BAD_PAGE;
+                x.page = -1;
+            } else {
+                x.refs = a.refs[x.page];
+            }
         }
-        return 0;
+        return x;
     };
-    auto for_rows = [&](auto &&f) {
-        for (int i = tid; i < a.num_seqs; i += kPlanThreads) f(i);
-    };
-    for_rows([&](int i) {
-        int len, g, page;
-        if (row(i, &len, &g, &page) == 0 && page >= 0 && a.refs[page] > 1) {
-            a.owner[page] = -1;
-            a.sharers[page] = 0;
+    Row mine{0, 0, -1, 0, 0};  // row tid: all that is needed up to kPlanThreads rows
+    if (tid < N) mine = row(tid);
+    bool shared = mine.refs > 1;
+    for (int i = tid + kPlanThreads; i < N; i += kPlanThreads) shared |= row(i).refs > 1;
+    if (__syncthreads_or(shared)) {
+        for (int i = tid; i < N; i += kPlanThreads) {
+            const Row x = i == tid ? mine : row(i);
+            if (x.refs > 1) {
+                a.owner[x.page] = -1;
+                a.sharers[x.page] = 0;
+            }
         }
-    });
-    __syncthreads();
-    for_rows([&](int i) {
-        int len, g, page;
-        if (row(i, &len, &g, &page) == 0 && page >= 0 && a.refs[page] > 1) {
-            atomicMax(&a.owner[page], i);
-            atomicAdd(&a.sharers[page], 1);
+        __syncthreads();
+        for (int i = tid; i < N; i += kPlanThreads) {
+            const Row x = i == tid ? mine : row(i);
+            if (x.refs > 1) {
+                atomicMax(&a.owner[x.page], i);
+                atomicAdd(&a.sharers[x.page], 1);
+            }
         }
-    });
-    __syncthreads();
+        __syncthreads();
+    }
 
     // Sums in 64 bits: many rows may ask for far more than the pool has.
     long long asked = 0;
-    for (int i0 = 0; i0 < a.num_seqs; i0 += kPlanThreads) {
+    for (int i0 = 0; i0 < N; i0 += kPlanThreads) {
         const int i = i0 + tid;
         long long need = 0;
-        int copy = -1, rows = 0;
-        if (i < a.num_seqs) {
-            int len, g, page;
-            const int bad = row(i, &len, &g, &page);
-            if (bad) {
-                record_error(a.status, bad == 1 ? POLAR_ERR_BAD_SEQLEN : POLAR_ERR_BAD_PAGE);
+        int copy = -1;
+        if (i < N) {
+            const Row x = i0 == 0 ? mine : row(i);
+            if (x.bad) {
+                record_error(a.status, x.bad);
             } else {
-                need = pages_of(len + g) - pages_of(len);
-                if (page >= 0 && a.refs[page] > 1 &&
-                    !(a.sharers[page] == a.refs[page] && a.owner[page] == i)) {
-                    copy = page;
-                    rows = len % kPage;
+                need = pages_of(x.len + x.g) - pages_of(x.len);
+                if (x.refs > 1 &&
+                    !(__ldcg(&a.sharers[x.page]) == x.refs && __ldcg(&a.owner[x.page]) == i)) {
+                    copy = x.page;
                     ++need;
                 }
             }
@@ -118,77 +158,74 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_plan_kernel(const 
         long long total;
         const long long end = asked + block_scan(need, wide, &total);
         asked += total;
-        if (i < a.num_seqs) {
-            a.end[i] = static_cast<int>(min(end, 0x7fffffffll));
-            a.copy_src[i] = copy;
-            a.copy_rows[i] = rows;
+        if (i < N) {
+            end_of[i] = static_cast<int>(min(end, 0x7fffffffll));
+            copy_of[i] = copy;
         }
     }
 
-    const int need_all = static_cast<int>(min(asked, 0x7ffffffell));
+    const int wanted = static_cast<int>(min(asked, 0x7ffffffell));
     int found = 0;
-    constexpr int kPer = 16;
-    for (int p0 = 0; p0 < a.num_pages && found < need_all; p0 += kPlanThreads * kPer) {
+    for (int p0 = 0; p0 < a.num_pages && found < wanted; p0 += kPlanThreads * kPer) {
         const int p = p0 + tid * kPer;
-        int r[kPer], mine = 0;
+        if (p0 > 0) fetch(p);
+        int free = 0;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) r[e] = p + e < a.num_pages ? a.refs[p + e] : 1;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) mine += r[e] == 0;
+        for (int e = 0; e < kPer; ++e) free += r[e] == 0;
         int total;
-        int at = found + block_scan(mine, scratch, &total) - mine;
+        int at = found + block_scan(free, scratch, &total) - free;
 #pragma unroll
         for (int e = 0; e < kPer; ++e)
             if (r[e] == 0) {
-                if (at < need_all) a.fresh[at] = p + e;
+                if (at < wanted) a.fresh[at] = p + e;
                 ++at;
             }
         found += total;
     }
     __syncthreads();
 
-    // A warp per row.
-    const int lane = tid & 31;
-    for (int i = tid >> 5; i < a.num_seqs; i += kPlanThreads / 32) {
-        int len, g, page;
-        const int bad = row(i, &len, &g, &page);
-        const bool served = !bad && a.end[i] <= found;
-        const int copy = a.copy_src[i];
-        const int have = bad ? 0 : pages_of(len);
-        const int extra = bad ? 0 : pages_of(len + g) - have;
-        const int first = a.end[i] - extra - (copy >= 0);
-        __syncwarp();
-        if (served) {
-            int32_t *pt = a.table + static_cast<size_t>(i) * a.max_pages;
-            for (int e = lane; e < extra; e += 32) {
-                const int id = a.fresh[first + (copy >= 0) + e];
-                pt[have + e] = id;
-                a.refs[id] = 1;
-            }
-            if (lane == 0 && copy >= 0) {
-                const int id = a.fresh[first];
-                pt[len / kPage] = id;
-                a.refs[id] = 1;
-                atomicSub(&a.refs[copy], 1);
-                a.copy_dst[i] = id;
-            }
+    // Each taken page, by its place in the running sums: its row is the first
+    // whose sum is past it; the row's copy comes before its new pages.  Rows
+    // are served up to the first whose sum is past the pages found.
+    for (int k = tid; k < min(found, wanted); k += kPlanThreads) {
+        int lo = 0, hi = N - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (end_of[mid] > k) hi = mid; else lo = mid + 1;
         }
-        if (lane == 0) {
-            if (!served || copy < 0) a.copy_dst[i] = -1;
-            if (!served && !bad && g > 0) record_error(a.status, POLAR_ERR_NO_PAGES);
-            a.granted[i] = served ? g : 0;
-            if (served) a.lens[i] = len + g;
+        if (end_of[lo] > found) break;  // not served, nor any page after
+        const int j = k - (lo > 0 ? end_of[lo - 1] : 0), copy = copy_of[lo], id = a.fresh[k];
+        const int len = a.lens[lo];
+        const bool copies = copy >= 0 && j == 0;
+        const int c = copies ? len / kPage : pages_of(len) + j - (copy >= 0);
+        a.table[static_cast<size_t>(lo) * a.max_pages + c] = id;
+        a.refs[id] = 1;
+        if (copies) {
+            atomicSub(&a.refs[copy], 1);
+            a.copy_src[lo] = copy;
+            a.copy_dst[lo] = id;
+            a.copy_rows[lo] = len % kPage;
         }
+    }
+    __syncthreads();  // the lengths above are the old ones
+    for (int i = tid; i < N; i += kPlanThreads) {
+        const int len = i == tid ? mine.len : a.lens[i], g = i == tid ? mine.g : a.grow[i];
+        const int bad = i == tid ? mine.bad : row(i).bad;
+        const bool served = !bad && end_of[i] <= found;
+        if (!served || copy_of[i] < 0) a.copy_dst[i] = -1;
+        if (!served && !bad && g > 0) record_error(a.status, POLAR_ERR_NO_PAGES);
+        a.granted[i] = served ? g : 0;
+        if (served) a.lens[i] = len + g;
     }
 }
 
 // The copies of a growth step: block (row, K|V and head), the valid rows of
 // one 8 KB block; the first 2 * Hkv blocks of a row also copy the bounds.
 __global__ void __launch_bounds__(128)
-cache_reserve_copy_kernel(uint4 *__restrict__ kv, uint4 *__restrict__ bounds,
-                          const int *__restrict__ copy_src, const int *__restrict__ copy_dst,
-                          const int *__restrict__ copy_rows, int Hkv) {
+cache_reserve_copy_kernel(uint4 *kv, uint4 *bounds,
+                          const int *copy_src, const int *copy_dst, const int *copy_rows, int Hkv) {
     const int i = blockIdx.x, blk = blockIdx.y;
+    wait_for_previous_kernel();
     const int dst = copy_dst[i];
     if (dst < 0) return;
     const int src = copy_src[i], vecs = copy_rows[i] * kRowVecs;
@@ -503,8 +540,8 @@ int chunk_count(int num_pages) { return (num_pages + kChunkPages - 1) / kChunkPa
 
 size_t cache_workspace_bytes(int num_pages, int num_seqs) {
     // Three ints a page (reserve: owner, sharers, fresh; compact: rank, src,
-    // dst), four a row, the compaction's chunk counts and its head.
-    return (3 * static_cast<size_t>(num_pages) + 4 * static_cast<size_t>(num_seqs) +
+    // dst), five a row, the compaction's chunk counts and its head.
+    return (3 * static_cast<size_t>(num_pages) + 5 * static_cast<size_t>(num_seqs) +
             chunk_count(num_pages) + 4) * sizeof(int);
 }
 
@@ -514,19 +551,19 @@ cudaError_t launch_cache_reserve(const CacheLaunch &a, const int32_t *grow, int3
     r.refs = a.refs; r.table = a.table; r.lens = a.lens; r.grow = grow; r.granted = granted;
     r.num_pages = a.num_pages; r.max_pages = a.max_pages; r.num_seqs = a.num_seqs;
     r.owner = ws; r.sharers = ws + a.num_pages; r.fresh = ws + 2 * static_cast<size_t>(a.num_pages);
+    const size_t n = a.num_seqs;
     int *rows = ws + 3 * static_cast<size_t>(a.num_pages);
-    r.end = rows; r.copy_src = rows + a.num_seqs;
-    r.copy_dst = rows + 2 * static_cast<size_t>(a.num_seqs);
-    r.copy_rows = rows + 3 * static_cast<size_t>(a.num_seqs);
+    r.end = rows; r.copy = rows + n; r.copy_src = rows + 2 * n; r.copy_dst = rows + 3 * n;
+    r.copy_rows = rows + 4 * n;
     r.status = a.status;
     cache_reserve_plan_kernel<<<1, kPlanThreads, 0, a.stream>>>(r);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cache_reserve_copy_kernel<<<dim3(a.num_seqs, 2 * a.Hkv), 128, 0, a.stream>>>(
-        static_cast<uint4 *>(a.kv), static_cast<uint4 *>(a.bounds), r.copy_src, r.copy_dst,
-        r.copy_rows, a.Hkv);
     count_launches(2);
-    return cudaGetLastError();
+    return launch_ex(cache_reserve_copy_kernel, dim3(a.num_seqs, 2 * a.Hkv), 128, 0, 1, true,
+                     a.stream, static_cast<uint4 *>(a.kv), static_cast<uint4 *>(a.bounds),
+                     static_cast<const int *>(r.copy_src), static_cast<const int *>(r.copy_dst),
+                     static_cast<const int *>(r.copy_rows), a.Hkv);
 }
 
 cudaError_t launch_cache_append(const CacheLaunch &a, const void *k, const void *v, int src_tokens,

@@ -1,7 +1,7 @@
 // decode_rows.cuh -- the streaming state of a tile of query rows over cached
 // pages, shared by the tree and the page-selecting decode.
 //
-// A CTA has four warps; warp w takes tokens 16w .. 16w+15 of every page that
+// A CTA has four computing warps; warp w takes tokens 16w .. 16w+15 of every page that
 // the CTA streams, for all of the CTA's rows.  Rows sit in m16 tiles of
 // mma.sync m16n8k16 (bf16 in, fp32 accumulate): lane (gq, tq) of a tile owns
 // rows gq and, with two row sets, gq + 8.  Each row keeps the method's state:
@@ -10,6 +10,7 @@
 // accumulator.  The S fragments are the P operand of the second product.
 #pragma once
 
+#include "launch.cuh"
 #include "mma_common.cuh"
 
 namespace polar {
@@ -181,14 +182,146 @@ __device__ __forceinline__ void page_step(RowTile<kHR> (&tile)[MT], uint32_t kb,
     }
 }
 
-// Merges the four warps' states exactly (mst: [4][rows][6], macc:
-// [4][rows][64], both shared) and writes the partials of the CTA's rows;
-// dest(r) is row r's partial, or null.  The caller's threads are all here.
-template <int MT, int kHR, typename Dest>
-__device__ __forceinline__ void merge_warps(RowTile<kHR> (&tile)[MT],
-                                            float (*mst)[8 * kHR * MT][6],
-                                            float (*macc)[8 * kHR * MT][kHeadDim], int w, int lane,
-                                            Dest &&dest) {
+// --------------------------------------------------------- page streaming ---
+
+constexpr int kRingStages = 3;       // steps in flight per CTA (16 KB each; four CTAs an SM)
+constexpr int kRowWarps = 4;         // warps that compute
+constexpr int kRowThreads = 160;     // and one that copies
+constexpr int kMaxSteps = 512;       // steps of a CTA: their page ids are held in shared memory
+
+struct PageRing {
+    uint64_t full[kRingStages], empty[kRingStages];
+    int page[kMaxSteps];  // physical page of each step; -1: skipped
+};
+
+__device__ __forceinline__ void init_ring(PageRing &r) {
+    for (int st = 0; st < kRingStages; ++st) {
+        mbar_init(&r.full[st], 1);
+        mbar_init(&r.empty[st], kRowWarps);
+    }
+    fence_barrier_init();
+}
+
+// The copying warp's part: load(kk, stage, barrier) starts the copies of step kk
+// (16 KB) or arrives on the barrier without any.  Every copy has landed on
+// return, unless a wait ran out.
+template <typename Load>
+__device__ __forceinline__ void copy_steps(PageRing &r, int np, int *status, Load &&load) {
+    int kk = 0;
+    for (; kk < np; ++kk) {
+        const int st = kk % kRingStages;
+        if (kk >= kRingStages && !mbar_wait(&r.empty[st], ((kk / kRingStages) - 1) & 1, status))
+            break;
+        load(kk, st, &r.full[st]);
+    }
+    for (int j = max(0, kk - kRingStages); j < kk; ++j)
+        mbar_wait(&r.full[j % kRingStages], (j / kRingStages) & 1, status);
+}
+
+// A computing warp's part: step(kk, stage) on each step as its copies land.
+template <typename Step>
+__device__ __forceinline__ void compute_steps(PageRing &r, int np, int lane, int *status,
+                                              Step &&step) {
+    for (int kk = 0; kk < np; ++kk) {
+        const int st = kk % kRingStages;
+        if (!__all_sync(~0u, mbar_wait(&r.full[st], (kk / kRingStages) & 1, status))) break;
+        step(kk, st);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&r.empty[st]);
+    }
+}
+
+// A row's merged state, spread over eight lanes: lane j of them holds value
+// columns 8j .. 8j + 7; the statistics are the same in all.
+struct RowState {
+    float M, m_raw, l, l2, s1, s2;
+    float4 o[2];
+};
+
+// Exact merge of `count` partial states of a row by eight lanes (four rows a
+// warp; all lanes of the warp are here); part(k) is the k-th (kPartialFloats
+// layout).  M = -inf: no key seen so far.
+template <typename Part>
+__device__ __forceinline__ RowState merge_parts(int count, Part &&part) {
+    const int j = threadIdx.x & 7;
+    RowState x;
+    x.M = x.m_raw = -INFINITY;
+    x.l = x.l2 = x.s1 = x.s2 = 0.f;
+    x.o[0] = x.o[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = j; k < count; k += 8) x.M = fmaxf(x.M, part(k)[64]);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) x.M = fmaxf(x.M, __shfl_xor_sync(~0u, x.M, o));
+#pragma unroll 4
+    for (int k = 0; k < count; ++k) {
+        const float *p = part(k);
+        const float4 st = *reinterpret_cast<const float4 *>(p + 64);
+        const float2 ss = *reinterpret_cast<const float2 *>(p + 68);
+        const float4 a = *reinterpret_cast<const float4 *>(p + 8 * j);
+        const float4 b = *reinterpret_cast<const float4 *>(p + 8 * j + 4);
+        const float r = x.M == -INFINITY ? 0.f : exp2f(st.x - x.M);  // st.x: reference max, log2
+        x.l = fmaf(st.z, r, x.l);
+        x.l2 = fmaf(st.w, r * r, x.l2);
+        x.o[0] = make_float4(fmaf(a.x, r, x.o[0].x), fmaf(a.y, r, x.o[0].y),
+                             fmaf(a.z, r, x.o[0].z), fmaf(a.w, r, x.o[0].w));
+        x.o[1] = make_float4(fmaf(b.x, r, x.o[1].x), fmaf(b.y, r, x.o[1].y),
+                             fmaf(b.z, r, x.o[1].z), fmaf(b.w, r, x.o[1].w));
+        x.s1 += ss.x;
+        x.s2 += ss.y;
+        x.m_raw = fmaxf(x.m_raw, st.y);
+    }
+    return x;
+}
+
+__device__ __forceinline__ void store_part(const RowState &x, float *dst, bool real) {
+    const int j = threadIdx.x & 7;
+    if (!real) return;
+    *reinterpret_cast<float4 *>(dst + 8 * j) = x.o[0];
+    *reinterpret_cast<float4 *>(dst + 8 * j + 4) = x.o[1];
+    if (j == 0) *reinterpret_cast<float4 *>(dst + 64) = make_float4(x.M, x.m_raw, x.l, x.l2);
+    if (j == 1) *reinterpret_cast<float2 *>(dst + 68) = make_float2(x.s1, x.s2);
+}
+
+struct Epilogue {  // the method's constants at a row's end
+    float s, alpha, L, beta, inv_ln_L;
+};
+
+// out = content + count and n_eff of a row of n visible keys, by eight lanes
+// (all lanes of the warp are here; rows that are not `real` are not written).
+// A row that sees nothing gives zeros.
+__device__ __forceinline__ void finish_row(const RowState &x, int n, const Epilogue &e,
+                                           const float *__restrict__ u, __nv_bfloat16 *out,
+                                           float *neff_out, bool real) {
+    const int j = threadIdx.x & 7;
+    float ne = 0.f, mag = 0.f;
+    if (n > 0) {
+        const float nf = static_cast<float>(n);
+        const float c = e.s * length_temperature(nf, e.alpha, e.L);
+        mag = polar_magnitude(x.l, x.l2, x.m_raw, x.s1, x.s2, c, nf, e.beta, e.inv_ln_L, &ne);
+    }
+    float o[8] = {x.o[0].x, x.o[0].y, x.o[0].z, x.o[0].w, x.o[1].x, x.o[1].y, x.o[1].z, x.o[1].w};
+    float sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sq = fmaf(o[i], o[i], sq);
+#pragma unroll
+    for (int k = 1; k < 8; k <<= 1) sq += __shfl_xor_sync(~0u, sq, k);
+    if (!real) return;
+    const float inv = 1.0f / fmaxf(sqrtf(sq), 1e-30f);
+    const float4 ua = *reinterpret_cast<const float4 *>(u + 8 * j);
+    const float4 ub = *reinterpret_cast<const float4 *>(u + 8 * j + 4);
+    const float uu[8] = {ua.x, ua.y, ua.z, ua.w, ub.x, ub.y, ub.z, ub.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = n > 0 ? fmaf(mag, uu[i], o[i] * inv) : 0.f;
+    *reinterpret_cast<uint4 *>(out + 8 * j) =
+        make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                   pack_bf16x2(o[6], o[7]));
+    if (neff_out && j == 0) *neff_out = ne;
+}
+
+// Writes each warp's states of all the CTA's rows to shared memory, one partial
+// per (row, warp): parts [rows][4][kPartialFloats].
+template <int MT, int kHR>
+__device__ __forceinline__ void spill_states(RowTile<kHR> (&tile)[MT], float *parts, int w,
+                                             int lane) {
     const int gq = lane >> 2, tq = lane & 3;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -203,87 +336,51 @@ __device__ __forceinline__ void merge_warps(RowTile<kHR> (&tile)[MT],
                 t.s2[hr] += __shfl_xor_sync(0xffffffffu, t.s2[hr], o);
                 t.m_raw[hr] = fmaxf(t.m_raw[hr], __shfl_xor_sync(0xffffffffu, t.m_raw[hr], o));
             }
-            const int r = m * 8 * kHR + 8 * hr + gq;
+            float *p = parts + ((m * 8 * kHR + 8 * hr + gq) * 4 + w) * kPartialFloats;
             if (tq == 0) {
-                mst[w][r][0] = t.m_ref[hr];
-                mst[w][r][1] = t.m_raw[hr];
-                mst[w][r][2] = t.l[hr];
-                mst[w][r][3] = t.l2[hr];
-                mst[w][r][4] = t.s1[hr];
-                mst[w][r][5] = t.s2[hr];
+                *reinterpret_cast<float4 *>(p + 64) =
+                    make_float4(t.m_ref[hr], t.m_raw[hr], t.l[hr], t.l2[hr]);
+                *reinterpret_cast<float2 *>(p + 68) = make_float2(t.s1[hr], t.s2[hr]);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<float2 *>(&macc[w][r][8 * i + 2 * tq]) =
+                *reinterpret_cast<float2 *>(p + 8 * i + 2 * tq) =
                     make_float2(t.acc[i][2 * hr], t.acc[i][2 * hr + 1]);
         }
-    __syncthreads();
-    for (int r = w; r < 8 * kHR * MT; r += 4) {
-        float *dst = dest(r);
-        if (!dst) continue;
-        float M = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) M = fmaxf(M, mst[k][r][0]);
-        float2 o = make_float2(0.f, 0.f);
-        float ml = 0.f, ml2 = 0.f, ms1 = 0.f, ms2 = 0.f, mraw = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float rr = M == -INFINITY ? 0.f : exp2f(mst[k][r][0] - M);
-            const float2 x = *reinterpret_cast<const float2 *>(&macc[k][r][2 * lane]);
-            o.x = fmaf(x.x, rr, o.x);
-            o.y = fmaf(x.y, rr, o.y);
-            ml = fmaf(mst[k][r][2], rr, ml);
-            ml2 = fmaf(mst[k][r][3], rr * rr, ml2);
-            ms1 += mst[k][r][4];
-            ms2 += mst[k][r][5];
-            mraw = fmaxf(mraw, mst[k][r][1]);
-        }
-        reinterpret_cast<float2 *>(dst)[lane] = o;
-        if (lane == 0) {
-            reinterpret_cast<float4 *>(dst + 64)[0] = make_float4(M, mraw, ml, ml2);
-            reinterpret_cast<float2 *>(dst + 68)[0] = make_float2(ms1, ms2);
-        }
-    }
 }
 
-// Exact merge of a row's split partials and the epilogue, by one warp (lane
-// owns columns 2 lane, 2 lane + 1).  A row that sees nothing gives zeros.
-__device__ __forceinline__ void merge_splits(const float *__restrict__ base, int nsplit, int n,
-                                             float s, float alpha, float L, float beta,
-                                             float inv_ln_L, const float *__restrict__ u, int lane,
-                                             __nv_bfloat16 *out, float *neff_out) {
-    float M = -INFINITY;
-    for (int sp = lane; sp < nsplit; sp += 32) M = fmaxf(M, base[sp * kPartialFloats + 64]);
-    M = warp_max(M);
-    float l = 0.f, l2 = 0.f, s1 = 0.f, s2 = 0.f, m_raw = -INFINITY, a0 = 0.f, a1 = 0.f;
-#pragma unroll 4
-    for (int sp = 0; sp < nsplit; ++sp) {
-        const float *p = base + static_cast<size_t>(sp) * kPartialFloats;
-        const float4 st = *reinterpret_cast<const float4 *>(p + 64);
-        const float2 ss = *reinterpret_cast<const float2 *>(p + 68);
-        const float2 ac = reinterpret_cast<const float2 *>(p)[lane];
-        const float r = M == -INFINITY ? 0.f : exp2f(st.x - M);
-        l = fmaf(st.z, r, l);
-        l2 = fmaf(st.w, r * r, l2);
-        a0 = fmaf(ac.x, r, a0);
-        a1 = fmaf(ac.y, r, a1);
-        s1 += ss.x;
-        s2 += ss.y;
-        m_raw = fmaxf(m_raw, st.y);
+// Reduces the rows' states over the CTA's warps and the cluster's CTAs and
+// hands each of the first nrows rows to fin(row, real, state) in eight lanes of
+// the cluster (lanes past the last row get it with real = false).  parts:
+// 5 * kRows partials of shared memory, at the same place in every CTA; all
+// threads of the cluster are here.
+template <int MT, int kHR, typename Final>
+__device__ __forceinline__ void reduce_rows(RowTile<kHR> (&tile)[MT], float *parts, int nrows,
+                                            int w, int lane, Final &&fin) {
+    constexpr int kRows = 8 * kHR * MT;
+    __syncthreads();  // the page ring is free
+    if (w < kRowWarps) spill_states<MT, kHR>(tile, parts, w, lane);
+    __syncthreads();
+    float *own = parts + kRows * 4 * kPartialFloats;
+    const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+    for (int r0 = w < kRowWarps ? 4 * w : nrows; r0 < nrows; r0 += 4 * kRowWarps) {
+        const int r = min(r0 + (lane >> 3), nrows - 1);
+        const bool real = r0 + (lane >> 3) < nrows;
+        const RowState x = merge_parts(
+            4, [&](int k) { return parts + (r * 4 + k) * kPartialFloats; });
+        if (C == 1)
+            fin(r, real, x);
+        else
+            store_part(x, own + r * kPartialFloats, real);
     }
-    float ne = 0.f, mag = 0.f;
-    if (n > 0) {
-        const float nf = static_cast<float>(n);
-        const float c = s * length_temperature(nf, alpha, L);
-        mag = polar_magnitude(l, l2, m_raw, s1, s2, c, nf, beta, inv_ln_L, &ne);
+    if (C == 1) return;
+    cluster_sync();
+    for (int r0 = w < kRowWarps ? 4 * (w * C + rank) : nrows; r0 < nrows; r0 += 4 * kRowWarps * C) {
+        const int r = min(r0 + (lane >> 3), nrows - 1);
+        const bool real = r0 + (lane >> 3) < nrows;
+        fin(r, real, merge_parts(C, [&](int k) { return cluster_map(own + r * kPartialFloats, k); }));
     }
-    const float nrm = sqrtf(warp_sum(a0 * a0 + a1 * a1));
-    const float inv = 1.0f / fmaxf(nrm, 1e-30f);
-    const float2 uu = reinterpret_cast<const float2 *>(u)[lane];
-    float2 o = make_float2(fmaf(mag, uu.x, a0 * inv), fmaf(mag, uu.y, a1 * inv));
-    if (n <= 0) o = make_float2(0.f, 0.f);
-    reinterpret_cast<__nv_bfloat162 *>(out)[lane] = __floats2bfloat162_rn(o.x, o.y);
-    if (neff_out && lane == 0) *neff_out = ne;
+    cluster_sync();  // no CTA leaves while its states are read
 }
 
 }  // namespace polar

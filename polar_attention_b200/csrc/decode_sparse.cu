@@ -15,14 +15,17 @@
 
 #include "decode_rows.cuh"
 #include "polar_internal.h"
+#include "tc_common.cuh"
 
 namespace polar {
 namespace {
 
-constexpr int kStages = 3;
-constexpr int kSmem = kStages * kStageBytes + 1024;  // + alignment slack
-constexpr int kScorePages = 64;  // pages per block of the score kernel
+constexpr int kSmem = kRingStages * kStageBytes + 1024;  // + alignment slack
+constexpr int kScoreThreads = 256;
 constexpr int kSelThreads = 512;
+constexpr int kSelKeys = 10240;  // keys that the selection holds in shared memory (40 KB)
+constexpr int kScorePages = 512;  // pages of a score block at most
+constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ bool valid_len(int len, int max_pages) {
     return len >= 1 && len <= static_cast<long long>(max_pages) * kPage;
@@ -36,151 +39,415 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Block (pages, kv head, sequence); eight lanes per page, eight dimensions
-// each.  Products of two bf16 are exact in fp32; their sum is formed in 64
-// bits and rounded once, so that the order of the pages does not depend on the
-// order of the sum.
+// The score of a key (a NaN for the highest, which no score has).
+__device__ __forceinline__ float key_score(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// A page's score in 64 bits, rounded once: what the pages are ordered by.  By a
+// warp: lane (head of four, eight dimensions).
 template <int G>
-__global__ void __launch_bounds__(256)
-sparse_score_kernel(const __nv_bfloat16 *__restrict__ q, const uint4 *__restrict__ bounds,
+__device__ __forceinline__ uint32_t exact_key(const uint4 *__restrict__ q,
+                                              const uint4 *__restrict__ b, int lane) {
+    const int c = lane & 7;
+    const uint4 lo = __ldg(b + c), hi = __ldg(b + 8 + c);
+    const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
+    uint32_t best = 0;
+#pragma unroll
+    for (int h0 = 0; h0 < G; h0 += 4) {
+        const int h = min(h0 + (lane >> 3), G - 1);
+        const uint4 x = __ldg(q + h * 8 + c);
+        const uint32_t qw[4] = {x.x, x.y, x.z, x.w};
+        double s = 0.0;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+            const float qd = __uint_as_float(d & 1 ? qw[d >> 1] & 0xffff0000u : qw[d >> 1] << 16);
+            const uint32_t e = qd < 0.f ? lw[d >> 1] : hw[d >> 1];
+            s = fma(static_cast<double>(qd),
+                    static_cast<double>(__uint_as_float(d & 1 ? e & 0xffff0000u : e << 16)), s);
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(~0u, s, o);
+        best = max(best, score_key(static_cast<float>(s)));
+    }
+    return __reduce_max_sync(~0u, best);
+}
+
+// Block (pages, kv head, sequence): scores in fp32 and a bound on each one's
+// error, from which the selection sees where 64 bits are needed.  Eight lanes
+// take a page for up to four query heads, eight dimensions each (a group of
+// eight heads takes sixteen lanes).  A product of two bf16 is exact in fp32 (a
+// subnormal one aside), so a score is at most 4 roundings in a lane, one to
+// join its two sums and 3 across lanes from the exact sum: off by at most
+// 8 * 2^-24 * sum_d max_h |q_d| max(|lo_d|, |hi_d|), which with that sum's own
+// roundings is below 12 * 2^-24 of it, and 2^-100 for subnormals.
+template <int G>
+__global__ void __launch_bounds__(kScoreThreads, 3)
+sparse_score_kernel(const uint4 *__restrict__ q, const uint4 *__restrict__ bounds,
                     const int32_t *__restrict__ page_table, const int32_t *__restrict__ seqlens,
-                    uint32_t *__restrict__ keys, int num_pages, int max_pages, int Hq, int Hkv,
-                    int keep, int *status) {
+                    float2 *__restrict__ scores, int num_pages, int max_pages, int Hkv, int keep,
+                    int pages_per_block) {
+    constexpr int GH = G < 4 ? G : 4;       // heads of a lane
+    constexpr int kLanes = 8 * (G / GH);    // lanes of a page
+    constexpr int kStep = kScoreThreads / kLanes;
+    constexpr int kDeep = 4;                // pages that a lane has in flight
+    __shared__ int phys[kScorePages];
     const int g = blockIdx.y, seq = blockIdx.z;
     const int len = seqlens[seq];
     if (!valid_len(len, max_pages)) return;  // reported by the selection
     const int npg = (len + kPage - 1) / kPage;
-    if (npg <= keep) return;  // every page is read
-    const int c = threadIdx.x & 7;
-    float qf[G][8];
-    const __nv_bfloat16 *qp =
-        q + (static_cast<size_t>(seq) * Hq + static_cast<size_t>(g) * G) * kHeadDim + 8 * c;
+    const int first = blockIdx.x * pages_per_block, count = min(npg - first, pages_per_block);
+    if (npg <= keep || count <= 0) return;  // every page is read, or none is here
+    const int32_t *pt = page_table + static_cast<size_t>(seq) * max_pages + first;
+    for (int p = threadIdx.x; p < count; p += kScoreThreads) {
+        const int x = pt[p];
+        phys[p] = x >= 0 && x < num_pages ? x : -1;
+    }
+    const int c = threadIdx.x & 7, part = threadIdx.x % kLanes / 8;
+    float2 qf[GH][4], qm[4];
 #pragma unroll
-    for (int h = 0; h < G; ++h)
+    for (int d = 0; d < 4; ++d) qm[d] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int d = 0; d < 8; ++d) qf[h][d] = __bfloat162float(qp[h * kHeadDim + d]);
-    const int32_t *pt = page_table + static_cast<size_t>(seq) * max_pages;
-    uint32_t *out = keys + (static_cast<size_t>(seq) * Hkv + g) * max_pages;
-    const int end = min(npg, (static_cast<int>(blockIdx.x) + 1) * kScorePages);
-    for (int p = blockIdx.x * kScorePages + (threadIdx.x >> 3); p < end; p += 32) {
-        const int phys = pt[p];
-        float best = -INFINITY;
-        bool nan = false;
-        if (phys >= 0 && phys < num_pages) {  // uniform over the page's eight lanes
-            const uint4 *b = bounds + (static_cast<size_t>(phys) * Hkv + g) * 16;
-            const uint4 lo4 = __ldg(b + c), hi4 = __ldg(b + 8 + c);
-            const uint32_t lw[4] = {lo4.x, lo4.y, lo4.z, lo4.w};
-            const uint32_t hw[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
-            const uint32_t group = 0xffu << (threadIdx.x & 24);
+    for (int h = 0; h < GH; ++h) {
+        const uint4 x = __ldg(q + ((static_cast<size_t>(seq) * Hkv + g) * G + part * GH + h) * 8 + c);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int h = 0; h < G; ++h) {
-                double acc = 0.0;
+        for (int d = 0; d < 4; ++d) {
+            const float2 v = make_float2(__uint_as_float(w[d] << 16),
+                                         __uint_as_float(w[d] & 0xffff0000u));
+            qf[h][d] = v;
+            qm[d] = make_float2(fmaxf(qm[d].x, fabsf(v.x)), fmaxf(qm[d].y, fabsf(v.y)));
+        }
+    }
+    __syncthreads();
+    float2 *out = scores + (static_cast<size_t>(seq) * Hkv + g) * max_pages + first;
+    for (int p0 = threadIdx.x / kLanes; p0 - static_cast<int>(threadIdx.x) / kLanes < count;
+         p0 += kStep * kDeep) {
+        uint4 lo4[kDeep], hi4[kDeep];
+        bool ok[kDeep];
 #pragma unroll
-                for (int d = 0; d < 8; ++d) {
-                    const uint32_t lb = d & 1 ? lw[d >> 1] & 0xffff0000u : lw[d >> 1] << 16;
-                    const uint32_t hb = d & 1 ? hw[d >> 1] & 0xffff0000u : hw[d >> 1] << 16;
-                    acc += static_cast<double>(
-                        fmaxf(qf[h][d] * __uint_as_float(lb), qf[h][d] * __uint_as_float(hb)));
-                }
-#pragma unroll
-                for (int o = 1; o < 8; o <<= 1) acc += __shfl_xor_sync(group, acc, o);
-                const float s = static_cast<float>(acc);
-                nan |= s != s;
-                best = fmaxf(best, s);
+        for (int e = 0; e < kDeep; ++e) {
+            const int p = p0 + e * kStep, x = p < count ? phys[p] : -1;
+            ok[e] = x >= 0;
+            if (ok[e]) {
+                const uint4 *b = bounds + (static_cast<size_t>(x) * Hkv + g) * 16;
+                lo4[e] = __ldg(b + c);
+                hi4[e] = __ldg(b + 8 + c);
+            } else {
+                lo4[e] = hi4[e] = make_uint4(0, 0, 0, 0);
             }
         }
-        if (c == 0) out[p] = nan ? 0xfffffffeu : score_key(best);
+#pragma unroll
+        for (int e = 0; e < kDeep; ++e) {
+            if (p0 - static_cast<int>(threadIdx.x) / kLanes + e * kStep >= count) break;  // uniform
+            const uint32_t lw[4] = {lo4[e].x, lo4[e].y, lo4[e].z, lo4[e].w};
+            const uint32_t hw[4] = {hi4[e].x, hi4[e].y, hi4[e].z, hi4[e].w};
+            float2 acc[GH], mag = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int h = 0; h < GH; ++h) acc[h] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const float2 lo = make_float2(__uint_as_float(lw[d] << 16),
+                                              __uint_as_float(lw[d] & 0xffff0000u));
+                const float2 hi = make_float2(__uint_as_float(hw[d] << 16),
+                                              __uint_as_float(hw[d] & 0xffff0000u));
+                const float2 m = make_float2(fmaxf(fabsf(lo.x), fabsf(hi.x)),
+                                             fmaxf(fabsf(lo.y), fabsf(hi.y)));
+                mag = f2_fma(qm[d], m, mag);
+#pragma unroll
+                for (int h = 0; h < GH; ++h)
+                    acc[h] = f2_add(acc[h], make_float2(fmaxf(qf[h][d].x * lo.x, qf[h][d].x * hi.x),
+                                                        fmaxf(qf[h][d].y * lo.y, qf[h][d].y * hi.y)));
+            }
+            // Sum over the eight lanes; where a lane has several heads, each
+            // step halves them instead of repeating the sum.
+            float err = mag.x + mag.y, best;
+            float s[GH];
+#pragma unroll
+            for (int h = 0; h < GH; ++h) s[h] = acc[h].x + acc[h].y;
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1)  // over both halves of eight heads: an upper bound
+                err = o < 8 ? err + __shfl_xor_sync(~0u, err, o)
+                            : fmaxf(err, __shfl_xor_sync(~0u, err, o));
+            if constexpr (GH == 4) {
+                const bool up = c & 4, up2 = c & 2;
+                const float s0 = (up ? s[2] : s[0]) + __shfl_xor_sync(~0u, up ? s[0] : s[2], 4);
+                const float s1 = (up ? s[3] : s[1]) + __shfl_xor_sync(~0u, up ? s[1] : s[3], 4);
+                best = (up2 ? s1 : s0) + __shfl_xor_sync(~0u, up2 ? s0 : s1, 2);
+                best += __shfl_xor_sync(~0u, best, 1);
+                best = fmaxf(best, __shfl_xor_sync(~0u, best, 2));
+                best = fmaxf(best, __shfl_xor_sync(~0u, best, 4));
+            } else if constexpr (GH == 2) {
+                const bool up = c & 4;
+                best = (up ? s[1] : s[0]) + __shfl_xor_sync(~0u, up ? s[0] : s[1], 4);
+                best += __shfl_xor_sync(~0u, best, 2);
+                best += __shfl_xor_sync(~0u, best, 1);
+                best = fmaxf(best, __shfl_xor_sync(~0u, best, 4));
+            } else {
+                best = s[0] + __shfl_xor_sync(~0u, s[0], 4);
+                best += __shfl_xor_sync(~0u, best, 2);
+                best += __shfl_xor_sync(~0u, best, 1);
+            }
+            if constexpr (kLanes == 16) best = fmaxf(best, __shfl_xor_sync(~0u, best, 8));
+            // Bounds that are not finite make err so, too: 64 bits then decide.
+            // A page outside the pool ranks last; the split reports it if read.
+            if (threadIdx.x % kLanes == 0 && p0 + e * kStep < count)
+                out[p0 + e * kStep] = ok[e] ? make_float2(best, fmaf(err, 12.0f * 0x1p-24f, 0x1p-100f))
+                                            : make_float2(-INFINITY, 0.f);
+        }
     }
 }
 
 struct SelectArgs {
-    const uint32_t *keys;
-    const int32_t *seqlens;
+    const uint4 *q, *bounds;
+    const float2 *scores;
+    const int32_t *page_table, *seqlens;
     int32_t *selected;  // [num_seqs, Hkv, keep]: ascending pages, then -1
-    int max_pages, Hkv, keep;
+    uint32_t *keys;     // per (sequence, head) row of max_pages: past kSelKeys pages
+    int num_pages, max_pages, Hkv, keep;
     int *status;
 };
 
-// Block (kv head, sequence): the keep highest keys by a radix selection, then
-// the pages in ascending order.
+// Block (kv head, sequence): the pages with the highest scores, ascending.
+//
+// A radix selection over keys in the scores' order finds the k-th highest.
+// Scores lie close together, so its digits begin at the highest bit in which
+// two keys differ, and it ends as soon as a bin is taken whole.  Scores come in
+// fp32 with error bounds; with E the largest of them and T the k-th highest
+// score, the k-th highest exact score is within E of T, so a page above T + 2E
+// is taken and one below T - 2E is not, whatever the roundings.  Where the pages
+// between are not all taken, they get their exact scores, and the selection
+// runs once more on (taken, exact, not taken).
+template <int G>
 __global__ void __launch_bounds__(kSelThreads) sparse_select_kernel(const SelectArgs a) {
+    extern __shared__ uint32_t held[];
     __shared__ int hist[256];
-    __shared__ int scratch[2][kSelThreads / 32];
-    __shared__ uint32_t s_prefix;
-    __shared__ int s_left;
+    __shared__ uint32_t ends[4][kSelThreads / 32];
+    __shared__ int counts[2][kSelThreads / 32];
+    __shared__ int s_bin, s_left, s_whole;
     const int g = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x;
+    const int lane = tid & 31, w = tid >> 5;
+    constexpr int kWarps = kSelThreads / 32;
     const int len = a.seqlens[seq];
+    wait_for_previous_kernel();  // every block, so that a later kernel's wait covers the scores
     if (!valid_len(len, a.max_pages)) {
         if (g == 0 && tid == 0) record_error(a.status, POLAR_ERR_BAD_SEQLEN);
         return;
     }
     const int npg = (len + kPage - 1) / kPage;
-    int32_t *out = a.selected + (static_cast<size_t>(seq) * a.Hkv + g) * a.keep;
+    const size_t row = static_cast<size_t>(seq) * a.Hkv + g;
+    int32_t *out = a.selected + row * a.keep;
     if (npg <= a.keep) {
         for (int i = tid; i < a.keep; i += kSelThreads) out[i] = i < npg ? i : -1;
         return;
     }
-    const uint32_t *keys = a.keys + (static_cast<size_t>(seq) * a.Hkv + g) * a.max_pages;
-    auto key = [&](int p) { return p == npg - 1 ? 0xffffffffu : keys[p]; };
+    if (tid == 0) out[a.keep - 1] = npg - 1;  // the newest page, without a score
+    if (a.keep == 1) return;
+    const float2 *scores = a.scores + row * a.max_pages;
+    const int n = npg - 1, take = a.keep - 1;
+    uint32_t *keys = n <= kSelKeys ? held : a.keys + row * a.max_pages;
 
-    // The keep-th highest key, byte by byte.
-    uint32_t prefix = 0;
-    int left = a.keep;  // still to be taken among the keys with this prefix
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int p = tid; p < npg; p += kSelThreads) {
-            const uint32_t k = key(p);
-            if (shift == 24 || (k >> (shift + 8)) == prefix >> (shift + 8))
-                atomicAdd(&hist[k >> shift & 255u], 1);
-        }
-        __syncthreads();
-        if (tid == 0) {
-            int b = 255;
-            while (left > hist[b]) left -= hist[b--];
-            s_prefix = prefix | static_cast<uint32_t>(b) << shift;
-            s_left = left;
-        }
-        __syncthreads();
-        prefix = s_prefix;
-        left = s_left;
+    uint32_t err = 0;  // as bits: in the order of the values, and a NaN above all
+    for (int p = tid; p < n; p += kSelThreads) {
+        const float2 x = scores[p];
+        keys[p] = score_key(x.x);
+        err = max(err, __float_as_uint(x.y) & 0x7fffffffu);
     }
+    if (tid < 256) hist[tid] = 0;
 
-    // Keys above it, and the first `left` equal to it, in ascending order.
-    int above = 0, equal = 0;  // in the pages before this step
-    const int lane = tid & 31, w = tid >> 5;
-    for (int p0 = 0; p0 < npg; p0 += kSelThreads) {
-        const int p = p0 + tid;
-        const uint32_t k = p < npg ? key(p) : 0u;
-        const bool gt = p < npg && k > prefix, eq = p < npg && k == prefix;
-        const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
+    // Keys above floor_key are taken, and the first `left` of those equal to it;
+    // `open`: low bits that do not count.
+    uint32_t floor_key = 0, open = 0;
+    int left = 0;
+    auto radix = [&]() {
+        uint32_t all_and = ~0u, all_or = 0u;
+        for (int p = tid; p < n; p += kSelThreads) {
+            all_and &= keys[p];
+            all_or |= keys[p];
+        }
+        all_and = __reduce_and_sync(~0u, all_and);
+        all_or = __reduce_or_sync(~0u, all_or);
         if (lane == 0) {
-            scratch[0][w] = __popc(mg);
-            scratch[1][w] = __popc(me);
+            ends[0][w] = all_and;
+            ends[1][w] = all_or;
         }
         __syncthreads();
-        const uint32_t below = (1u << lane) - 1;
-        int ng = above + __popc(mg & below), ne = equal + __popc(me & below);
-        for (int i = 0; i < kSelThreads / 32; ++i) {
-            if (i < w) {
-                ng += scratch[0][i];
-                ne += scratch[1][i];
+        for (int i = 0; i < kWarps; ++i) {
+            all_and &= ends[0][i];
+            all_or |= ends[1][i];
+        }
+        int bits = 32 - __clz(static_cast<int>(all_and ^ all_or));
+        floor_key = bits == 32 ? 0u : all_and >> bits << bits;
+        left = take;
+        while (bits > 0) {
+            const int shift = max(bits - 8, 0);
+            const uint32_t digit = (1u << (bits - shift)) - 1;
+            for (int p = tid; p < n; p += kSelThreads) {
+                const uint32_t k = keys[p];
+                if (bits == 32 || (k ^ floor_key) >> bits == 0)
+                    atomicAdd(&hist[k >> shift & digit], 1);
             }
-            above += scratch[0][i];
-            equal += scratch[1][i];
+            __syncthreads();
+            if (w == 0) {  // the left-th key's bin from above: lane l has bins 255-8l .. 248-8l
+                int h[8], sum = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum += h[e] = hist[255 - 8 * lane - e];
+                int upto = sum;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(~0u, upto, o);
+                    if (lane >= o) upto += y;
+                }
+                int before = upto - sum;
+                if (before < left && left <= upto) {
+                    bool found = false;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (!found && left <= before + h[e]) {
+                            s_bin = 255 - 8 * lane - e;
+                            s_left = left - before;
+                            s_whole = left - before == h[e];
+                            found = true;
+                        }
+                        before += h[e];
+                    }
+                }
+            }
+            __syncthreads();
+            if (tid < 256) hist[tid] = 0;
+            floor_key |= static_cast<uint32_t>(s_bin) << shift;
+            left = s_left;
+            const bool whole = s_whole != 0;
+            bits = shift;
+            __syncthreads();
+            if (whole) break;
         }
-        if (gt || (eq && ne < left)) out[ng + min(ne, left)] = p;
-        __syncthreads();
+        open = bits > 0 ? (1u << bits) - 1 : 0u;
+    };
+    __syncthreads();
+    radix();
+
+    // The pages whose place the roundings could change.
+    err = __reduce_max_sync(~0u, err);
+    if (lane == 0) ends[2][w] = err;
+    // T: the lowest key that is taken (with a bin taken whole, the lowest in it).
+    uint32_t lowest = ~0u;
+    for (int p = tid; p < n; p += kSelThreads) {
+        const uint32_t k = keys[p];
+        if ((k & ~open) >= floor_key) lowest = min(lowest, k);
     }
+    lowest = __reduce_min_sync(~0u, lowest);
+    if (lane == 0) ends[3][w] = lowest;
+    __syncthreads();
+    for (int i = 0; i < kWarps; ++i) {
+        lowest = min(lowest, ends[3][i]);
+        err = max(err, ends[2][i]);
+    }
+    const float E = __uint_as_float(err);
+    const float T = key_score(lowest);
+    // Rounded outwards by more than the sums' own roundings and the exact
+    // scores' rounding to fp32.
+    const float reach = 2.0f * E + (fabsf(T) + E) * 0x1p-22f;
+    const float above = T + reach, below = T - reach;
+    // Where nothing can change, ties included, the fp32 keys' choice stands.
+    auto place = [&](uint32_t k) {  // 2: taken, 0: not taken, 1: to be seen
+        const float x = key_score(k);
+        return x > above ? 2 : x < below ? 0 : 1;
+    };
+    int mid = 0, sure = 0;
+    for (int p = tid; p < n; p += kSelThreads) {
+        const int c = place(keys[p]);
+        mid += c == 1;
+        sure += c == 2;
+    }
+    mid = __reduce_add_sync(~0u, mid);
+    sure = __reduce_add_sync(~0u, sure);
+    if (lane == 0) {
+        counts[0][w] = mid;
+        counts[1][w] = sure;
+    }
+    __syncthreads();
+    mid = sure = 0;
+    for (int i = 0; i < kWarps; ++i) {
+        mid += counts[0][i];
+        sure += counts[1][i];
+    }
+    if (sure + mid != take) {
+        const int32_t *pt = a.page_table + static_cast<size_t>(seq) * a.max_pages;
+        const uint4 *q = a.q + row * G * 8;
+        for (int first = 32 * w; first < n; first += kSelThreads) {
+            const int p = first + lane, c = p < n ? place(keys[p]) : 0;
+            const int phys = c == 1 ? pt[p] : -1;
+            uint32_t k = c == 2 ? 0xffffffffu : 0u;
+            for (uint32_t todo = __ballot_sync(~0u, phys >= 0 && phys < a.num_pages); todo;
+                 todo &= todo - 1) {
+                const int who = __ffs(todo) - 1;
+                const size_t page = __shfl_sync(~0u, phys, who);
+                const uint32_t e = exact_key<G>(q, a.bounds + (page * a.Hkv + g) * 16, lane);
+                if (lane == who) k = e;
+            }
+            if (p < n) keys[p] = k;
+        }
+        __syncthreads();
+        radix();
+    } else {  // all of `mid` are taken
+        floor_key = lowest;
+        open = 0;
+        left = n;
+    }
+
+    // Ascending order: thread t has pages t * per .. t * per + per - 1.
+    const int per = (n + kSelThreads - 1) / kSelThreads;
+    const int p0 = min(tid * per, n), p1 = min(p0 + per, n);
+    int gt = 0, eq = 0;
+    for (int p = p0; p < p1; ++p) {
+        const uint32_t k = keys[p] & ~open;
+        gt += k > floor_key;
+        eq += k == floor_key;
+    }
+    int gs = gt, es = eq;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, gs, o), z = __shfl_up_sync(~0u, es, o);
+        if (lane >= o) {
+            gs += y;
+            es += z;
+        }
+    }
+    __syncthreads();  // the counts above are read
+    if (lane == 31) {
+        counts[0][w] = gs;
+        counts[1][w] = es;
+    }
+    __syncthreads();
+    gs -= gt;
+    es -= eq;
+    for (int i = 0; i < w; ++i) {
+        gs += counts[0][i];
+        es += counts[1][i];
+    }
+    if (gt + eq > 0)
+        for (int p = p0; p < p1; ++p) {
+            const uint32_t k = keys[p] & ~open;
+            if (k > floor_key) {
+                out[gs + min(es, left)] = p;
+                ++gs;
+            } else if (k == floor_key) {
+                if (es < left) out[gs + es] = p;
+                ++es;
+            }
+        }
 }
 
 struct SparseArgs {
     const int32_t *page_table, *seqlens, *selected;
     const __nv_bfloat16 *q;
-    float *partials;
+    const float *u;
+    __nv_bfloat16 *out;
+    float *neff, *partials;
     int *status;
-    int num_pages, max_pages, Hq, Hkv, keep, pages_per_split, max_splits;
-    float s, alpha, L;
+    int num_pages, max_pages, Hq, Hkv, keep, splits;
+    Epilogue ep;
 };
 
 // Positions of the selected pages: all are full but the newest.
@@ -189,130 +456,131 @@ __device__ __forceinline__ int selected_tokens(int len, int keep) {
     return (min(npg, keep) - 1) * kPage + len - (npg - 1) * kPage;
 }
 
-// CTA (split of the selected pages, kv head, sequence).
+// CTA (part of the selected pages, kv head, sequence): the parts are equal
+// shares of what is selected.  A cluster along x merges its CTAs' states; with
+// one cluster per (kv head, sequence) it writes the rows, else a partial.
 template <int G>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kRowThreads)
 sparse_split_kernel(const __grid_constant__ CUtensorMap kv_map, const SparseArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) uint64_t full_bar[kStages];
-    __shared__ float mst[4][8][6];
-    float(*macc)[8][kHeadDim] = reinterpret_cast<float(*)[8][kHeadDim]>(smem);
-    const int split = blockIdx.x, g = blockIdx.y, seq = blockIdx.z;
+    __shared__ __align__(8) PageRing ring;
+    const int g = blockIdx.y, seq = blockIdx.z;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, tq = lane & 3;
 
     const int len = a.seqlens[seq];
-    if (!valid_len(len, a.max_pages)) return;
-    const int npg = (len + kPage - 1) / kPage;
-    const int p0 = split * a.pages_per_split, nsel = min(npg, a.keep);
-    if (p0 >= nsel) return;
-    const int np = min(nsel, p0 + a.pages_per_split) - p0;
-    const int32_t *pt = a.page_table + static_cast<size_t>(seq) * a.max_pages;
-    const int32_t *sel = a.selected + (static_cast<size_t>(seq) * a.Hkv + g) * a.keep + p0;
-
-    if (threadIdx.x == 0) {
-        tma_prefetch_desc(&kv_map);
-        for (int st = 0; st < kStages; ++st) mbar_init(&full_bar[st], 1);
-        fence_barrier_init();
+    if (!valid_len(len, a.max_pages)) {  // the whole cluster; reported by the selection
+        wait_for_previous_kernel();
+        return;
     }
-    __syncthreads();
-    auto issue = [&](int kk) {
-        const int st = kk % kStages, phys = pt[sel[kk]];
-        if (phys >= 0 && phys < a.num_pages) {
-            mbar_arrive_expect_tx(&full_bar[st], kStageBytes);
-            const int row = (phys * 2 * a.Hkv + g) * kPage;  // K block of the kv head
-            tma_load_2d(smem + st * kStageBytes, &kv_map, 0, row, &full_bar[st]);
-            tma_load_2d(smem + st * kStageBytes + kChunkBytes, &kv_map, 0, row + a.Hkv * kPage,
-                        &full_bar[st]);
-        } else {
-            record_error(a.status, POLAR_ERR_BAD_PAGE);
-            mbar_arrive(&full_bar[st]);
-        }
-    };
-    if (threadIdx.x == 0)
-        for (int kk = 0; kk < min(kStages, np); ++kk) issue(kk);
+    const int npg = (len + kPage - 1) / kPage;
+    const int nsel = min(npg, a.keep), per = (nsel + gridDim.x - 1) / gridDim.x;
+    const int p0 = min(static_cast<int>(blockIdx.x) * per, nsel);
+    const int np = min(nsel, p0 + per) - p0;
 
     RowTile<1> tile[1];
     tile[0].clear();
-    tile[0].load_row(0,
-                     gq < G ? a.q + (static_cast<size_t>(seq) * a.Hq + g * G + gq) * kHeadDim
-                            : nullptr,
-                     tq,
-                     a.s * length_temperature(static_cast<float>(selected_tokens(len, a.keep)),
-                                              a.alpha, a.L) * kLog2e);
-    int issued = min(kStages, np), consumed = 0;
-    bool ok = true;
+    if (w < kRowWarps)
+        tile[0].load_row(0,
+                         gq < G ? a.q + (static_cast<size_t>(seq) * a.Hq + g * G + gq) * kHeadDim
+                                : nullptr,
+                         tq,
+                         a.ep.s * length_temperature(
+                             static_cast<float>(selected_tokens(len, a.keep)), a.ep.alpha,
+                             a.ep.L) * kLog2e);
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&kv_map);
+        init_ring(ring);
+    }
+    wait_for_previous_kernel();
+    {
+        const int32_t *pt = a.page_table + static_cast<size_t>(seq) * a.max_pages;
+        const int32_t *sel = a.selected + (static_cast<size_t>(seq) * a.Hkv + g) * a.keep + p0;
+        for (int i = threadIdx.x; i < np; i += kRowThreads) {
+            const int x = pt[sel[i]];
+            ring.page[i] = x >= 0 && x < a.num_pages ? x : -1;
+            if (ring.page[i] < 0) record_error(a.status, POLAR_ERR_BAD_PAGE);
+        }
+    }
+    __syncthreads();
     const uint32_t sbase = smem_u32(smem);
-    for (int kk = 0; kk < np; ++kk) {
-        const int st = kk % kStages;
-        const bool ready = mbar_wait(&full_bar[st], (kk / kStages) & 1, a.status);
-        if (!__syncthreads_and(ready)) { ok = false; break; }
-        consumed = kk + 1;
-        const int page = sel[kk], phys = pt[page];
-        if (phys >= 0 && phys < a.num_pages)
-            page_step<1, 1>(tile, sbase + st * kStageBytes, sbase + st * kStageBytes + kChunkBytes,
-                            w, lane, first_tokens(len - page * kPage));
-        __syncthreads();  // every warp is done with stage st
-        if (threadIdx.x == 0 && issued < np) issue(issued++);
+    if (w == kRowWarps) {
+        if (lane == 0)
+            copy_steps(ring, np, a.status, [&](int kk, int st, uint64_t *bar) {
+                const int phys = ring.page[kk];
+                if (phys < 0) {
+                    mbar_arrive(bar);
+                    return;
+                }
+                mbar_arrive_expect_tx(bar, kStageBytes);
+                const int row = (phys * 2 * a.Hkv + g) * kPage;  // K block of the kv head
+                tma_load_2d(smem + st * kStageBytes, &kv_map, 0, row, bar);
+                tma_load_2d(smem + st * kStageBytes + kChunkBytes, &kv_map, 0,
+                            row + a.Hkv * kPage, bar);
+            });
+        __syncwarp();
+    } else {
+        // The newest page is the last that is selected; all others are full.
+        const uint64_t newest = first_tokens(len - (npg - 1) * kPage);
+        compute_steps(ring, np, lane, a.status, [&](int kk, int st) {
+            const uint32_t kb = sbase + st * kStageBytes;
+            if (ring.page[kk] >= 0)
+                page_step<1, 1>(tile, kb, kb + kChunkBytes, w, lane,
+                                p0 + kk == nsel - 1 ? newest : ~0ull);
+        });
     }
-    if (!ok) {
-        // Bounded drain of copies still in flight before shared memory is released.
-        if (threadIdx.x == 0)
-            for (int kk = consumed; kk < issued; ++kk)
-                mbar_wait(&full_bar[kk % kStages], (kk / kStages) & 1, a.status);
-        __syncthreads();
-        return;
-    }
-    merge_warps<1, 1>(tile, mst, macc, w, lane, [&](int r) -> float * {
-        if (r >= G) return nullptr;
-        return a.partials + ((static_cast<size_t>(seq) * a.Hq + g * G + r) * a.max_splits + split) *
-                                kPartialFloats;
+    let_next_kernel_start();
+    reduce_rows<1, 1>(tile, reinterpret_cast<float *>(smem), G, w, lane,
+                      [&](int r, bool real, const RowState &x) {
+        const size_t row = static_cast<size_t>(seq) * a.Hq + g * G + r;
+        if (a.splits > 1)
+            store_part(x, a.partials + (row * a.splits + blockIdx.x / cluster_size()) *
+                                           kPartialFloats, real);
+        else
+            finish_row(x, selected_tokens(len, a.keep), a.ep, a.u + (g * G + r) * kHeadDim,
+                       a.out + row * kHeadDim, a.neff ? a.neff + row : nullptr, real);
     });
 }
 
-// One warp per (sequence, query head).
-__global__ void __launch_bounds__(128)
-sparse_merge_kernel(const float *__restrict__ partials, const int32_t *__restrict__ seqlens,
-                    const float *__restrict__ u, __nv_bfloat16 *__restrict__ out,
-                    float *__restrict__ neff_out, long long rows, int Hq, int max_pages, int keep,
-                    int pages_per_split, int max_splits, float s, float alpha, float L, float beta,
-                    float inv_ln_L) {
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (row >= rows) return;
-    const int len = seqlens[row / Hq];
-    if (!valid_len(len, max_pages)) return;
-    const int nsel = min((len + kPage - 1) / kPage, keep);
-    merge_splits(partials + row * max_splits * kPartialFloats,
-                 (nsel + pages_per_split - 1) / pages_per_split, selected_tokens(len, keep), s,
-                 alpha, L, beta, inv_ln_L, u + (row % Hq) * kHeadDim, threadIdx.x & 31,
-                 out + row * kHeadDim, neff_out ? neff_out + row : nullptr);
+// Eight lanes per (sequence, query head).
+__global__ void __launch_bounds__(128) sparse_merge_kernel(const SparseArgs a, int rows) {
+    int row = blockIdx.x * 16 + (threadIdx.x >> 3);
+    bool real = row < rows;
+    row = min(row, rows - 1);
+    const int len = a.seqlens[row / a.Hq];
+    real = real && valid_len(len, a.max_pages);
+    wait_for_previous_kernel();
+    const float *base = a.partials + static_cast<size_t>(row) * a.splits * kPartialFloats;
+    finish_row(merge_parts(a.splits, [&](int k) { return base + k * kPartialFloats; }),
+               selected_tokens(len, a.keep), a.ep, a.u + (row % a.Hq) * kHeadDim,
+               a.out + static_cast<size_t>(row) * kHeadDim, a.neff ? a.neff + row : nullptr, real);
 }
 
-int pages_per_split(int num_seqs, int pages, int Hkv) {
-    const long long work = static_cast<long long>(num_seqs) * Hkv * pages;
-    int n = 64;
-    while (n > 2 && work / n < 148ll * 3 * 4) n >>= 1;
-    return n;
-}
-
-struct Layout {  // the workspace: keys, selected pages, partials
-    size_t selected, partials, total;
-    int pps, splits;
+struct Layout {  // the workspace: scores, keys (long rows), selected pages, partials
+    size_t keys, selected, partials, total;
+    int cluster, splits;  // CTAs of a cluster, clusters of a (sequence, kv head)
 };
 
 Layout layout(int num_seqs, int max_pages, int keep, int Hq, int Hkv) {
     Layout l;
     const int pages = std::min(keep, max_pages);
-    l.pps = pages_per_split(num_seqs, pages, Hkv);
-    l.splits = (pages + l.pps - 1) / l.pps;
+    const long long heads = static_cast<long long>(num_seqs) * Hkv;
+    // Enough CTAs for four on each of 148 SMs, of at least two pages each.
+    l.cluster = 1;
+    while (l.cluster < kMaxCluster && heads * l.cluster < 148 * 4 && l.cluster * 4 <= pages)
+        l.cluster *= 2;
+    l.splits = 1;
+    while ((heads * l.cluster * l.splits * 2 <= 148 * 4 && l.cluster * l.splits * 16 <= pages) ||
+           l.cluster * l.splits * kMaxSteps < pages)
+        l.splits *= 2;
     auto pad = [](size_t x) { return (x + 15) / 16 * 16; };
-    const size_t heads = static_cast<size_t>(num_seqs) * Hkv;
-    l.selected = pad(heads * max_pages * 4);
+    l.keys = pad(heads * max_pages * 8);
+    l.selected = l.keys + (max_pages > kSelKeys ? pad(heads * max_pages * 4) : 0);
     l.partials = l.selected + pad(heads * keep * 4);
-    l.total = l.partials +
-              static_cast<size_t>(num_seqs) * Hq * l.splits * kPartialFloats * sizeof(float);
+    l.total = l.partials + (l.splits > 1 ? static_cast<size_t>(num_seqs) * Hq * l.splits *
+                                               kPartialFloats * sizeof(float) : 0);
     return l;
 }
 
@@ -330,38 +598,54 @@ cudaError_t launch_all(const SparseLaunch &a, const CUtensorMap &map, const Layo
         configured.fetch_or(bit);
     }
     char *ws = static_cast<char *>(a.workspace);
-    uint32_t *keys = reinterpret_cast<uint32_t *>(ws);
+    float2 *scores = reinterpret_cast<float2 *>(ws);
     int32_t *sel = a.selected ? a.selected : reinterpret_cast<int32_t *>(ws + l.selected);
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q);
-    if (a.max_pages > a.keep) {
-        sparse_score_kernel<G><<<dim3((a.max_pages + kScorePages - 1) / kScorePages, a.Hkv,
-                                      a.num_seqs), 256, 0, a.stream>>>(
-            q, static_cast<const uint4 *>(a.bounds), a.page_table, a.seqlens, keys, a.num_pages,
-            a.max_pages, a.Hq, a.Hkv, a.keep, a.status);
+    const uint4 *q = static_cast<const uint4 *>(a.q), *bounds = static_cast<const uint4 *>(a.bounds);
+    const bool scored = a.max_pages > a.keep;
+    if (scored) {
+        // Three blocks fit an SM; about twelve, since lengths differ.  A step is
+        // 32 pages (16 for groups of eight heads).
+        const int step = kScoreThreads / (G == 8 ? 16 : 8);
+        const long long all = static_cast<long long>(a.num_seqs) * a.Hkv *
+                              ((a.max_pages + step - 1) / step);
+        const int per = step * static_cast<int>(
+            std::clamp<long long>(all / (148 * 12), 1, kScorePages / step));
+        sparse_score_kernel<G><<<dim3((a.max_pages + per - 1) / per, a.Hkv, a.num_seqs),
+                                 kScoreThreads, 0, a.stream>>>(
+            q, bounds, a.page_table, a.seqlens, scores, a.num_pages, a.max_pages, a.Hkv, a.keep,
+            per);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         count_launches(1);
     }
-    SelectArgs s{keys, a.seqlens, sel, a.max_pages, a.Hkv, a.keep, a.status};
-    sparse_select_kernel<<<dim3(a.Hkv, a.num_seqs), kSelThreads, 0, a.stream>>>(s);
-    e = cudaGetLastError();
+    SelectArgs s{q, bounds, scores, a.page_table, a.seqlens, sel,
+                 reinterpret_cast<uint32_t *>(ws + l.keys), a.num_pages, a.max_pages, a.Hkv,
+                 a.keep, a.status};
+    const size_t held = std::min(a.max_pages, kSelKeys) * sizeof(uint32_t);
+    e = launch_ex(sparse_select_kernel<G>, dim3(a.Hkv, a.num_seqs), kSelThreads, held, 1, scored,
+                  a.stream, s);
     if (e != cudaSuccess) return e;
     SparseArgs p;
-    p.page_table = a.page_table; p.seqlens = a.seqlens; p.selected = sel; p.q = q;
+    p.page_table = a.page_table; p.seqlens = a.seqlens; p.selected = sel;
+    p.q = static_cast<const __nv_bfloat16 *>(a.q); p.u = a.u;
+    p.out = static_cast<__nv_bfloat16 *>(a.out); p.neff = a.neff;
     p.partials = reinterpret_cast<float *>(ws + l.partials);
     p.status = a.status; p.num_pages = a.num_pages; p.max_pages = a.max_pages;
-    p.Hq = a.Hq; p.Hkv = a.Hkv; p.keep = a.keep;
-    p.pages_per_split = l.pps; p.max_splits = l.splits;
-    p.s = a.s; p.alpha = a.alpha; p.L = static_cast<float>(a.L);
-    sparse_split_kernel<G><<<dim3(l.splits, a.Hkv, a.num_seqs), 128, kSmem, a.stream>>>(map, p);
-    e = cudaGetLastError();
+    p.Hq = a.Hq; p.Hkv = a.Hkv; p.keep = a.keep; p.splits = l.splits;
+    const float L = static_cast<float>(a.L);
+    p.ep = Epilogue{a.s, a.alpha, L, a.beta, 1.0f / logf(L)};
+    e = launch_ex(sparse_split_kernel<G>, dim3(l.cluster * l.splits, a.Hkv, a.num_seqs), kRowThreads,
+                  kSmem, l.cluster, true, a.stream, map, p);
     if (e != cudaSuccess) return e;
-    const long long rows = static_cast<long long>(a.num_seqs) * a.Hq;
-    sparse_merge_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, a.stream>>>(
-        p.partials, a.seqlens, a.u, static_cast<__nv_bfloat16 *>(a.out), a.neff, rows, a.Hq,
-        a.max_pages, a.keep, l.pps, l.splits, a.s, a.alpha, p.L, a.beta, 1.0f / logf(p.L));
-    count_launches(3);
-    return cudaGetLastError();
+    count_launches(2);
+    if (l.splits > 1) {
+        const int rows = a.num_seqs * a.Hq;
+        e = launch_ex(sparse_merge_kernel, dim3((rows + 15) / 16), 128, 0, 1, true, a.stream, p,
+                      rows);
+        if (e != cudaSuccess) return e;
+        count_launches(1);
+    }
+    return cudaSuccess;
 }
 
 }  // namespace

@@ -11,42 +11,21 @@
 #include <algorithm>
 #include <atomic>
 
-#include "decode_rows.cuh"
+#include "decode_tree.cuh"
 #include "polar_internal.h"
 #include "tc_common.cuh"
 
 namespace polar {
 namespace {
 
-constexpr int kStages = 3;
-constexpr int kSmem = kStages * kStageBytes + 1024;  // + alignment slack
+constexpr int kSmem = kRingStages * kStageBytes + 1024;  // + alignment slack
+constexpr int kMaxCluster = 8;
 
-struct TreeArgs {
-    const int32_t *page_table, *seqlens, *tree_lens;
-    const uint64_t *mask;
-    const __nv_bfloat16 *q;
-    float *partials;
-    int *status;
-    int num_pages, max_pages, Hq, Hkv, tree, steps_per_split, max_splits, row_tiles;
-    float s, alpha, L;
-};
-
-// Number of drafted nodes of a sequence, or -1 if its lengths are out of range.
-__device__ __forceinline__ int tree_nodes(const int32_t *seqlens, const int32_t *tree_lens, int seq,
-                                          int tree, int max_pages) {
-    const int len = seqlens[seq], n = tree_lens ? tree_lens[seq] : tree;
-    const bool ok = len >= 0 && len <= static_cast<long long>(max_pages) * kPage && n >= 0 &&
-                    n <= tree;
-    return ok ? n : -1;
-}
-
-__device__ __forceinline__ bool not_finite(uint32_t half_bits) {
-    return (half_bits & 0x7f80u) == 0x7f80u;
-}
-
-// CTA (row tile within split, kv head, sequence).
+// CTA (part and row tile, kv head, sequence); the parts are equal shares of the
+// sequence's steps.  A cluster along x merges its CTAs' states; with one
+// cluster per row tile it writes the rows, else partials.
 template <int G, int MT, int kHR>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kRowThreads)
 tree_split_kernel(const __grid_constant__ CUtensorMap kv_map,
                   const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map, const TreeArgs a) {
@@ -54,13 +33,14 @@ tree_split_kernel(const __grid_constant__ CUtensorMap kv_map,
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     constexpr int kRows = 8 * kHR * MT;
-    __shared__ __align__(8) uint64_t full_bar[kStages];
-    __shared__ float mst[4][kRows][6];
-    // The warps' value sums, in the page ring once every page is consumed.
-    static_assert(4 * kRows * kHeadDim * sizeof(float) <= kStages * kStageBytes, "ring too small");
-    float(*macc)[kRows][kHeadDim] = reinterpret_cast<float(*)[kRows][kHeadDim]>(smem);
+    __shared__ __align__(8) PageRing ring;
+    // The rows' states go to the page ring once every page is consumed.
+    static_assert(5 * kRows * kPartialFloats * sizeof(float) <= kRingStages * kStageBytes,
+                  "ring too small");
 
-    const int split = blockIdx.x / a.row_tiles, rt = blockIdx.x % a.row_tiles;
+    const int C = static_cast<int>(cluster_size()), group = blockIdx.x / C;
+    const int rt = group % a.row_tiles, split = group / a.row_tiles;
+    const int part = split * C + static_cast<int>(cluster_rank());
     const int g = blockIdx.y, seq = blockIdx.z;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, tq = lane & 3;
@@ -75,46 +55,49 @@ tree_split_kernel(const __grid_constant__ CUtensorMap kv_map,
     if (row0 >= R) return;
     const int len = a.seqlens[seq];
     const int npg = (len + kPage - 1) / kPage;
-    const int p0 = split * a.steps_per_split;
-    if (p0 > npg) return;  // step npg is the drafted rows
-    const int np = min(npg + 1, p0 + a.steps_per_split) - p0;
+    const int per = (npg + a.splits * C) / (a.splits * C);  // of npg + 1 steps: the drafted rows last
+    const int p0 = min(part * per, npg + 1);
+    const int np = min(npg + 1, p0 + per) - p0;
     const int32_t *pt = a.page_table + static_cast<size_t>(seq) * a.max_pages + p0;
 
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&kv_map);
-        for (int st = 0; st < kStages; ++st) mbar_init(&full_bar[st], 1);
-        fence_barrier_init();
+        init_ring(ring);
+    }
+    // A page id outside the pool is reported and its step skipped.
+    for (int i = threadIdx.x; i < np; i += kRowThreads) {
+        const int x = p0 + i == npg ? 0 : pt[i];
+        ring.page[i] = x >= 0 && x < a.num_pages ? x : -1;
+        if (ring.page[i] < 0) record_error(a.status, POLAR_ERR_BAD_PAGE);
     }
     __syncthreads();
 
-    // Producer: thread 0 fills a stage with the K and V blocks of one step.  A
-    // page id outside the pool is reported and replaced by a plain arrive.
-    auto usable = [&](int kk) {
-        return p0 + kk == npg || (pt[kk] >= 0 && pt[kk] < a.num_pages);
-    };
-    auto issue = [&](int kk) {
-        const int st = kk % kStages;
-        uint8_t *dst = smem + st * kStageBytes;
-        if (p0 + kk == npg) {
-            mbar_arrive_expect_tx(&full_bar[st], kStageBytes);
-            tma_load_3d(dst, &k_map, 0, g, seq * a.tree, &full_bar[st]);
-            tma_load_3d(dst + kChunkBytes, &v_map, 0, g, seq * a.tree, &full_bar[st]);
-        } else if (usable(kk)) {
-            mbar_arrive_expect_tx(&full_bar[st], kStageBytes);
-            const int row = (pt[kk] * 2 * a.Hkv + g) * kPage;  // K block of the kv head
-            tma_load_2d(dst, &kv_map, 0, row, &full_bar[st]);
-            tma_load_2d(dst + kChunkBytes, &kv_map, 0, row + a.Hkv * kPage, &full_bar[st]);
-        } else {
-            record_error(a.status, POLAR_ERR_BAD_PAGE);
-            mbar_arrive(&full_bar[st]);
-        }
-    };
-    if (threadIdx.x == 0)
-        for (int kk = 0; kk < min(kStages, np); ++kk) issue(kk);
-
+    const uint32_t sbase = smem_u32(smem);
     const uint64_t drafted = first_tokens(nodes);
     const uint64_t *masks = a.mask + static_cast<size_t>(seq) * a.tree;
     RowTile<kHR> tile[MT];
+    if (w == kRowWarps) {
+        if (lane == 0)
+            copy_steps(ring, np, a.status, [&](int kk, int st, uint64_t *bar) {
+                uint8_t *dst = smem + st * kStageBytes;
+                const int phys = ring.page[kk];
+                if (phys < 0) {
+                    mbar_arrive(bar);
+                    return;
+                }
+                mbar_arrive_expect_tx(bar, kStageBytes);
+                if (p0 + kk == npg) {
+                    tma_load_3d(dst, &k_map, 0, g, seq * a.tree, bar);
+                    tma_load_3d(dst + kChunkBytes, &v_map, 0, g, seq * a.tree, bar);
+                } else {
+                    const int row = (phys * 2 * a.Hkv + g) * kPage;  // K block of the kv head
+                    tma_load_2d(dst, &kv_map, 0, row, bar);
+                    tma_load_2d(dst + kChunkBytes, &kv_map, 0, row + a.Hkv * kPage, bar);
+                }
+            });
+        __syncwarp();
+    }
+    const bool computes = w < kRowWarps;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         tile[m].clear();
@@ -122,28 +105,22 @@ tree_split_kernel(const __grid_constant__ CUtensorMap kv_map,
         for (int hr = 0; hr < kHR; ++hr) {
             const int r = row0 + m * 8 * kHR + 8 * hr + gq;
             const int t = r / G, hh = r % G;
-            const bool real = r < R;
+            const bool real = computes && r < R;
             const int n = real ? len + __popcll(masks[t] & drafted) : 0;
             tile[m].load_row(hr,
                              real ? a.q + ((static_cast<size_t>(seq) * a.tree + t) * a.Hq + g * G +
                                            hh) * kHeadDim
                                   : nullptr,
                              tq,
-                             a.s * length_temperature(static_cast<float>(n), a.alpha, a.L) * kLog2e);
+                             a.ep.s * length_temperature(static_cast<float>(n), a.ep.alpha, a.ep.L) *
+                                 kLog2e);
         }
     }
 
-    int issued = min(kStages, np), consumed = 0;
-    bool ok = true;
-    const uint32_t sbase = smem_u32(smem);
-    for (int kk = 0; kk < np; ++kk) {
-        const int st = kk % kStages;
-        const bool ready = mbar_wait(&full_bar[st], (kk / kStages) & 1, a.status);
-        if (!__syncthreads_and(ready)) { ok = false; break; }
-        consumed = kk + 1;
+    if (computes) compute_steps(ring, np, lane, a.status, [&](int kk, int st) {
         const uint32_t kb = sbase + st * kStageBytes, vb = kb + kChunkBytes;
         if (p0 + kk < npg) {
-            if (usable(kk))
+            if (ring.page[kk] >= 0)
                 page_step<MT, kHR>(tile, kb, vb, w, lane, first_tokens(len - (p0 + kk) * kPage));
         } else {
             // The drafted rows: a mask for each row.  A value row that is not
@@ -200,53 +177,42 @@ tree_split_kernel(const __grid_constant__ CUtensorMap kv_map,
                         }
             }
         }
-        __syncthreads();  // every warp is done with stage st
-        if (threadIdx.x == 0 && issued < np) issue(issued++);
-    }
-    if (!ok) {
-        // Bounded drain of copies still in flight before shared memory is released.
-        if (threadIdx.x == 0)
-            for (int kk = consumed; kk < issued; ++kk)
-                mbar_wait(&full_bar[kk % kStages], (kk / kStages) & 1, a.status);
-        __syncthreads();
-        return;
-    }
-    merge_warps<MT, kHR>(tile, mst, macc, w, lane, [&](int r) -> float * {
-        r += row0;
-        if (r >= R) return nullptr;
-        return a.partials + (((static_cast<size_t>(seq) * a.tree + r / G) * a.Hq + g * G + r % G) *
-                                 a.max_splits + split) * kPartialFloats;
+    });
+    let_next_kernel_start();
+    reduce_rows<MT, kHR>(tile, reinterpret_cast<float *>(smem), min(kRows, R - row0), w, lane,
+                         [&](int r, bool real, const RowState &x) {
+        const int t = (row0 + r) / G, h = g * G + (row0 + r) % G;
+        const size_t row = (static_cast<size_t>(seq) * a.tree + t) * a.Hq + h;
+        if (a.splits > 1)
+            store_part(x, a.partials + (row * a.splits + split) * kPartialFloats, real);
+        else
+            finish_row(x, len + __popcll(masks[t] & drafted), a.ep, a.u + h * kHeadDim,
+                       a.out + row * kHeadDim, a.neff ? a.neff + row : nullptr, real);
     });
 }
 
-// One warp per (sequence, node, query head).
-__global__ void __launch_bounds__(128)
-tree_merge_kernel(const float *__restrict__ partials, const int32_t *__restrict__ seqlens,
-                  const int32_t *__restrict__ tree_lens, const uint64_t *__restrict__ mask,
-                  const float *__restrict__ u, __nv_bfloat16 *__restrict__ out,
-                  float *__restrict__ neff_out, long long rows, int Hq, int tree, int max_pages,
-                  int steps_per_split, int max_splits, float s, float alpha, float L, float beta,
-                  float inv_ln_L) {
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (row >= rows) return;
-    const int lane = threadIdx.x & 31;
-    const int h = static_cast<int>(row % Hq);
-    const long long node = row / Hq;  // seq * tree + t
-    const int seq = static_cast<int>(node / tree), t = static_cast<int>(node % tree);
-    const int nodes = tree_nodes(seqlens, tree_lens, seq, tree, max_pages);
-    if (t >= nodes) return;  // also a sequence out of range (-1)
-    const int len = seqlens[seq];
-    const int n = len + __popcll(mask[node] & first_tokens(nodes));
-    const int steps = (len + kPage - 1) / kPage + 1;
-    merge_splits(partials + row * max_splits * kPartialFloats,
-                 (steps + steps_per_split - 1) / steps_per_split, n, s, alpha, L, beta, inv_ln_L,
-                 u + static_cast<size_t>(h) * kHeadDim, lane, out + row * kHeadDim,
-                 neff_out ? neff_out + row : nullptr);
+// Eight lanes per (sequence, node, query head).
+__global__ void __launch_bounds__(128) tree_merge_kernel(const TreeArgs a, long long rows) {
+    long long row = static_cast<long long>(blockIdx.x) * 16 + (threadIdx.x >> 3);
+    bool real = row < rows;
+    row = min(row, rows - 1);
+    const int h = static_cast<int>(row % a.Hq);
+    const long long node = row / a.Hq;  // seq * tree + t
+    const int seq = static_cast<int>(node / a.tree), t = static_cast<int>(node % a.tree);
+    const int nodes = tree_nodes(a.seqlens, a.tree_lens, seq, a.tree, a.max_pages);
+    real = real && t < nodes;  // not of a sequence out of range (-1)
+    const int n = real ? a.seqlens[seq] + __popcll(a.mask[node] & first_tokens(nodes)) : 0;
+    wait_for_previous_kernel();
+    const float *base = a.partials + row * a.splits * kPartialFloats;
+    finish_row(merge_parts(real ? a.splits : 0, [&](int k) { return base + k * kPartialFloats; }),
+               n, a.ep, a.u + h * kHeadDim, a.out + row * kHeadDim,
+               a.neff ? a.neff + row : nullptr, real);
 }
 
 template <int G, int MT, int kHR>
 cudaError_t launch_split(const CUtensorMap &kv, const CUtensorMap &k, const CUtensorMap &v,
-                         TreeArgs &t, int num_seqs, cudaStream_t stream) {
+                         const TreeArgs &t, const TreePlan &plan, int num_seqs,
+                         cudaStream_t stream) {
     static std::atomic<uint64_t> configured{0};  // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -258,34 +224,45 @@ cudaError_t launch_split(const CUtensorMap &kv, const CUtensorMap &k, const CUte
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
-    t.row_tiles = (G * t.tree + 8 * kHR * MT - 1) / (8 * kHR * MT);
-    tree_split_kernel<G, MT, kHR><<<dim3(t.max_splits * t.row_tiles, t.Hkv, num_seqs), 128, kSmem,
-                                    stream>>>(kv, k, v, t);
-    return cudaGetLastError();
+    return launch_ex(tree_split_kernel<G, MT, kHR>,
+                     dim3(plan.cluster * plan.splits * plan.row_tiles, t.Hkv, num_seqs),
+                     kRowThreads, kSmem, plan.cluster, false, stream, kv, k, v, t);
 }
 
 template <int G>
 cudaError_t launch_split_rows(const CUtensorMap &kv, const CUtensorMap &k, const CUtensorMap &v,
-                              TreeArgs &t, int num_seqs, cudaStream_t stream) {
-    if (G * t.tree <= 8) return launch_split<G, 1, 1>(kv, k, v, t, num_seqs, stream);
-    if (G * t.tree <= 16) return launch_split<G, 1, 2>(kv, k, v, t, num_seqs, stream);
-    return launch_split<G, 2, 2>(kv, k, v, t, num_seqs, stream);
+                              const TreeArgs &t, const TreePlan &plan, int num_seqs,
+                              cudaStream_t stream) {
+    if (plan.tile_rows == 8) return launch_split<G, 1, 1>(kv, k, v, t, plan, num_seqs, stream);
+    if (plan.tile_rows == 16) return launch_split<G, 1, 2>(kv, k, v, t, plan, num_seqs, stream);
+    return launch_split<G, 2, 2>(kv, k, v, t, plan, num_seqs, stream);
 }
 
-// Steps (pages, and the drafted rows) per split.
-int steps_per_split(int num_seqs, int max_pages, int Hkv) {
-    const long long work = static_cast<long long>(num_seqs) * Hkv * (max_pages + 1);
-    int n = 64;
-    while (n > 2 && work / n < 148ll * 3 * 4) n >>= 1;
-    return n;
+TreePlan tree_plan(int num_seqs, int max_pages, int tree, int Hq, int Hkv) {
+    TreePlan p;
+    const int R = Hq / Hkv * tree;
+    p.tile_rows = R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 128;
+    p.row_tiles = (R + p.tile_rows - 1) / p.tile_rows;
+    const long long tiles = static_cast<long long>(num_seqs) * Hkv * p.row_tiles;
+    const int steps = max_pages + 1;
+    const int per_sm = p.tile_rows == 128 ? 2 : 4;  // CTAs that an SM holds
+    p.cluster = 1;
+    while (p.cluster < kMaxCluster && tiles * p.cluster < 148 * per_sm && p.cluster * 2 <= steps)
+        p.cluster *= 2;
+    p.splits = 1;
+    while ((tiles * p.cluster * p.splits * 2 <= 148 * 2 * per_sm &&
+            p.cluster * p.splits * 16 <= steps) ||
+           p.cluster * p.splits * kMaxSteps < steps)
+        p.splits *= 2;
+    return p;
 }
 
 }  // namespace
 
 size_t tree_workspace_bytes(int num_seqs, int max_pages, int tree, int Hq, int Hkv) {
-    const int per = steps_per_split(num_seqs, max_pages, Hkv);
-    const size_t splits = (static_cast<size_t>(max_pages) + per) / per;
-    return static_cast<size_t>(num_seqs) * tree * Hq * splits * kPartialFloats * sizeof(float);
+    const TreePlan p = tree_plan(num_seqs, max_pages, tree, Hq, Hkv);
+    if (p.splits == 1) return 16;  // none is used
+    return static_cast<size_t>(num_seqs) * tree * Hq * p.splits * kPartialFloats * sizeof(float);
 }
 
 bool page_pool_map(CUtensorMap *map, const void *kv_pages, int num_pages, int Hkv) {
@@ -310,31 +287,37 @@ cudaError_t launch_decode_tree(const TreeLaunch &a) {
         encode_tiled(&v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.v), dims,
                      strides, box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
+    const TreePlan plan = tree_plan(a.num_seqs, a.max_pages, a.tree, a.Hq, a.Hkv);
     TreeArgs t;
     t.page_table = a.page_table; t.seqlens = a.seqlens; t.tree_lens = a.tree_lens; t.mask = a.mask;
-    t.q = static_cast<const __nv_bfloat16 *>(a.q);
+    t.q = static_cast<const __nv_bfloat16 *>(a.q); t.v = static_cast<const __nv_bfloat16 *>(a.v);
+    t.u = a.u; t.out = static_cast<__nv_bfloat16 *>(a.out); t.neff = a.neff;
     t.partials = static_cast<float *>(a.workspace);
     t.status = a.status; t.num_pages = a.num_pages; t.max_pages = a.max_pages;
     t.Hq = a.Hq; t.Hkv = a.Hkv; t.tree = a.tree;
-    t.steps_per_split = steps_per_split(a.num_seqs, a.max_pages, a.Hkv);
-    t.max_splits = (a.max_pages + t.steps_per_split) / t.steps_per_split;
-    t.s = a.s; t.alpha = a.alpha; t.L = static_cast<float>(a.L);
+    t.splits = plan.splits; t.row_tiles = plan.row_tiles;
+    const float L = static_cast<float>(a.L);
+    t.ep = Epilogue{a.s, a.alpha, L, a.beta, 1.0f / logf(L)};
     cudaError_t e;
-    switch (a.Hq / a.Hkv) {
-        case 1: e = launch_split_rows<1>(kv, k, v, t, a.num_seqs, a.stream); break;
-        case 2: e = launch_split_rows<2>(kv, k, v, t, a.num_seqs, a.stream); break;
-        case 4: e = launch_split_rows<4>(kv, k, v, t, a.num_seqs, a.stream); break;
-        case 8: e = launch_split_rows<8>(kv, k, v, t, a.num_seqs, a.stream); break;
+    if (plan.tile_rows == 128)
+        e = launch_tree_tc(kv, k, v, t, plan, a.num_seqs, a.stream);
+    else switch (a.Hq / a.Hkv) {
+        case 1: e = launch_split_rows<1>(kv, k, v, t, plan, a.num_seqs, a.stream); break;
+        case 2: e = launch_split_rows<2>(kv, k, v, t, plan, a.num_seqs, a.stream); break;
+        case 4: e = launch_split_rows<4>(kv, k, v, t, plan, a.num_seqs, a.stream); break;
+        case 8: e = launch_split_rows<8>(kv, k, v, t, plan, a.num_seqs, a.stream); break;
         default: return cudaErrorInvalidValue;
     }
     if (e != cudaSuccess) return e;
-    const long long rows = static_cast<long long>(a.num_seqs) * a.tree * a.Hq;
-    tree_merge_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, a.stream>>>(
-        t.partials, a.seqlens, a.tree_lens, a.mask, a.u, static_cast<__nv_bfloat16 *>(a.out),
-        a.neff, rows, a.Hq, a.tree, a.max_pages, t.steps_per_split, t.max_splits, a.s, a.alpha,
-        static_cast<float>(a.L), a.beta, 1.0f / logf(static_cast<float>(a.L)));
-    count_launches(2);
-    return cudaGetLastError();
+    count_launches(1);
+    if (plan.splits > 1) {
+        const long long rows = static_cast<long long>(a.num_seqs) * a.tree * a.Hq;
+        e = launch_ex(tree_merge_kernel, dim3(static_cast<unsigned>((rows + 15) / 16)), 128, 0, 1,
+                      true, a.stream, t, rows);
+        if (e != cudaSuccess) return e;
+        count_launches(1);
+    }
+    return cudaSuccess;
 }
 
 }  // namespace polar

@@ -553,53 +553,60 @@ def _decode_params(Hq, Hkv, D, dtype, s, alpha, L, beta):
 
 
 class _Scope:
-    """A call on `device` and `stream` (None: the device's current stream):
-    what the call allocates belongs to that device and stream."""
-    __slots__ = ("device", "given", "stack")
+    """A call on the device of `tensor` and on `stream` (None: the device's
+    current stream): what the call allocates belongs to that device and stream.
+    Entering gives the stream's handle; where the device is current and no
+    stream is given, nothing is switched."""
+    __slots__ = ("tensor", "given", "stack")
 
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError("inputs must be contiguous CUDA tensors")
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream of {stream.device} for tensors on {device}")
-        self.device, self.given, self.stack = device, stream, []
+    def __init__(self, tensor, stream):
+        self.tensor, self.given, self.stack = tensor, stream, None
 
     def __enter__(self):
-        if torch.cuda.current_device() != self.device.index:
-            self.stack.append(torch.cuda.device(self.device))
+        index = self.tensor.get_device()
+        if index < 0:
+            raise ValueError("inputs must be contiguous CUDA tensors")
+        if self.given is None and index == torch._C._cuda_getDevice():
+            return torch._C._cuda_getCurrentRawStream(index)
+        if self.given is not None and self.given.device.index != index:
+            raise ValueError(f"stream of {self.given.device} for tensors on cuda:{index}")
+        self.stack = [torch.cuda.device(index)]
         if self.given is not None:
             self.stack.append(torch.cuda.stream(self.given))
         for c in self.stack:
             c.__enter__()
-        s = self.given if self.given is not None else torch.cuda.current_stream()
-        return s.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(index)
 
     def __exit__(self, *exc):
-        for c in reversed(self.stack):
+        for c in reversed(self.stack or ()):
             c.__exit__(*exc)
 
 
-def _need(name, t, dtype, shape, device):
-    """t's address, once it is a contiguous tensor of this type, shape and device."""
-    if t.dtype is dtype and t.device == device and t.is_contiguous() and tuple(t.shape) == shape:
+def _need(name, t, dtype, shape, like):
+    """t's address, once it is a contiguous tensor of this type and shape on the
+    device of `like`."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() \
+            and t.get_device() == like.get_device():
         return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on {device}")
+    if t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on {like.device}")
     raise ValueError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
 
 
-def _need_or_none(name, t, dtype, shape, device):
-    return None if t is None else _need(name, t, dtype, shape, device)
+def _need_or_none(name, t, dtype, shape, like):
+    return None if t is None else _need(name, t, dtype, shape, like)
 
 
-def _scratch(workspace, need, device):
-    """The workspace's address and size; a fresh one where the caller gave none."""
+def _scratch(workspace, need, like):
+    """The workspace, its address and its size; a fresh one of need() bytes where
+    the caller gave none."""
     if workspace is None:
-        workspace = torch.empty(max(int(need), 16), device=device, dtype=torch.uint8)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        workspace = torch.empty(max(need(), 16), device=like.device, dtype=torch.uint8)
+        return workspace, workspace.data_ptr(), workspace.numel()
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -609,6 +616,7 @@ def _pool_shape(kv_pages, D):
     return kv_pages.shape[0], kv_pages.shape[2]
 
 
+@functools.lru_cache(maxsize=256)
 def decode_tree_workspace_size(num_seqs: int, max_pages: int, tree: int, Hq: int, Hkv: int) -> int:
     _, pp = _decode_params(Hq, Hkv, 64, POLAR_BF16, 8.0, 0.3, 2048, 1.0)
     return int(lib().polar_attn_decode_tree_workspace_size(num_seqs, max_pages, tree, pp))
@@ -626,31 +634,31 @@ def decode_paged_tree(q, k, v, tree_mask, kv_pages, page_table, seqlens, u, out=
     here)."""
     N, M, Hq, D = q.shape
     P_, Hkv = _pool_shape(kv_pages, D)
-    dev, bf16, i32, f32 = q.device, torch.bfloat16, torch.int32, torch.float32
+    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     max_pages = page_table.shape[1]
-    with _Scope(dev, stream) as st:
-        ptr = (_need("q", q, bf16, (N, M, Hq, D), dev), _need("k", k, bf16, (N, M, Hkv, D), dev),
-               _need("v", v, bf16, (N, M, Hkv, D), dev),
-               _need("tree_mask", tree_mask, torch.int64, (N, M), dev),
-               _need_or_none("tree_lens", tree_lens, i32, (N,), dev), M,
-               _need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, D), dev), P_,
-               _need("page_table", page_table, i32, (N, max_pages), dev), max_pages,
-               _need("seqlens", seqlens, i32, (N,), dev), N, _need("u", u, f32, (Hq, D), dev))
+    with _Scope(q, stream) as st:
+        ptr = (_need("q", q, bf16, (N, M, Hq, D), q), _need("k", k, bf16, (N, M, Hkv, D), q),
+               _need("v", v, bf16, (N, M, Hkv, D), q),
+               _need("tree_mask", tree_mask, torch.int64, (N, M), q),
+               _need_or_none("tree_lens", tree_lens, i32, (N,), q), M,
+               _need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, D), q), P_,
+               _need("page_table", page_table, i32, (N, max_pages), q), max_pages,
+               _need("seqlens", seqlens, i32, (N,), q), N, _need("u", u, f32, (Hq, D), q))
         _, pp = _decode_params(Hq, Hkv, D, POLAR_BF16, s, alpha, L, beta)
         if out is None:
             out = torch.empty_like(q)
         if neff is None and want_neff:
-            neff = torch.empty((N, M, Hq), device=dev, dtype=f32)
-        need = 0 if workspace is not None else \
-            lib().polar_attn_decode_tree_workspace_size(N, max_pages, M, pp)
-        workspace, wp, wb = _scratch(workspace, need, dev)
+            neff = torch.empty((N, M, Hq), device=q.device, dtype=f32)
+        workspace, wp, wb = _scratch(
+            workspace, lambda: decode_tree_workspace_size(N, max_pages, M, Hq, Hkv), q)
         _check(lib().polar_attn_decode_paged_tree(
-            *ptr, pp, _need("out", out, bf16, (N, M, Hq, D), dev),
-            _need_or_none("neff", neff, f32, (N, M, Hq), dev), wp, wb, st),
+            *ptr, pp, _need("out", out, bf16, (N, M, Hq, D), q),
+            _need_or_none("neff", neff, f32, (N, M, Hq), q), wp, wb, st),
             "polar_attn_decode_paged_tree")
     return out, neff
 
 
+@functools.lru_cache(maxsize=256)
 def decode_sparse_workspace_size(num_seqs: int, max_pages: int, keep: int, Hq: int,
                                  Hkv: int) -> int:
     _, pp = _decode_params(Hq, Hkv, 64, POLAR_BF16, 8.0, 0.3, 2048, 1.0)
@@ -668,29 +676,28 @@ def decode_paged_sparse(q, kv_pages, bounds, page_table, seqlens, u, keep, out=N
     N, Hq, D = q.shape
     P_, Hkv = _pool_shape(kv_pages, D)
     keep = int(keep)
-    dev, bf16, i32, f32 = q.device, torch.bfloat16, torch.int32, torch.float32
+    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     max_pages = page_table.shape[1]
-    with _Scope(dev, stream) as st:
-        ptr = (_need("q", q, bf16, (N, Hq, D), dev),
-               _need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, D), dev),
-               _need("bounds", bounds, bf16, (P_, Hkv, 2, D), dev), P_,
-               _need("page_table", page_table, i32, (N, max_pages), dev), max_pages,
-               _need("seqlens", seqlens, i32, (N,), dev), N, keep,
-               _need("u", u, f32, (Hq, D), dev))
+    with _Scope(q, stream) as st:
+        ptr = (_need("q", q, bf16, (N, Hq, D), q),
+               _need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, D), q),
+               _need("bounds", bounds, bf16, (P_, Hkv, 2, D), q), P_,
+               _need("page_table", page_table, i32, (N, max_pages), q), max_pages,
+               _need("seqlens", seqlens, i32, (N,), q), N, keep,
+               _need("u", u, f32, (Hq, D), q))
         _, pp = _decode_params(Hq, Hkv, D, POLAR_BF16, s, alpha, L, beta)
         if out is None:
             out = torch.empty_like(q)
         if neff is None and want_neff:
-            neff = torch.empty((N, Hq), device=dev, dtype=f32)
+            neff = torch.empty((N, Hq), device=q.device, dtype=f32)
         if selected is None and want_selected:
-            selected = torch.empty((N, Hkv, max(keep, 0)), device=dev, dtype=i32)
-        need = 0 if workspace is not None else \
-            lib().polar_attn_decode_sparse_workspace_size(N, max_pages, keep, pp)
-        workspace, wp, wb = _scratch(workspace, need, dev)
+            selected = torch.empty((N, Hkv, max(keep, 0)), device=q.device, dtype=i32)
+        workspace, wp, wb = _scratch(
+            workspace, lambda: decode_sparse_workspace_size(N, max_pages, keep, Hq, Hkv), q)
         _check(lib().polar_attn_decode_paged_sparse(
-            *ptr, pp, _need("out", out, bf16, (N, Hq, D), dev),
-            _need_or_none("neff", neff, f32, (N, Hq), dev),
-            _need_or_none("selected", selected, i32, (N, Hkv, keep), dev), wp, wb, st),
+            *ptr, pp, _need("out", out, bf16, (N, Hq, D), q),
+            _need_or_none("neff", neff, f32, (N, Hq), q),
+            _need_or_none("selected", selected, i32, (N, Hkv, keep), q), wp, wb, st),
             "polar_attn_decode_paged_sparse")
     return out, neff, selected
 
@@ -705,8 +712,8 @@ class PageCache:
 
     def __init__(self, kv_pages, refs=None, bounds=None):
         P_, Hkv = _pool_shape(kv_pages, 64)
-        dev, bf16 = kv_pages.device, torch.bfloat16
-        if dev.type != "cuda":
+        dev, bf16 = kv_pages, torch.bfloat16
+        if not kv_pages.is_cuda:
             raise ValueError("inputs must be contiguous CUDA tensors")
         self.kv_pages, self.refs, self.bounds = kv_pages, refs, bounds
         self._c = Cache(_need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, 64), dev),
@@ -722,7 +729,7 @@ def cache_workspace_size(cache: PageCache, num_seqs: int) -> int:
 
 def _rows(cache, page_table, seqlens):
     """(addresses and sizes of a page table and its lengths), rows, pages a row."""
-    dev, i32 = cache.kv_pages.device, torch.int32
+    dev, i32 = cache.kv_pages, torch.int32
     N, max_pages = page_table.shape
     return (_need("page_table", page_table, i32, (N, max_pages), dev),
             _need("seqlens", seqlens, i32, (N,), dev), N, max_pages)
@@ -734,14 +741,13 @@ def cache_reserve(cache: PageCache, page_table, seqlens, grow, granted=None, wor
     copies a shared last page) and grows page_table [N,max_pages] and seqlens
     [N] (int32) in place.  Returns granted [N] int32: grow, or 0 from the first
     row on that the pool cannot serve."""
-    dev, i32 = cache.kv_pages.device, torch.int32
-    with _Scope(dev, stream) as st:
+    dev, i32 = cache.kv_pages, torch.int32
+    with _Scope(cache.kv_pages, stream) as st:
         table, lens, N, max_pages = _rows(cache, page_table, seqlens)
         g = _need("grow", grow, i32, (N,), dev)
         if granted is None:
             granted = torch.empty_like(grow)
-        need = 0 if workspace is not None else cache_workspace_size(cache, N)
-        workspace, wp, wb = _scratch(workspace, need, dev)
+        workspace, wp, wb = _scratch(workspace, lambda: cache_workspace_size(cache, N), dev)
         _check(lib().polar_attn_cache_reserve(cache._p, table, max_pages, lens, g, N,
                                               _need("granted", granted, i32, (N,), dev), wp, wb,
                                               st), "polar_attn_cache_reserve")
@@ -753,8 +759,8 @@ def cache_append(cache: PageCache, k, v, page_table, seqlens, counts=None, pick=
     """Writes the newest tokens of each row: token t < counts[n] (None: all) of
     row n, from k, v [N,T,Hkv,64] row t (pick [N,C] int32: row pick[n,t]), to
     position seqlens[n] - counts[n] + t; the touched pages' bounds are kept."""
-    dev, bf16, i32 = cache.kv_pages.device, torch.bfloat16, torch.int32
-    with _Scope(dev, stream) as st:
+    dev, bf16, i32 = cache.kv_pages, torch.bfloat16, torch.int32
+    with _Scope(cache.kv_pages, stream) as st:
         table, lens, N, max_pages = _rows(cache, page_table, seqlens)
         if k.dim() != 4:
             raise ValueError(f"k must be [N, T, Hkv, 64], not {tuple(k.shape)}")
@@ -773,8 +779,8 @@ def cache_fork(cache: PageCache, src_table, src_lens, src_rows, dst_table, dst_l
     """Row i of dst_table, dst_lens becomes a copy of row src_rows[i] (int32) of
     src_table, src_lens that shares its pages; a negative source leaves the row
     alone.  The two tables may not overlap."""
-    dev, i32 = cache.kv_pages.device, torch.int32
-    with _Scope(dev, stream) as st:
+    dev, i32 = cache.kv_pages, torch.int32
+    with _Scope(cache.kv_pages, stream) as st:
         src, slens, S, width = _rows(cache, src_table, src_lens)
         dst, dlens, N, max_pages = _rows(cache, dst_table, dst_lens)
         if width != max_pages:
@@ -787,8 +793,8 @@ def cache_fork(cache: PageCache, src_table, src_lens, src_rows, dst_table, dst_l
 def cache_free(cache: PageCache, page_table, seqlens, keep=None, *, stream=None):
     """Cuts each row to its first keep [N] int32 tokens (None: none; negative:
     the row is left alone) and gives the pages behind them back, in place."""
-    dev = cache.kv_pages.device
-    with _Scope(dev, stream) as st:
+    dev = cache.kv_pages
+    with _Scope(cache.kv_pages, stream) as st:
         table, lens, N, max_pages = _rows(cache, page_table, seqlens)
         _check(lib().polar_attn_cache_free(
             cache._p, table, max_pages, lens,
@@ -800,13 +806,12 @@ def cache_compact(cache: PageCache, page_table, seqlens, used=None, workspace=No
     """Moves the live pages to the front of the pool and rewrites page_table (all
     rows that name pages of this pool) in place.  Returns used [1] int32: the
     number of live pages, which are pages 0 .. used - 1 afterwards."""
-    dev, i32 = cache.kv_pages.device, torch.int32
-    with _Scope(dev, stream) as st:
+    dev, i32 = cache.kv_pages, torch.int32
+    with _Scope(cache.kv_pages, stream) as st:
         table, lens, N, max_pages = _rows(cache, page_table, seqlens)
         if used is None:
-            used = torch.empty(1, device=dev, dtype=i32)
-        need = 0 if workspace is not None else cache_workspace_size(cache, N)
-        workspace, wp, wb = _scratch(workspace, need, dev)
+            used = torch.empty(1, device=dev.device, dtype=i32)
+        workspace, wp, wb = _scratch(workspace, lambda: cache_workspace_size(cache, N), dev)
         _check(lib().polar_attn_cache_compact(cache._p, table, max_pages, lens, N,
                                               _need("used", used, i32, (1,), dev), wp, wb, st),
                "polar_attn_cache_compact")
