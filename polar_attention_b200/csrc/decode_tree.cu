@@ -241,25 +241,29 @@ cudaError_t launch_split_rows(const CUtensorMap &kv, const CUtensorMap &k, const
 TreePlan tree_plan(int num_seqs, int max_pages, int tree, int Hq, int Hkv) {
     TreePlan p;
     const int R = Hq / Hkv * tree;
-    p.tile_rows = R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 128;
+    p.tile_rows = R <= 8 ? 8 : R <= 16 ? 16 : 32;
     p.row_tiles = (R + p.tile_rows - 1) / p.tile_rows;
     const long long tiles = static_cast<long long>(num_seqs) * Hkv * p.row_tiles;
     const int steps = max_pages + 1;
-    const int per_sm = p.tile_rows == 128 ? 2 : 4;  // CTAs that an SM holds
     p.cluster = 1;
-    while (p.cluster < kMaxCluster && tiles * p.cluster < 148 * per_sm && p.cluster * 2 <= steps)
+    while (p.cluster < kMaxCluster && tiles * p.cluster < 148 * 4 && p.cluster * 2 <= steps)
         p.cluster *= 2;
     p.splits = 1;
-    while ((tiles * p.cluster * p.splits * 2 <= 148 * 2 * per_sm &&
-            p.cluster * p.splits * 16 <= steps) ||
+    while ((tiles * p.cluster * p.splits * 2 <= 148 * 8 && p.cluster * p.splits * 16 <= steps) ||
            p.cluster * p.splits * kMaxSteps < steps)
         p.splits *= 2;
     return p;
 }
 
+// Above 32 rows the 128-row tiles of the tensor cores are faster, though most of
+// a tile may be padding.
+bool uses_tc(int tree, int Hq, int Hkv) { return Hq / Hkv * tree > 32; }
+
 }  // namespace
 
 size_t tree_workspace_bytes(int num_seqs, int max_pages, int tree, int Hq, int Hkv) {
+    if (uses_tc(tree, Hq, Hkv))
+        return tree_tc_workspace_bytes(tree_tc_ctas(num_seqs, max_pages, tree, Hq, Hkv));
     const TreePlan p = tree_plan(num_seqs, max_pages, tree, Hq, Hkv);
     if (p.splits == 1) return 16;  // none is used
     return static_cast<size_t>(num_seqs) * tree * Hq * p.splits * kPartialFloats * sizeof(float);
@@ -294,14 +298,17 @@ cudaError_t launch_decode_tree(const TreeLaunch &a) {
     t.u = a.u; t.out = static_cast<__nv_bfloat16 *>(a.out); t.neff = a.neff;
     t.partials = static_cast<float *>(a.workspace);
     t.status = a.status; t.num_pages = a.num_pages; t.max_pages = a.max_pages;
-    t.Hq = a.Hq; t.Hkv = a.Hkv; t.tree = a.tree;
+    t.Hq = a.Hq; t.Hkv = a.Hkv; t.tree = a.tree; t.num_seqs = a.num_seqs;
     t.splits = plan.splits; t.row_tiles = plan.row_tiles;
     const float L = static_cast<float>(a.L);
     t.ep = Epilogue{a.s, a.alpha, L, a.beta, 1.0f / logf(L)};
     cudaError_t e;
-    if (plan.tile_rows == 128)
-        e = launch_tree_tc(kv, k, v, t, plan, a.num_seqs, a.stream);
-    else switch (a.Hq / a.Hkv) {
+    if (uses_tc(a.tree, a.Hq, a.Hkv)) {
+        count_launches(2);
+        return launch_tree_tc(kv, k, v, t,
+                              tree_tc_ctas(a.num_seqs, a.max_pages, a.tree, a.Hq, a.Hkv), a.stream);
+    }
+    switch (a.Hq / a.Hkv) {
         case 1: e = launch_split_rows<1>(kv, k, v, t, plan, a.num_seqs, a.stream); break;
         case 2: e = launch_split_rows<2>(kv, k, v, t, plan, a.num_seqs, a.stream); break;
         case 4: e = launch_split_rows<4>(kv, k, v, t, plan, a.num_seqs, a.stream); break;

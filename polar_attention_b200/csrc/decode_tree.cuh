@@ -14,22 +14,23 @@ struct TreeArgs {
     __nv_bfloat16 *out;
     float *neff, *partials;
     int *status;
-    int num_pages, max_pages, Hq, Hkv, tree;
+    int num_seqs, num_pages, max_pages, Hq, Hkv, tree;
     int splits;     // clusters per row tile
     int row_tiles;  // row tiles per (sequence, kv head)
     Epilogue ep;
 };
 
-struct TreePlan {
-    int tile_rows;  // 8, 16 or 32: mma.sync; 128: tcgen05
+struct TreePlan {  // the mma.sync kernel's grid
+    int tile_rows;  // 8, 16 or 32
     int row_tiles, cluster, splits;
 };
 
-// The tcgen05 kernel (128-row tiles), given the tensor maps over the page pool
-// and the drafted keys and values.
+// The tcgen05 kernel (128-row tiles): its CTAs, the workspace they need, and
+// the launch, given the tensor maps over the page pool and the drafted rows.
+int tree_tc_ctas(int num_seqs, int max_pages, int tree, int Hq, int Hkv);
+size_t tree_tc_workspace_bytes(int ctas);
 cudaError_t launch_tree_tc(const CUtensorMap &kv, const CUtensorMap &k, const CUtensorMap &v,
-                           const TreeArgs &t, const TreePlan &plan, int num_seqs,
-                           cudaStream_t stream);
+                           const TreeArgs &t, int ctas, cudaStream_t stream);
 
 // Number of drafted nodes of a sequence, or -1 if its lengths are out of range.
 __device__ __forceinline__ int tree_nodes(const int32_t *seqlens, const int32_t *tree_lens, int seq,

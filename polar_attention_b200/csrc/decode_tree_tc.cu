@@ -2,21 +2,29 @@
 // for trees whose rows (node, query head of the kv group) fill a good part of
 // a 128-row tile.
 //
-// A CTA has one row tile of a (sequence, kv head) and a share of its steps: the
-// cached pages and, last, the drafted rows.  Per step of 64 keys:
-//   S = Q K^T   tcgen05.mma M=128 N=64 K=64, both operands in shared memory
-//   P, stats    one thread per row reads its 64 scores from tensor memory,
-//               keeps max, l, l2, S1 and S2 in registers and writes the weights
-//               back as bf16
-//   O += P V    tcgen05.mma M=128 N=64 K=64, P from tensor memory
-// S is double-buffered (P lies in its S's columns), so that the next scores are
-// formed while the softmax warps work.  The reference max of a row moves only
-// when a logit exceeds it by more than 2^8 (kRescaleThreshold); O is then
-// rescaled in tensor memory by the row's thread, behind the products in flight.
+// Work.  A tile is 128 rows of one (sequence, kv head); its steps are the
+// cached pages and, last, the drafted rows, 64 keys each.  All steps of all
+// tiles in a row, cut into equal shares, are the CTAs' work: whatever the
+// sequences' lengths, the CTAs end together, and tiles that read the same pages
+// do so at the same time.  A CTA goes through its share tile by tile; a tile it
+// holds whole it finishes, of a tile it shares it stores the rows' states, which
+// tree_tc_merge_kernel joins (at most two such tiles a CTA: its first and last).
 //
-// Tensor memory: 256 columns (S0 S1 O: 64 fp32 columns each), so two CTAs share
-// an SM and one's softmax covers the other's waits.  Four warps do the softmax,
-// one copies, one issues the products.
+// Step.  S = Q K^T   tcgen05.mma M=128 N=64 K=64, operands in shared memory
+//        P, stats    one thread per row reads its scores from tensor memory 32
+//                    at a time, keeps max, l, l2, S1 and S2 in registers and
+//                    writes the weights back as bf16
+//        O += P V    tcgen05.mma M=128 N=64 K=64, P from tensor memory
+// P lies in S's columns, so a CTA's step is one chain, and 128 columns (S, O) and
+// two 16 KB stages are all it needs: four CTAs share an SM and cover each other's
+// waits.  What bounds the kernel is the exponentials (16 an SM and clock: 512
+// clocks a step of a full tile).
+//
+// The reference max of a row moves only when a logit exceeds it by more than
+// 2^8 (kRescaleThreshold), and then to a whole number of log2 units: weights are
+// formed against the one at hand in the pass that finds the scores' max, and only
+// where that was too low they are formed again, and O and the step's stored
+// weights multiplied by a power of two in tensor memory by the row's thread.
 #include <algorithm>
 #include <atomic>
 
@@ -28,394 +36,559 @@ namespace polar {
 namespace {
 
 constexpr int kTileRows = 128;
-constexpr int kStagesTc = 5;
-constexpr int kTcThreads = 192;
+constexpr int kStagesTc = 2;
+constexpr int kTcThreads = 160;  // four softmax warps and one that copies and issues
+constexpr int kTcPerSm = 4;
 constexpr int kQBytes = kTileRows * kHeadDim * 2;
 constexpr int kSmemTc = kQBytes + kStagesTc * kStageBytes + 1024;  // + alignment slack
-constexpr uint32_t kColS = 0, kColO = 128, kTmemCols = 256;
-static_assert(kTileRows * kPartialFloats * 4 <= kStagesTc * kStageBytes, "ring too small");
+constexpr uint32_t kColS = 0, kColO = 64;
+constexpr int kSlotFloats = kTileRows * kPartialFloats;
 
-__device__ __forceinline__ void tmem_alloc_256(uint32_t *dst_smem) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(
+__device__ __forceinline__ void tmem_alloc_128(uint32_t *dst_smem) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(
                      smem_u32(dst_smem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_dealloc_256(uint32_t taddr) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(taddr) : "memory");
+__device__ __forceinline__ void tmem_dealloc_128(uint32_t taddr) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(taddr) : "memory");
+}
+
+// Steps that a share has at least.
+constexpr int kMinShare = 4;
+constexpr int kMergeRows = 16;  // rows of a merge block
+
+constexpr size_t tc_tiles_bytes(int ctas) {
+    return (static_cast<size_t>(ctas) * 5 * sizeof(int) + 15) / 16 * 16;
+}
+
+// One pass over a thread's 32 scores against its reference max: the weights
+// 2^(cl2 S - m_ref) as packed bf16 (operands of the second product, off by at
+// most half a step, 2^-8 of themselves; the sums take them unrounded), their
+// sums, the raw sums and the max.  Scores whose mask bit is clear do not count.
+struct TileSums {
+    float top, s1, s2, l, l2;
+};
+template <bool kAll>
+__device__ __forceinline__ TileSums tile_pass(const uint32_t (&sr)[32], uint32_t mask, float cl2,
+                                              float m_ref, uint32_t (&pk)[16]) {
+    const float2 sc = make_float2(cl2, cl2), nm = make_float2(-m_ref, -m_ref);
+    float mx[2] = {-INFINITY, -INFINITY};
+    float2 a1 = make_float2(0.f, 0.f), a2 = a1, la = a1, l2a = a1;
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        float2 v = make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
+        const bool v0 = kAll || (mask >> e & 1u), v1 = kAll || (mask >> (e + 1) & 1u);
+        const float2 z = f2_fma(v, sc, nm);
+        mx[(e >> 1) & 1] = max3(mx[(e >> 1) & 1], v0 ? v.x : -INFINITY, v1 ? v.y : -INFINITY);
+        if (!kAll) v = make_float2(v0 ? v.x : 0.f, v1 ? v.y : 0.f);
+        a1 = f2_add(a1, v);
+        a2 = f2_fma(v, v, a2);
+        float2 p = make_float2(ex2(z.x), ex2(z.y));
+        if (!kAll) p = make_float2(v0 ? p.x : 0.f, v1 ? p.y : 0.f);
+        la = f2_add(la, p);
+        l2a = f2_fma(p, p, l2a);
+        pk[e >> 1] = pack_bf16(p.x, p.y);
+    }
+    return TileSums{fmaxf(mx[0], mx[1]), a1.x + a1.y, a2.x + a2.y, la.x + la.y, l2a.x + l2a.y};
 }
 
 struct RowStats {  // one row's streaming state, in its thread
     float m_ref, m_raw, l, l2, s1, s2;
 };
 
-// Max and raw sums of a row's 64 scores; masked scores (bit clear) do not count.
-template <bool kAll>
-__device__ __forceinline__ float raw_stats(uint32_t (&sr)[2][32], uint64_t mask, RowStats &x) {
-    float mx[2] = {-INFINITY, -INFINITY};
-    float2 a1 = make_float2(0.f, 0.f), a2 = a1;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t m = static_cast<uint32_t>(mask >> (32 * h));
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-            float2 v = make_float2(__uint_as_float(sr[h][e]), __uint_as_float(sr[h][e + 1]));
-            if (!kAll) {
-                const bool v0 = m >> e & 1u, v1 = m >> (e + 1) & 1u;
-                mx[(e >> 1) & 1] = max3(mx[(e >> 1) & 1], v0 ? v.x : -INFINITY, v1 ? v.y : -INFINITY);
-                v.x = v0 ? v.x : 0.f;
-                v.y = v1 ? v.y : 0.f;
-            } else {
-                mx[(e >> 1) & 1] = max3(mx[(e >> 1) & 1], v.x, v.y);
-            }
-            a1 = f2_add(a1, v);
-            a2 = f2_fma(v, v, a2);
-        }
-    }
-    x.s1 += a1.x + a1.y;
-    x.s2 += a2.x + a2.y;
-    return fmaxf(mx[0], mx[1]);
-}
+// What a share's last tile leaves to the merge: where a shared tile begins.
+struct SharedTile {
+    int seq, head, row0, parts;  // parts 0: none begins here
+    int slot;                    // of the first part; part j > 0: slot 2 (cta + j)
+};
 
-// Weights 2^(cl2 S - m_ref) as packed bf16, and their sums l and l2 (of the
-// unrounded weights; the bf16 operand is off by at most 2^-9 of itself).
-template <bool kAll>
-__device__ __forceinline__ void weights(const uint32_t (&sr)[2][32], uint64_t mask, float cl2,
-                                        RowStats &x, uint32_t (&pk)[32]) {
-    const float ref = x.m_ref == -INFINITY ? 0.f : x.m_ref;  // nothing seen yet: weights are zero
-    const float2 sc = make_float2(cl2, cl2), nm = make_float2(-ref, -ref);
-    float2 la = make_float2(0.f, 0.f), l2a = la;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t m = static_cast<uint32_t>(mask >> (32 * h));
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-            const float2 v = make_float2(__uint_as_float(sr[h][e]), __uint_as_float(sr[h][e + 1]));
-            const float2 z = f2_fma(v, sc, nm);
-            float2 p = make_float2(ex2(z.x), ex2(z.y));
-            if (!kAll) {
-                p.x = m >> e & 1u ? p.x : 0.f;
-                p.y = m >> (e + 1) & 1u ? p.y : 0.f;
-            }
-            la = f2_add(la, p);
-            l2a = f2_fma(p, p, l2a);
-            pk[16 * h + (e >> 1)] = pack_bf16(p.x, p.y);
+// A share of the steps, tile by tile.
+template <int G>
+struct Walk {
+    const TreeArgs &a;
+    int seq, tile, step;      // tile: head * tiles per head + row tile
+    int nodes, len, per_tile, tiles;  // of the sequence
+    long long left;
+
+    __device__ __forceinline__ int tiles_per_head() const {
+        return (G * nodes + kTileRows - 1) / kTileRows;
+    }
+    __device__ __forceinline__ void enter(int s) {
+        seq = s;
+        nodes = tree_nodes(a.seqlens, a.tree_lens, s, a.tree, a.max_pages);
+        len = a.seqlens[s];
+        per_tile = (len + kPage - 1) / kPage + 1;
+        tiles = nodes > 0 ? tiles_per_head() * a.Hkv : 0;
+    }
+    __device__ __forceinline__ int head() const { return tile / tiles_per_head(); }
+    __device__ __forceinline__ int row0() const { return tile % tiles_per_head() * kTileRows; }
+    // Steps of the current tile in this share.
+    __device__ __forceinline__ int count() const {
+        return static_cast<int>(min(left, static_cast<long long>(per_tile - step)));
+    }
+    __device__ __forceinline__ void next() {
+        left -= count();
+        step = 0;
+        if (++tile == tiles && left > 0) {
+            tile = 0;
+            do enter(seq + 1); while (tiles == 0);
         }
     }
-    x.l += la.x + la.y;
-    x.l2 += l2a.x + l2a.y;
+};
+
+template <int G>
+__device__ __forceinline__ long long steps_of(const TreeArgs &a, int seq) {
+    const int nodes = tree_nodes(a.seqlens, a.tree_lens, seq, a.tree, a.max_pages);
+    if (nodes <= 0) return 0;
+    return static_cast<long long>((a.seqlens[seq] + kPage - 1) / kPage + 1) * a.Hkv *
+           ((G * nodes + kTileRows - 1) / kTileRows);
 }
 
 template <int G>
-__global__ void __launch_bounds__(kTcThreads, 2)
+__global__ void __launch_bounds__(kTcThreads, kTcPerSm)
 tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
                const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-               const TreeArgs a) {
+               const TreeArgs a, SharedTile *__restrict__ shared_tiles) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *ring = smem + kQBytes;
-    __shared__ __align__(8) uint64_t q_full, full[kStagesTc], empty[kStagesTc];
-    __shared__ __align__(8) uint64_t s_full[2], p_ready[2], pv_done, mma_done;
+    __shared__ __align__(8) uint64_t q_full, full[kStagesTc], s_full, p_ready, pv_done, mma_done;
     __shared__ unsigned long long odd_nodes;  // drafted nodes with values that are not finite
     __shared__ uint32_t tmem_base_sh;
-    __shared__ int page[kMaxSteps];
-
-    const int C = static_cast<int>(cluster_size()), group = blockIdx.x / C;
-    const int rt = group % a.row_tiles, split = group / a.row_tiles;
-    const int part = split * C + static_cast<int>(cluster_rank());
-    const int g = blockIdx.y, seq = blockIdx.z;
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    const int nodes = tree_nodes(a.seqlens, a.tree_lens, seq, a.tree, a.max_pages);
-    if (nodes <= 0) {
-        if (nodes < 0 && blockIdx.x == 0 && g == 0 && threadIdx.x == 0)
-            record_error(a.status, POLAR_ERR_BAD_SEQLEN);
-        return;
-    }
-    const int R = G * nodes, row0 = rt * kTileRows;
-    if (row0 >= R) return;
-    const int len = a.seqlens[seq];
-    const int npg = (len + kPage - 1) / kPage;
-    const int per = (npg + a.splits * C) / (a.splits * C);  // of npg + 1 steps: the drafted rows last
-    const int p0 = min(part * per, npg + 1);
-    const int np = min(npg + 1, p0 + per) - p0;
-    const int32_t *pt = a.page_table + static_cast<size_t>(seq) * a.max_pages + p0;
+    __shared__ long long wide[kTcThreads / 32];
+    __shared__ int s_seq;
+    __shared__ long long s_offset;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
     if (threadIdx.x == 0) {
         mbar_init(&q_full, 1);
-        for (int st = 0; st < kStagesTc; ++st) {
-            mbar_init(&full[st], 1);
-            mbar_init(&empty[st], 1);
-        }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&s_full[b], 1);
-            mbar_init(&p_ready[b], 4);
-        }
+        for (int st = 0; st < kStagesTc; ++st) mbar_init(&full[st], 1);
+        mbar_init(&s_full, 1);
+        mbar_init(&p_ready, 4);
         mbar_init(&pv_done, 1);
         mbar_init(&mma_done, 1);
         odd_nodes = 0;
         fence_barrier_init();
     }
-    if (w == 5) tmem_alloc_256(&tmem_base_sh);
-    // A page id outside the pool is reported; its step reads page 0 and counts no key.
-    for (int i = threadIdx.x; i < np; i += kTcThreads) {
-        const int x = p0 + i == npg ? 0 : pt[i];
-        page[i] = x >= 0 && x < a.num_pages ? x : -1;
-        if (page[i] < 0) record_error(a.status, POLAR_ERR_BAD_PAGE);
+    // This CTA's share: steps cta * share .. of all sequences' steps in a row.
+    long long all = 0;
+    for (int s = threadIdx.x; s < a.num_seqs; s += kTcThreads) {
+        if (cta == 0 && tree_nodes(a.seqlens, a.tree_lens, s, a.tree, a.max_pages) < 0)
+            record_error(a.status, POLAR_ERR_BAD_SEQLEN);
+        all += steps_of<G>(a, s);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
+    if (lane == 0) wide[w] = all;
+    __syncthreads();
+    all = 0;
+    for (int i = 0; i < kTcThreads / 32; ++i) all += wide[i];
+    const long long share = max((all + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinShare));
+    const long long first = min(cta * share, all), count = min(share, all - first);
+    if (count == 0) {
+        if (threadIdx.x == 0) shared_tiles[cta].parts = 0;
+        return;
+    }
+    long long before = 0;
+    for (int s0 = 0; s0 < a.num_seqs; s0 += kTcThreads) {
+        const int s = s0 + threadIdx.x;
+        const long long mine = s < a.num_seqs ? steps_of<G>(a, s) : 0;
+        long long upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(~0u, upto, o);
+            if (lane >= o) upto += y;
+        }
+        __syncthreads();  // `wide` was read
+        if (lane == 31) wide[w] = upto;
+        __syncthreads();
+        for (int i = 0; i < w; ++i) upto += wide[i];
+        upto += before;
+        if (upto - mine <= first && first < upto) {
+            s_seq = s;
+            s_offset = first - (upto - mine);
+        }
+        for (int i = 0; i < kTcThreads / 32; ++i) before += wide[i];
+        if (before > first) break;  // uniform
+    }
+    if (w == 4) tmem_alloc_128(&tmem_base_sh);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
-    const uint64_t drafted = first_tokens(nodes);
-    const uint64_t *masks = a.mask + static_cast<size_t>(seq) * a.tree;
+    Walk<G> walk{a};
+    walk.left = count;
+    walk.enter(s_seq);
+    walk.tile = static_cast<int>(s_offset / walk.per_tile);
+    walk.step = static_cast<int>(s_offset % walk.per_tile);
+    if (threadIdx.x == 0) {
+        // The tile that begins here and goes on in the next shares, if any: the last.
+        Walk<G> x = walk;
+        SharedTile t{0, 0, 0, 0, 2 * cta};
+        long long done = 0;
+        for (; x.left > 0; x.next()) {
+            if (x.step == 0 && x.left < x.per_tile) {
+                const long long end = first + done + x.per_tile;  // the step behind the tile
+                t.seq = x.seq; t.head = x.head(); t.row0 = x.row0();
+                t.parts = static_cast<int>((end - 1) / share) - cta + 1;
+                t.slot = 2 * cta + (done > 0);
+            }
+            done += x.count();
+        }
+        shared_tiles[cta] = t;
+    }
 
-    // This thread's row (softmax warps).
-    const int row = row0 + static_cast<int>(threadIdx.x);
-    const bool active = w < 4 && row0 + 32 * w < R;  // the warp has a row at all
-    const uint64_t seen = w < 4 && row < R ? masks[row / G] & drafted : 0ull;
-    const int n = w < 4 && row < R ? len + __popcll(seen) : 0;
-    RowStats x{-INFINITY, -INFINITY, 0.f, 0.f, 0.f, 0.f};
-
+    int it = 0;     // steps so far, for the barriers' phases
     if (w == 4) {
-        if (lane == 0 && np > 0) {
+        // ------------------------------------------- copies and products
+        constexpr uint32_t idesc_qk = idesc_bf16(kTileRows, kPage, false);
+        constexpr uint32_t idesc_pv = idesc_bf16(kTileRows, kHeadDim, true);
+        // Q and K are K-major (SBO 1024), V is MN-major (one 64-column atom).
+        const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
+        const uint32_t k_lo = sdesc_lo(smem_u32(ring), 16);
+        const uint32_t v_lo = sdesc_lo(smem_u32(ring) + kChunkBytes, 8192);
+        constexpr uint32_t hi = kSdescHi128B, kStep = kStageBytes >> 4;
+        if (lane == 0) {
             tma_prefetch_desc(&q_map);
             tma_prefetch_desc(&kv_map);
-            mbar_arrive_expect_tx(&q_full, kQBytes);
-            tma_load_3d(smem, &q_map, 0, g * G, seq * a.tree + row0 / G, &q_full);
-            int kk = 0;
-            for (; kk < np; ++kk) {
-                const int st = kk % kStagesTc;
-                if (kk >= kStagesTc && !mbar_wait(&empty[st], ((kk / kStagesTc) - 1) & 1, a.status))
-                    break;
+        }
+        bool ok = true;
+        int tiles = 0;
+        for (; ok && walk.left > 0; walk.next(), ++tiles) {
+            const int npg = walk.per_tile - 1, g = walk.head(), row0 = walk.row0();
+            const int s0 = walk.step, n = walk.count(), base = it;
+            const int32_t *pt = a.page_table + static_cast<size_t>(walk.seq) * a.max_pages;
+            // Page ids, 32 steps at a time, one stretch ahead (in turn in two
+            // registers).  A page id outside the pool is reported; its step
+            // reads page 0 and counts no key.
+            auto ids = [&](int j0) {
+                const int p = s0 + j0 + lane;
+                return j0 + lane < n && p < npg ? pt[p] : 0;
+            };
+            int even = ids(0), odd = ids(32);
+            auto load = [&](int j) {  // step j of this tile, by lane 0 with all lanes here
+                if (j > 0 && (j & 31) == 0) {
+                    if (j & 32) even = ids(j + 32); else odd = ids(j + 32);
+                }
+                int phys = __shfl_sync(~0u, j & 32 ? odd : even, j & 31);
+                if (lane != 0) return;
+                if (phys < 0 || phys >= a.num_pages) {
+                    record_error(a.status, POLAR_ERR_BAD_PAGE);
+                    phys = 0;
+                }
+                const int st = (base + j) % kStagesTc;
                 uint8_t *dst = ring + st * kStageBytes;
                 mbar_arrive_expect_tx(&full[st], kStageBytes);
-                if (p0 + kk == npg) {
-                    tma_load_3d(dst, &k_map, 0, g, seq * a.tree, &full[st]);
-                    tma_load_3d(dst + kChunkBytes, &v_map, 0, g, seq * a.tree, &full[st]);
+                if (s0 + j == npg) {
+                    tma_load_3d(dst, &k_map, 0, g, walk.seq * a.tree, &full[st]);
+                    tma_load_3d(dst + kChunkBytes, &v_map, 0, g, walk.seq * a.tree, &full[st]);
                 } else {
-                    const int at = (max(page[kk], 0) * 2 * a.Hkv + g) * kPage;
+                    const int at = (phys * 2 * a.Hkv + g) * kPage;  // K block of the kv head
                     tma_load_2d(dst, &kv_map, 0, at, &full[st]);
                     tma_load_2d(dst + kChunkBytes, &kv_map, 0, at + a.Hkv * kPage, &full[st]);
                 }
+            };
+            // The tile before is done with its queries and stages: its last
+            // product was waited for.
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&q_full, kQBytes);
+                tma_load_3d(smem, &q_map, 0, g * G, walk.seq * a.tree + row0 / G, &q_full);
             }
-            // Every copy lands before shared memory is reused or released.
-            mbar_wait(&q_full, 0, a.status);
-            for (int j = max(0, kk - kStagesTc); j < kk; ++j)
-                mbar_wait(&full[j % kStagesTc], (j / kStagesTc) & 1, a.status);
-        }
-        __syncwarp();
-    } else if (w == 5) {
-        if (lane == 0 && np > 0) {
-            constexpr uint32_t idesc_qk = idesc_bf16(kTileRows, kPage, false);
-            constexpr uint32_t idesc_pv = idesc_bf16(kTileRows, kHeadDim, true);
-            // Q and K are K-major (SBO 1024), V is MN-major (one 64-column atom).
-            const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
-            const uint32_t k_lo = sdesc_lo(smem_u32(ring), 16);
-            const uint32_t v_lo = sdesc_lo(smem_u32(ring) + kChunkBytes, 8192);
-            constexpr uint32_t hi = kSdescHi128B, kStep = kStageBytes >> 4;
-            bool ok = mbar_wait(&q_full, 0, a.status);
-            for (int i = 0; i <= np && ok; ++i) {
-                if (i < np) {
-                    const int st = i % kStagesTc;
-                    // S_i overwrites P_(i-2): its product is done.
-                    if (i >= 2 && !(ok = mbar_wait(&pv_done, (i - 2) & 1, a.status))) break;
-                    if (!(ok = mbar_wait(&full[st], (i / kStagesTc) & 1, a.status))) break;
+            int loaded = 0;
+            for (; loaded < min(n, kStagesTc); ++loaded) load(loaded);
+            auto wait = [&](uint64_t *bar, int parity) {
+                return __all_sync(~0u, mbar_wait(bar, parity, a.status)) != 0;
+            };
+            ok = wait(&q_full, tiles & 1);
+            for (int j = 0; j < n && ok; ++j, ++it) {
+                const int st = it % kStagesTc;
+                if (!(ok = wait(&full[st], (it / kStagesTc) & 1))) break;
+                if (lane == 0) {
                     tc_fence_after();
-                    const uint32_t d = tmem + kColS + (i & 1) * 64, ka = k_lo + st * kStep;
+                    const uint32_t d = tmem + kColS, ka = k_lo + st * kStep;
                     mma_ss2<0>(d, q_lo, hi, ka, hi, idesc_qk);
                     mma_ss2<1>(d, q_lo + 2, hi, ka + 2, hi, idesc_qk);
                     mma_ss2<1>(d, q_lo + 4, hi, ka + 4, hi, idesc_qk);
                     mma_ss2<1>(d, q_lo + 6, hi, ka + 6, hi, idesc_qk);
-                    tc_commit(&s_full[i & 1]);
+                    tc_commit(&s_full);
                 }
-                if (i >= 1) {
-                    const int j = i - 1, st = j % kStagesTc;
-                    if (!(ok = mbar_wait(&p_ready[j & 1], (j >> 1) & 1, a.status))) break;
+                if (!(ok = wait(&p_ready, it & 1))) break;
+                if (lane == 0) {
                     tc_fence_after();
-                    const uint32_t va = v_lo + st * kStep, pa = tmem + kColS + (j & 1) * 64;
-                    mma_ts2(tmem + kColO, pa, va, hi, idesc_pv, j > 0);
-#pragma unroll
-                    for (int kk = 1; kk < kPage / 16; ++kk)
-                        mma_ts2(tmem + kColO, pa + 8 * kk, va + 128 * kk, hi, idesc_pv, 1u);
-                    tc_commit(&empty[st]);
+                    const uint32_t va = v_lo + st * kStep, pa = tmem + kColS, o = tmem + kColO;
+                    mma_ts2(o, pa, va, hi, idesc_pv, j > 0);
+                    mma_ts2(o, pa + 8, va + 128, hi, idesc_pv, 1u);
+                    mma_ts2(o, pa + 16, va + 256, hi, idesc_pv, 1u);
+                    mma_ts2(o, pa + 24, va + 384, hi, idesc_pv, 1u);
                     tc_commit(&pv_done);
                 }
+                // The next scores overwrite P, and the next copy this stage.
+                if (!(ok = wait(&pv_done, it & 1))) break;
+                if (loaded < n) load(loaded++);
             }
-            // All products complete before tensor memory is freed.
+            if (!ok)  // copies in flight land before shared memory is released
+                for (int st = 0; st < kStagesTc; ++st)
+                    for (int ph = 0; ph < 2; ++ph) mbar_wait(&full[st], ph, a.status);
+        }
+        if (lane == 0) {  // all products complete before tensor memory is freed
             tc_commit(&mma_done);
             mbar_wait(&mma_done, 0, a.status);
         }
         __syncwarp();
     } else {
+        // ------------------------------------------------- softmax warps
+        const int r_tile = static_cast<int>(threadIdx.x);  // row of the tile = lane of tensor memory
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * w) << 16);
-        const uint32_t tO = lane_base + kColO;
-        const float cl2 = a.ep.s * length_temperature(static_cast<float>(n), a.ep.alpha, a.ep.L) *
-                          kLog2e;
+        const uint32_t tS = lane_base + kColS, tO = lane_base + kColO;
         bool ok = true;
-        for (int i = 0; i < np; ++i) {
-            ok = mbar_wait(&s_full[i & 1], (i >> 1) & 1, a.status);
+        int segment = 0;
+        for (; ok && walk.left > 0; walk.next(), ++segment) {
+            const int npg = walk.per_tile - 1, g = walk.head(), row = walk.row0() + r_tile;
+            const int s0 = walk.step, cnt = walk.count(), nodes = walk.nodes, len = walk.len;
+            const int R = G * nodes;
+            const bool active = walk.row0() + 32 * w < R;  // the warp has a row at all
+            const uint64_t drafted = first_tokens(nodes);
+            const size_t node0 = static_cast<size_t>(walk.seq) * a.tree;
+            const uint64_t seen = row < R ? a.mask[node0 + row / G] & drafted : 0ull;
+            const int n = row < R ? len + __popcll(seen) : 0;
+            const float cl2 = a.ep.s * length_temperature(static_cast<float>(n), a.ep.alpha,
+                                                          a.ep.L) * kLog2e;
+            const int32_t *pt = a.page_table + static_cast<size_t>(walk.seq) * a.max_pages;
+            RowStats x{-INFINITY, -INFINITY, 0.f, 0.f, 0.f, 0.f};
+            uint32_t bad = 0;  // pages outside the pool, of 32 steps
+            for (int j = 0; j < cnt; ++j, ++it) {
+                if ((j & 31) == 0) {
+                    const int p = s0 + j + lane;
+                    const int id = j + lane < cnt && p < npg ? pt[p] : 0;
+                    bad = __ballot_sync(~0u, id < 0 || id >= a.num_pages);
+                }
+                ok = mbar_wait(&s_full, it & 1, a.status);
+                if (!__all_sync(~0u, ok)) { ok = false; break; }
+                tc_fence_after();
+                const bool draft = s0 + j == npg, skip = bad >> (j & 31) & 1u;
+                const int rest = len - (s0 + j) * kPage;  // cached tokens from this step on
+                const uint64_t mask = draft ? seen : skip ? 0ull : first_tokens(rest);
+                const bool whole = !draft && !skip && rest >= kPage;
+                if (!whole) {
+                    // Value rows that no row may see are zeroed, since a zero
+                    // weight does not silence what is not finite; drafted
+                    // values that are not finite are zeroed and added to the
+                    // rows that see them at the end.
+                    const int st = it % kStagesTc;
+                    const bool landed = mbar_wait(&full[st], (it / kStagesTc) & 1, a.status);
+                    const uint64_t keep = draft ? drafted : mask;
+                    uint32_t odd = 0;
+                    if (landed)
+#pragma unroll 1
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = 16 * w + 4 * e + (lane >> 3);
+                            uint4 *v = reinterpret_cast<uint4 *>(ring + st * kStageBytes +
+                                                                 kChunkBytes + r * 128) + (lane & 7);
+                            if (!(keep >> r & 1)) {
+                                *v = make_uint4(0, 0, 0, 0);
+                            } else if (draft) {
+                                const uint4 y = *v;
+                                uint32_t word[4] = {y.x, y.y, y.z, y.w};
+                                bool found = false;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const bool lo = not_finite(word[k]);
+                                    const bool up = not_finite(word[k] >> 16);
+                                    found |= lo | up;
+                                    word[k] = mask_pair(word[k], !lo, !up);
+                                }
+                                if (found) {
+                                    *v = make_uint4(word[0], word[1], word[2], word[3]);
+                                    odd |= 1u << (4 * e + (lane >> 3));
+                                }
+                            }
+                        }
+                    if (odd) atomicOr(&odd_nodes, static_cast<unsigned long long>(odd) << (16 * w));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (active) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t bits = static_cast<uint32_t>(mask >> (32 * h));
+                        uint32_t sr[32], pk[16];
+                        tmem_ld32(tS + 32 * h, sr);
+                        tmem_wait_ld();
+                        auto pass = [&](float ref) {
+                            return whole ? tile_pass<true>(sr, bits, cl2, ref, pk)
+                                         : tile_pass<false>(sr, bits, cl2, ref, pk);
+                        };
+                        TileSums t = pass(x.m_ref == -INFINITY ? 0.f : x.m_ref);
+                        const float zmax = t.top * cl2;
+                        const bool need = zmax > x.m_ref + kRescaleThreshold;
+                        if (__any_sync(~0u, need)) {
+                            // 0 where nothing was seen before; else a power of two.
+                            const float ref = ceilf(zmax);
+                            const float r = need ? exp2f(x.m_ref - ref) : 1.f;
+                            x.l *= r;
+                            x.l2 *= r * r;
+                            if (need) x.m_ref = ref;
+                            if (j > 0) {  // the product before is done: its P is overwritten here
+#pragma unroll 1
+                                for (int c = 0; c < 4; ++c) {
+                                    uint32_t o[16];
+                                    tmem_ld16(tO + 16 * c, o);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e)
+                                        o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
+                                    tmem_st16(tO + 16 * c, o);
+                                }
+                            }
+                            if (h == 1) {  // the step's first weights, exactly
+                                uint32_t o[16];
+                                tmem_ld16(tS, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = pack_bf16(__uint_as_float(o[e] << 16) * r,
+                                                     __uint_as_float(o[e] & 0xffff0000u) * r);
+                                tmem_st16(tS, o);
+                            }
+                            t = pass(x.m_ref == -INFINITY ? 0.f : x.m_ref);
+                        }
+                        x.m_raw = fmaxf(x.m_raw, t.top);
+                        x.s1 += t.s1;
+                        x.s2 += t.s2;
+                        x.l += t.l;
+                        x.l2 += t.l2;
+                        tmem_st16(tS + 16 * h, pk);
+                    }
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready);
+            }
+            if (!ok) break;
+            // The tile's last product.
+            ok = mbar_wait(&pv_done, (it - 1) & 1, a.status);
             if (!__all_sync(~0u, ok)) { ok = false; break; }
             tc_fence_after();
-            const bool draft = p0 + i == npg;
-            const int left = len - (p0 + i) * kPage;  // cached tokens of this step
-            // The step's keys: a full page, or a mask.
-            const uint64_t mask = draft ? seen : page[i] < 0 ? 0ull : first_tokens(left);
-            const bool all = !draft && page[i] >= 0 && left >= kPage;
-            if (!all) {
-                // Value rows that no row may see are zeroed, since a zero weight
-                // does not silence what is not finite; drafted values that are
-                // not finite are zeroed and added to the rows that see them at
-                // the end.
-                const int st = i % kStagesTc;
-                const bool landed = mbar_wait(&full[st], (i / kStagesTc) & 1, a.status);
-                const uint64_t keep = draft ? drafted : mask;
-                uint32_t odd = 0;
-                if (landed)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = 16 * w + 4 * e + (lane >> 3);
-                        uint4 *v = reinterpret_cast<uint4 *>(ring + st * kStageBytes + kChunkBytes +
-                                                             r * 128) + (lane & 7);
-                        if (!(keep >> r & 1)) {
-                            *v = make_uint4(0, 0, 0, 0);
-                        } else if (draft) {
-                            uint4 y = *v;
-                            uint32_t *word = reinterpret_cast<uint32_t *>(&y);
-                            bool bad = false;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const bool lo = not_finite(word[k]), up = not_finite(word[k] >> 16);
-                                bad |= lo | up;
-                                word[k] = mask_pair(word[k], !lo, !up);
-                            }
-                            if (bad) {
-                                *v = y;
-                                odd |= 1u << (4 * e + (lane >> 3));
-                            }
-                        }
-                    }
-                if (odd) atomicOr(&odd_nodes, static_cast<unsigned long long>(odd) << (16 * w));
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
-            if (active) {
-                const uint32_t tS = lane_base + kColS + (i & 1) * 64;
-                uint32_t sr[2][32], pk[32];
-                tmem_ld32(tS, sr[0]);
-                tmem_ld32(tS + 32, sr[1]);
+            if (!active) continue;
+            // Drafted values that are not finite, where they count.
+            const uint64_t extra = s0 + cnt > npg ? odd_nodes & seen : 0ull;
+            const __nv_bfloat16 *vrow = a.v + (node0 * a.Hkv + g) * kHeadDim;
+            auto column = [&](int c, uint32_t (&o)[16]) {  // O's columns 16c .. 16c + 15
+                tmem_ld16(tO + 16 * c, o);
                 tmem_wait_ld();
-                const float tmax = all ? raw_stats<true>(sr, mask, x) : raw_stats<false>(sr, mask, x);
-                x.m_raw = fmaxf(x.m_raw, tmax);
-                const float zmax = tmax * cl2;
-                const bool need = zmax > x.m_ref + kRescaleThreshold;
-                if (__any_sync(~0u, need)) {
-                    const float r = need ? exp2f(x.m_ref - zmax) : 1.f;  // 0 where nothing was seen
-                    x.l *= r;
-                    x.l2 *= r * r;
-                    if (need) x.m_ref = zmax;
-                    if (i > 0) {  // O *= r, once the products before are done
-                        ok = mbar_wait(&pv_done, (i - 1) & 1, a.status);
-                        if (!__all_sync(~0u, ok)) { ok = false; break; }
-                        tc_fence_after();
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t o[32];
-                            tmem_ld32(tO + 32 * h, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
-                            tmem_st32(tO + 32 * h, o);
-                        }
-                    }
-                }
-                if (all)
-                    weights<true>(sr, mask, cl2, x, pk);
-                else
-                    weights<false>(sr, mask, cl2, x, pk);
-                tmem_st32(tS, pk);
-                tmem_wait_st();
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready[i & 1]);
-        }
-        // Rows without a step keep the empty state.
-        if (ok && np > 0) ok = mbar_wait(&pv_done, (np - 1) & 1, a.status);
-        ok = __all_sync(~0u, ok) && np > 0;
-        tc_fence_after();
-        // The copies of this CTA have all been consumed: its ring takes the rows' states.
-        float *own = reinterpret_cast<float *>(ring) + threadIdx.x * kPartialFloats;
-        named_barrier(1, 128);  // every softmax warp is past the last product
-        if (active) {
-            // Where it counts, drafted values that are not finite.
-            const uint64_t extra = ok ? odd_nodes & seen : 0ull;
-            const __nv_bfloat16 *vrow = a.v + (static_cast<size_t>(seq) * a.tree * a.Hkv + g) *
-                                                  kHeadDim;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t o[32];
-                if (ok) {
-                    tmem_ld32(tO + 32 * h, o);
-                    tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0u;
-                }
                 for (uint64_t todo = extra; todo; todo &= todo - 1) {
                     const int j = __ffsll(static_cast<long long>(todo)) - 1;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
+                    for (int e = 0; e < 16; ++e) {
                         const float y = __bfloat162float(
-                            vrow[static_cast<size_t>(j) * a.Hkv * kHeadDim + 32 * h + e]);
+                            vrow[static_cast<size_t>(j) * a.Hkv * kHeadDim + 16 * c + e]);
                         if (!(fabsf(y) < INFINITY))
                             o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
                     }
                 }
+            };
+            if (s0 > 0 || s0 + cnt <= npg) {  // a shared tile: its state for the merge
+                float *part = a.partials + static_cast<size_t>(2 * cta + (segment > 0)) * kSlotFloats +
+                              r_tile * kPartialFloats;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[16];
+                    column(c, o);
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<uint4 *>(own + 32 * h + e) =
-                        make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    for (int e = 0; e < 16; e += 4)
+                        *reinterpret_cast<uint4 *>(part + 16 * c + e) =
+                            make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+                *reinterpret_cast<float4 *>(part + 64) = make_float4(x.m_ref, x.m_raw, x.l, x.l2);
+                *reinterpret_cast<float2 *>(part + 68) = make_float2(x.s1, x.s2);
+            } else {
+                float sq = 0.f, ne = 0.f, mag = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[16];
+                    column(c, o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        sq = fmaf(__uint_as_float(o[e]), __uint_as_float(o[e]), sq);
+                }
+                if (n > 0) {
+                    const float nf = static_cast<float>(n);
+                    mag = polar_magnitude(x.l, x.l2, x.m_raw, x.s1, x.s2,
+                                          a.ep.s * length_temperature(nf, a.ep.alpha, a.ep.L), nf,
+                                          a.ep.beta, a.ep.inv_ln_L, &ne);
+                }
+                const float inv = n > 0 ? 1.0f / fmaxf(sqrtf(sq), 1e-30f) : 0.f;
+                const int h = g * G + row % G;
+                const size_t out_row = (node0 + row / G) * a.Hq + h;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[16];
+                    column(c, o);
+                    if (row >= R) continue;
+                    uint32_t y[8];
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 uu = *reinterpret_cast<const float2 *>(a.u + h * kHeadDim +
+                                                                            16 * c + e);
+                        y[e >> 1] = n > 0 ? pack_bf16(fmaf(mag, uu.x, __uint_as_float(o[e]) * inv),
+                                                      fmaf(mag, uu.y, __uint_as_float(o[e + 1]) * inv))
+                                          : 0u;
+                    }
+                    uint4 *dst = reinterpret_cast<uint4 *>(a.out + out_row * kHeadDim + 16 * c);
+                    dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+                    dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+                }
+                if (row < R && a.neff) a.neff[out_row] = ne;
             }
-            if (!ok) x = RowStats{-INFINITY, -INFINITY, 0.f, 0.f, 0.f, 0.f};
-            *reinterpret_cast<float4 *>(own + 64) = make_float4(x.m_ref, x.m_raw, x.l, x.l2);
-            *reinterpret_cast<float2 *>(own + 68) = make_float2(x.s1, x.s2);
+            tc_fence_before();  // O is read before the next tile's first product
         }
-        tc_fence_before();
     }
     let_next_kernel_start();
+    tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (w == 5) tmem_dealloc_256(tmem);
+    if (w == 4) tmem_dealloc_128(tmem);
+}
 
-    // The cluster's states of a row: eight lanes merge them and finish the row.
-    const float *parts = reinterpret_cast<const float *>(ring);
-    const int nrows = min(kTileRows, R - row0), rank = static_cast<int>(cluster_rank());
-    if (C > 1) cluster_sync();
-    for (int r0 = w < 4 ? 4 * (w * C + rank) : nrows; r0 < nrows; r0 += 16 * C) {
-        const int r = min(r0 + (lane >> 3), nrows - 1);
-        const bool real = r0 + (lane >> 3) < nrows;
-        const RowState st = merge_parts(C, [&](int k) {
-            const float *p = parts + r * kPartialFloats;
-            return C > 1 ? cluster_map(p, k) : p;
-        });
-        const int t = (row0 + r) / G, h = g * G + (row0 + r) % G;
-        const size_t out_row = (static_cast<size_t>(seq) * a.tree + t) * a.Hq + h;
-        if (a.splits > 1)
-            store_part(st, a.partials + (out_row * a.splits + split) * kPartialFloats, real);
-        else
-            finish_row(st, len + __popcll(masks[t] & drafted), a.ep, a.u + h * kHeadDim,
-                       a.out + out_row * kHeadDim, a.neff ? a.neff + out_row : nullptr, real);
-    }
-    if (C > 1) cluster_sync();  // no CTA leaves while its states are read
+// Rows of the tiles that several CTAs share: block (CTA in which the tile begins,
+// sixteen rows); a row's parts go to four groups of eight lanes, whose states
+// are then joined.
+template <int G>
+__global__ void __launch_bounds__(32 * kMergeRows)
+tree_tc_merge_kernel(const TreeArgs a, const SharedTile *__restrict__ shared_tiles) {
+    __shared__ __align__(16) float parts[kMergeRows][4][kPartialFloats];
+    wait_for_previous_kernel();
+    const int cta = blockIdx.x;
+    const SharedTile t = shared_tiles[cta];
+    if (t.parts == 0) return;
+    const int nodes = tree_nodes(a.seqlens, a.tree_lens, t.seq, a.tree, a.max_pages);
+    const int r0 = kMergeRows * blockIdx.y, rows = G * nodes - t.row0;
+    if (r0 >= rows) return;
+    const int group = threadIdx.x >> 3, r = group % kMergeRows, share = group / kMergeRows;
+    const int row = min(r0 + r, kTileRows - 1);
+    const RowState x = merge_parts((t.parts - share + 3) / 4, [&](int k) {
+        const int j = 4 * k + share;
+        const size_t slot = j == 0 ? t.slot : 2 * (cta + j);
+        return a.partials + slot * kSlotFloats + row * kPartialFloats;
+    });
+    store_part(x, parts[r][share], true);
+    __syncthreads();
+    if (share > 0) return;  // whole warps
+    const int tile_row = t.row0 + r0 + r;
+    const bool real = r0 + r < min(rows, kTileRows);
+    const int node = min(tile_row / G, nodes - 1), h = t.head * G + tile_row % G;
+    const size_t at = static_cast<size_t>(t.seq) * a.tree + node;
+    const int n = a.seqlens[t.seq] + __popcll(a.mask[at] & first_tokens(nodes));
+    finish_row(merge_parts(4, [&](int k) { return parts[r][k]; }), n, a.ep, a.u + h * kHeadDim,
+               a.out + (at * a.Hq + h) * kHeadDim, a.neff ? a.neff + at * a.Hq + h : nullptr, real);
 }
 
 template <int G>
 cudaError_t launch_tc(const CUtensorMap &q, const CUtensorMap &kv, const CUtensorMap &k,
-                      const CUtensorMap &v, const TreeArgs &t, const TreePlan &plan, int num_seqs,
-                      cudaStream_t stream) {
+                      const CUtensorMap &v, const TreeArgs &t, int ctas, cudaStream_t stream) {
     static std::atomic<uint64_t> configured{0};  // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -427,21 +600,38 @@ cudaError_t launch_tc(const CUtensorMap &q, const CUtensorMap &kv, const CUtenso
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
-    return launch_ex(tree_tc_kernel<G>, dim3(plan.cluster * plan.splits * plan.row_tiles, t.Hkv,
-                                             num_seqs),
-                     kTcThreads, kSmemTc, plan.cluster, false, stream, q, kv, k, v, t);
+    // The workspace: the CTAs' shared tiles, then two slots of row states each.
+    SharedTile *tiles = reinterpret_cast<SharedTile *>(t.partials);
+    TreeArgs a = t;
+    a.partials = t.partials + tc_tiles_bytes(ctas) / sizeof(float);
+    e = launch_ex(tree_tc_kernel<G>, dim3(ctas), kTcThreads, kSmemTc, 1, false, stream, q, kv, k, v,
+                  a, tiles);
+    if (e != cudaSuccess) return e;
+    const int rows = std::min(G * t.tree, kTileRows);
+    return launch_ex(tree_tc_merge_kernel<G>, dim3(ctas, (rows + kMergeRows - 1) / kMergeRows), 32 * kMergeRows, 0, 1, true, stream, a,
+                     static_cast<const SharedTile *>(tiles));
 }
 
 }  // namespace
 
+int tree_tc_ctas(int num_seqs, int max_pages, int tree, int Hq, int Hkv) {
+    const long long tiles = static_cast<long long>(num_seqs) * Hkv *
+                            ((Hq / Hkv * tree + kTileRows - 1) / kTileRows);
+    const long long most = (tiles * (max_pages + 1ll) + kMinShare - 1) / kMinShare;
+    return static_cast<int>(std::min<long long>(148 * kTcPerSm, most));
+}
+
+size_t tree_tc_workspace_bytes(int ctas) {
+    return tc_tiles_bytes(ctas) + static_cast<size_t>(2 * ctas) * kSlotFloats * sizeof(float);
+}
+
 cudaError_t launch_tree_tc(const CUtensorMap &kv, const CUtensorMap &k, const CUtensorMap &v,
-                           const TreeArgs &t, const TreePlan &plan, int num_seqs,
-                           cudaStream_t stream) {
+                           const TreeArgs &t, int ctas, cudaStream_t stream) {
     CUtensorMap q;
     const int G = t.Hq / t.Hkv;
     // Query rows as (dim, head, node): a tile is the group's heads of 128 / G nodes.
     const uint64_t dims[3] = {static_cast<uint64_t>(kHeadDim), static_cast<uint64_t>(t.Hq),
-                              static_cast<uint64_t>(num_seqs) * t.tree};
+                              static_cast<uint64_t>(t.num_seqs) * t.tree};
     const uint64_t strides[2] = {kHeadDim * 2, static_cast<uint64_t>(t.Hq) * kHeadDim * 2};
     const uint32_t box[3] = {kHeadDim, static_cast<uint32_t>(G),
                              static_cast<uint32_t>(kTileRows / G)};
@@ -449,10 +639,10 @@ cudaError_t launch_tree_tc(const CUtensorMap &kv, const CUtensorMap &k, const CU
                      strides, box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     switch (G) {
-        case 1: return launch_tc<1>(q, kv, k, v, t, plan, num_seqs, stream);
-        case 2: return launch_tc<2>(q, kv, k, v, t, plan, num_seqs, stream);
-        case 4: return launch_tc<4>(q, kv, k, v, t, plan, num_seqs, stream);
-        case 8: return launch_tc<8>(q, kv, k, v, t, plan, num_seqs, stream);
+        case 1: return launch_tc<1>(q, kv, k, v, t, ctas, stream);
+        case 2: return launch_tc<2>(q, kv, k, v, t, ctas, stream);
+        case 4: return launch_tc<4>(q, kv, k, v, t, ctas, stream);
+        case 8: return launch_tc<8>(q, kv, k, v, t, ctas, stream);
         default: return cudaErrorInvalidValue;
     }
 }
