@@ -10,21 +10,25 @@
 // holds whole it finishes, of a tile it shares it stores the rows' states, which
 // tree_tc_merge_kernel joins (at most two such tiles a CTA: its first and last).
 //
-// Step.  S = Q K^T   tcgen05.mma M=128 N=64 K=64, operands in shared memory
-//        P, stats    one thread per row reads its scores from tensor memory 32
-//                    at a time, keeps max, l, l2, S1 and S2 in registers and
-//                    writes the weights back as bf16
-//        O += P V    tcgen05.mma M=128 N=64 K=64, P from tensor memory
-// P lies in S's columns, so a CTA's step is one chain, and 128 columns (S, O) and
-// two 16 KB stages are all it needs: four CTAs share an SM and cover each other's
-// waits.  What bounds the kernel is the exponentials (16 an SM and clock: 512
-// clocks a step of a full tile).
+// A step goes in two halves of 32 keys, in two buffers that take turns:
+//   S = Q K^T   tcgen05.mma M=128 N=32 K=64, operands in shared memory
+//   P, stats    one thread per row reads its scores from tensor memory, keeps
+//               max, l, l2, S1 and S2 in registers and writes the weights back
+//               as bf16 (P lies in its S's columns)
+//   O += P V    tcgen05.mma M=128 N=64 K=32, P from tensor memory
+// While the softmax warps work on one half, the other's product and the next
+// scores in its buffer are formed.  128 columns (S0 S1 O) and two 16 KB stages
+// are all a CTA needs: four share an SM.  What bounds the kernel is the
+// exponentials (16 an SM and clock: 512 clocks a step of a full tile).  Measured
+// on the widest tree (64 nodes, 8 sequences of 32K-64K): eight softmax warps a
+// CTA, two CTAs an SM and clusters of eight 330 us; one 64-key buffer, four CTAs
+// and equal shares 268 us; the two half buffers XXX us.
 //
 // The reference max of a row moves only when a logit exceeds it by more than
-// 2^8 (kRescaleThreshold), and then to a whole number of log2 units: weights are
-// formed against the one at hand in the pass that finds the scores' max, and only
-// where that was too low they are formed again, and O and the step's stored
-// weights multiplied by a power of two in tensor memory by the row's thread.
+// 2^8 (kRescaleThreshold): weights are formed against the one at hand in the pass
+// that finds the scores' max, and only where that was too low they are formed
+// again, and O rescaled in tensor memory by the row's thread once the product
+// before is done.
 #include <algorithm>
 #include <atomic>
 
@@ -154,7 +158,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *ring = smem + kQBytes;
-    __shared__ __align__(8) uint64_t q_full, full[kStagesTc], s_full, p_ready, pv_done, mma_done;
+    __shared__ __align__(8) uint64_t q_full, full[kStagesTc], s_full[2], p_ready[2], pv_done[2], mma_done;
     __shared__ unsigned long long odd_nodes;  // drafted nodes with values that are not finite
     __shared__ uint32_t tmem_base_sh;
     __shared__ long long wide[kTcThreads / 32];
@@ -165,9 +169,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
     if (threadIdx.x == 0) {
         mbar_init(&q_full, 1);
         for (int st = 0; st < kStagesTc; ++st) mbar_init(&full[st], 1);
-        mbar_init(&s_full, 1);
-        mbar_init(&p_ready, 4);
-        mbar_init(&pv_done, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&s_full[b], 1);
+            mbar_init(&p_ready[b], 4);
+            mbar_init(&pv_done[b], 1);
+        }
         mbar_init(&mma_done, 1);
         odd_nodes = 0;
         fence_barrier_init();
@@ -243,7 +249,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
     int it = 0;     // steps so far, for the barriers' phases
     if (w == 4) {
         // ------------------------------------------- copies and products
-        constexpr uint32_t idesc_qk = idesc_bf16(kTileRows, kPage, false);
+        constexpr uint32_t idesc_qk = idesc_bf16(kTileRows, kPage / 2, false);
         constexpr uint32_t idesc_pv = idesc_bf16(kTileRows, kHeadDim, true);
         // Q and K are K-major (SBO 1024), V is MN-major (one 64-column atom).
         const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
@@ -302,31 +308,40 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                 return __all_sync(~0u, mbar_wait(bar, parity, a.status)) != 0;
             };
             ok = wait(&q_full, tiles & 1);
-            for (int j = 0; j < n && ok; ++j, ++it) {
-                const int st = it % kStagesTc;
-                if (!(ok = wait(&full[st], (it / kStagesTc) & 1))) break;
+            // Scores of half h of step j: keys 32 h .. 32 h + 31 of its page.
+            auto scores = [&](int j, int h) {
+                const int st = (base + j) % kStagesTc;
+                if (h == 0 && !(ok = wait(&full[st], ((base + j) / kStagesTc) & 1))) return;
                 if (lane == 0) {
                     tc_fence_after();
-                    const uint32_t d = tmem + kColS, ka = k_lo + st * kStep;
+                    const uint32_t d = tmem + kColS + 32 * h, ka = k_lo + st * kStep + 256 * h;
                     mma_ss2<0>(d, q_lo, hi, ka, hi, idesc_qk);
                     mma_ss2<1>(d, q_lo + 2, hi, ka + 2, hi, idesc_qk);
                     mma_ss2<1>(d, q_lo + 4, hi, ka + 4, hi, idesc_qk);
                     mma_ss2<1>(d, q_lo + 6, hi, ka + 6, hi, idesc_qk);
-                    tc_commit(&s_full);
+                    tc_commit(&s_full[h]);
                 }
-                if (!(ok = wait(&p_ready, it & 1))) break;
-                if (lane == 0) {
-                    tc_fence_after();
-                    const uint32_t va = v_lo + st * kStep, pa = tmem + kColS, o = tmem + kColO;
-                    mma_ts2(o, pa, va, hi, idesc_pv, j > 0);
-                    mma_ts2(o, pa + 8, va + 128, hi, idesc_pv, 1u);
-                    mma_ts2(o, pa + 16, va + 256, hi, idesc_pv, 1u);
-                    mma_ts2(o, pa + 24, va + 384, hi, idesc_pv, 1u);
-                    tc_commit(&pv_done);
+            };
+            if (ok) scores(0, 0);
+            if (ok) scores(0, 1);
+            for (int j = 0; j < n && ok; ++j, ++it) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!(ok = wait(&p_ready[h], it & 1))) break;
+                    if (lane == 0) {
+                        tc_fence_after();
+                        const uint32_t va = v_lo + (it % kStagesTc) * kStep + 256 * h;
+                        const uint32_t pa = tmem + kColS + 32 * h, o = tmem + kColO;
+                        mma_ts2(o, pa, va, hi, idesc_pv, j > 0 || h > 0);
+                        mma_ts2(o, pa + 8, va + 128, hi, idesc_pv, 1u);
+                        tc_commit(&pv_done[h]);
+                    }
+                    // The buffer's next scores overwrite P, the next copy the stage.
+                    if (!(ok = wait(&pv_done[h], it & 1))) break;
+                    if (j + 1 < n) scores(j + 1, h);
+                    if (!ok) break;
                 }
-                // The next scores overwrite P, and the next copy this stage.
-                if (!(ok = wait(&pv_done, it & 1))) break;
-                if (loaded < n) load(loaded++);
+                if (ok && loaded < n) load(loaded++);
             }
             if (!ok)  // copies in flight land before shared memory is released
                 for (int st = 0; st < kStagesTc; ++st)
@@ -364,14 +379,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                     const int id = j + lane < cnt && p < npg ? pt[p] : 0;
                     bad = __ballot_sync(~0u, id < 0 || id >= a.num_pages);
                 }
-                ok = mbar_wait(&s_full, it & 1, a.status);
-                if (!__all_sync(~0u, ok)) { ok = false; break; }
-                tc_fence_after();
                 const bool draft = s0 + j == npg, skip = bad >> (j & 31) & 1u;
                 const int rest = len - (s0 + j) * kPage;  // cached tokens from this step on
                 const uint64_t mask = draft ? seen : skip ? 0ull : first_tokens(rest);
                 const bool whole = !draft && !skip && rest >= kPage;
                 if (!whole) {
+                    // (The copies have landed where the scores have.)
                     // Value rows that no row may see are zeroed, since a zero
                     // weight does not silence what is not finite; drafted
                     // values that are not finite are zeroed and added to the
@@ -409,9 +422,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                if (active) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    ok = mbar_wait(&s_full[h], it & 1, a.status);
+                    if (!__all_sync(~0u, ok)) { ok = false; break; }
+                    tc_fence_after();
+                    if (active) {
                         const uint32_t bits = static_cast<uint32_t>(mask >> (32 * h));
                         uint32_t sr[32], pk[16];
                         tmem_ld32(tS + 32 * h, sr);
@@ -424,13 +440,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                         const float zmax = t.top * cl2;
                         const bool need = zmax > x.m_ref + kRescaleThreshold;
                         if (__any_sync(~0u, need)) {
-                            // 0 where nothing was seen before; else a power of two.
-                            const float ref = ceilf(zmax);
-                            const float r = need ? exp2f(x.m_ref - ref) : 1.f;
+                            // 0 where nothing was seen before.
+                            const float r = need ? exp2f(x.m_ref - zmax) : 1.f;
                             x.l *= r;
                             x.l2 *= r * r;
-                            if (need) x.m_ref = ref;
-                            if (j > 0) {  // the product before is done: its P is overwritten here
+                            if (need) x.m_ref = zmax;
+                            if (j > 0 || h > 0) {  // O *= r, once the product before is done
+                                ok = mbar_wait(&pv_done[h ^ 1], (it + h + 1) & 1, a.status);
+                                if (!__all_sync(~0u, ok)) { ok = false; break; }
+                                tc_fence_after();
 #pragma unroll 1
                                 for (int c = 0; c < 4; ++c) {
                                     uint32_t o[16];
@@ -442,16 +460,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                                     tmem_st16(tO + 16 * c, o);
                                 }
                             }
-                            if (h == 1) {  // the step's first weights, exactly
-                                uint32_t o[16];
-                                tmem_ld16(tS, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    o[e] = pack_bf16(__uint_as_float(o[e] << 16) * r,
-                                                     __uint_as_float(o[e] & 0xffff0000u) * r);
-                                tmem_st16(tS, o);
-                            }
                             t = pass(x.m_ref == -INFINITY ? 0.f : x.m_ref);
                         }
                         x.m_raw = fmaxf(x.m_raw, t.top);
@@ -459,17 +467,18 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                         x.s2 += t.s2;
                         x.l += t.l;
                         x.l2 += t.l2;
-                        tmem_st16(tS + 16 * h, pk);
+                        tmem_st16(tS + 32 * h, pk);
+                        tmem_wait_st();
                     }
-                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_ready[h]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_ready);
+                if (!ok) break;
             }
             if (!ok) break;
             // The tile's last product.
-            ok = mbar_wait(&pv_done, (it - 1) & 1, a.status);
+            ok = mbar_wait(&pv_done[1], (it - 1) & 1, a.status);
             if (!__all_sync(~0u, ok)) { ok = false; break; }
             tc_fence_after();
             if (!active) continue;
