@@ -17,8 +17,8 @@
 //               as bf16 (P lies in its S's columns)
 //   O += P V    tcgen05.mma M=128 N=64 K=32, P from tensor memory
 // While the softmax warps work on one half, the other's product and the next
-// scores in its buffer are formed.  128 columns (S0 S1 O) and two 16 KB stages
-// are all a CTA needs: four share an SM.  What bounds the kernel is the
+// scores in its buffer are formed.  128 columns (S0 S1 O) and three 16 KB stages
+// are all a CTA needs: three share an SM.  What bounds the kernel is the
 // exponentials (16 an SM and clock: 512 clocks a step of a full tile).  Measured
 // on the widest tree (64 nodes, 8 sequences of 32K-64K): eight softmax warps a
 // CTA, two CTAs an SM and clusters of eight 330 us; one 64-key buffer, four CTAs
@@ -31,6 +31,7 @@
 // before is done.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "decode_tree.cuh"
 #include "polar_internal.h"
@@ -40,9 +41,9 @@ namespace polar {
 namespace {
 
 constexpr int kTileRows = 128;
-constexpr int kStagesTc = 2;
-constexpr int kTcThreads = 160;  // four softmax warps and one that copies and issues
-constexpr int kTcPerSm = 4;
+constexpr int kStagesTc = 3;
+constexpr int kTcThreads = 192;  // four softmax warps, one that copies, one that issues products
+constexpr int kTcPerSm = 3;
 constexpr int kQBytes = kTileRows * kHeadDim * 2;
 constexpr int kSmemTc = kQBytes + kStagesTc * kStageBytes + 1024;  // + alignment slack
 constexpr uint32_t kColS = 0, kColO = 64;
@@ -158,7 +159,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *ring = smem + kQBytes;
-    __shared__ __align__(8) uint64_t q_full, full[kStagesTc], s_full[2], p_ready[2], pv_done[2], mma_done;
+    __shared__ __align__(8) uint64_t q_full, q_empty, full[kStagesTc], empty[kStagesTc], s_full[2], p_ready[2], pv_done[2], mma_done;
     __shared__ unsigned long long odd_nodes;  // drafted nodes with values that are not finite
     __shared__ uint32_t tmem_base_sh;
     __shared__ long long wide[kTcThreads / 32];
@@ -168,7 +169,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
 
     if (threadIdx.x == 0) {
         mbar_init(&q_full, 1);
-        for (int st = 0; st < kStagesTc; ++st) mbar_init(&full[st], 1);
+        mbar_init(&q_empty, 1);
+        for (int st = 0; st < kStagesTc; ++st) {
+            mbar_init(&full[st], 1);
+            mbar_init(&empty[st], 1);
+        }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&s_full[b], 1);
             mbar_init(&p_ready[b], 4);
@@ -219,7 +224,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
         for (int i = 0; i < kTcThreads / 32; ++i) before += wide[i];
         if (before > first) break;  // uniform
     }
-    if (w == 4) tmem_alloc_128(&tmem_base_sh);
+    if (w == 5) tmem_alloc_128(&tmem_base_sh);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -248,106 +253,116 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
 
     int it = 0;     // steps so far, for the barriers' phases
     if (w == 4) {
-        // ------------------------------------------- copies and products
-        constexpr uint32_t idesc_qk = idesc_bf16(kTileRows, kPage / 2, false);
-        constexpr uint32_t idesc_pv = idesc_bf16(kTileRows, kHeadDim, true);
-        // Q and K are K-major (SBO 1024), V is MN-major (one 64-column atom).
-        const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
-        const uint32_t k_lo = sdesc_lo(smem_u32(ring), 16);
-        const uint32_t v_lo = sdesc_lo(smem_u32(ring) + kChunkBytes, 8192);
-        constexpr uint32_t hi = kSdescHi128B, kStep = kStageBytes >> 4;
+        // -------------------------------------------- copies (one thread)
         if (lane == 0) {
             tma_prefetch_desc(&q_map);
             tma_prefetch_desc(&kv_map);
-        }
-        bool ok = true;
-        int tiles = 0;
-        for (; ok && walk.left > 0; walk.next(), ++tiles) {
-            const int npg = walk.per_tile - 1, g = walk.head(), row0 = walk.row0();
-            const int s0 = walk.step, n = walk.count(), base = it;
-            const int32_t *pt = a.page_table + static_cast<size_t>(walk.seq) * a.max_pages;
-            // Page ids, 32 steps at a time, one stretch ahead (in turn in two
-            // registers).  A page id outside the pool is reported; its step
-            // reads page 0 and counts no key.
-            auto ids = [&](int j0) {
-                const int p = s0 + j0 + lane;
-                return j0 + lane < n && p < npg ? pt[p] : 0;
-            };
-            int even = ids(0), odd = ids(32);
-            auto load = [&](int j) {  // step j of this tile, by lane 0 with all lanes here
-                if (j > 0 && (j & 31) == 0) {
-                    if (j & 32) even = ids(j + 32); else odd = ids(j + 32);
-                }
-                int phys = __shfl_sync(~0u, j & 32 ? odd : even, j & 31);
-                if (lane != 0) return;
-                if (phys < 0 || phys >= a.num_pages) {
-                    record_error(a.status, POLAR_ERR_BAD_PAGE);
-                    phys = 0;
-                }
-                const int st = (base + j) % kStagesTc;
-                uint8_t *dst = ring + st * kStageBytes;
-                mbar_arrive_expect_tx(&full[st], kStageBytes);
-                if (s0 + j == npg) {
-                    tma_load_3d(dst, &k_map, 0, g, walk.seq * a.tree, &full[st]);
-                    tma_load_3d(dst + kChunkBytes, &v_map, 0, g, walk.seq * a.tree, &full[st]);
-                } else {
-                    const int at = (phys * 2 * a.Hkv + g) * kPage;  // K block of the kv head
-                    tma_load_2d(dst, &kv_map, 0, at, &full[st]);
-                    tma_load_2d(dst + kChunkBytes, &kv_map, 0, at + a.Hkv * kPage, &full[st]);
-                }
-            };
-            // The tile before is done with its queries and stages: its last
-            // product was waited for.
-            if (lane == 0) {
+            bool ok = true;
+            int tiles = 0;
+            for (; ok && walk.left > 0; walk.next(), ++tiles) {
+                const int npg = walk.per_tile - 1, g = walk.head(), s0 = walk.step;
+                const int n = walk.count();
+                const int32_t *pt = a.page_table + static_cast<size_t>(walk.seq) * a.max_pages + s0;
+                int id = s0 < npg ? pt[0] : 0;
+                // The queries, once the tile before has formed its last scores.
+                if (tiles > 0 && !(ok = mbar_wait(&q_empty, (tiles - 1) & 1, a.status))) break;
                 mbar_arrive_expect_tx(&q_full, kQBytes);
-                tma_load_3d(smem, &q_map, 0, g * G, walk.seq * a.tree + row0 / G, &q_full);
-            }
-            int loaded = 0;
-            for (; loaded < min(n, kStagesTc); ++loaded) load(loaded);
-            auto wait = [&](uint64_t *bar, int parity) {
-                return __all_sync(~0u, mbar_wait(bar, parity, a.status)) != 0;
-            };
-            ok = wait(&q_full, tiles & 1);
-            // Scores of half h of step j: keys 32 h .. 32 h + 31 of its page.
-            auto scores = [&](int j, int h) {
-                const int st = (base + j) % kStagesTc;
-                if (h == 0 && !(ok = wait(&full[st], ((base + j) / kStagesTc) & 1))) return;
-                if (lane == 0) {
-                    tc_fence_after();
-                    const uint32_t d = tmem + kColS + 32 * h, ka = k_lo + st * kStep + 256 * h;
-                    mma_ss2<0>(d, q_lo, hi, ka, hi, idesc_qk);
-                    mma_ss2<1>(d, q_lo + 2, hi, ka + 2, hi, idesc_qk);
-                    mma_ss2<1>(d, q_lo + 4, hi, ka + 4, hi, idesc_qk);
-                    mma_ss2<1>(d, q_lo + 6, hi, ka + 6, hi, idesc_qk);
-                    tc_commit(&s_full[h]);
-                }
-            };
-            if (ok) scores(0, 0);
-            if (ok) scores(0, 1);
-            for (int j = 0; j < n && ok; ++j, ++it) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!(ok = wait(&p_ready[h], it & 1))) break;
-                    if (lane == 0) {
-                        tc_fence_after();
-                        const uint32_t va = v_lo + (it % kStagesTc) * kStep + 256 * h;
-                        const uint32_t pa = tmem + kColS + 32 * h, o = tmem + kColO;
-                        mma_ts2(o, pa, va, hi, idesc_pv, j > 0 || h > 0);
-                        mma_ts2(o, pa + 8, va + 128, hi, idesc_pv, 1u);
-                        tc_commit(&pv_done[h]);
+                tma_load_3d(smem, &q_map, 0, g * G, walk.seq * a.tree + walk.row0() / G, &q_full);
+                for (int j = 0; j < n; ++j, ++it) {
+                    const int st = it % kStagesTc;
+                    int phys = id;
+                    id = j + 1 < n && s0 + j + 1 < npg ? pt[j + 1] : 0;
+                    // A page id outside the pool is reported; its step reads page
+                    // 0 and counts no key.
+                    if (phys < 0 || phys >= a.num_pages) {
+                        record_error(a.status, POLAR_ERR_BAD_PAGE);
+                        phys = 0;
                     }
-                    // The buffer's next scores overwrite P, the next copy the stage.
-                    if (!(ok = wait(&pv_done[h], it & 1))) break;
-                    if (j + 1 < n) scores(j + 1, h);
-                    if (!ok) break;
+                    if (it >= kStagesTc &&
+                        !(ok = mbar_wait(&empty[st], (it / kStagesTc - 1) & 1, a.status)))
+                        break;
+                    uint8_t *dst = ring + st * kStageBytes;
+                    mbar_arrive_expect_tx(&full[st], kStageBytes);
+                    if (s0 + j == npg) {
+                        tma_load_3d(dst, &k_map, 0, g, walk.seq * a.tree, &full[st]);
+                        tma_load_3d(dst + kChunkBytes, &v_map, 0, g, walk.seq * a.tree, &full[st]);
+                    } else {
+                        const int at = (phys * 2 * a.Hkv + g) * kPage;  // K block of the kv head
+                        tma_load_2d(dst, &kv_map, 0, at, &full[st]);
+                        tma_load_2d(dst + kChunkBytes, &kv_map, 0, at + a.Hkv * kPage, &full[st]);
+                    }
                 }
-                if (ok && loaded < n) load(loaded++);
             }
-            if (!ok)  // copies in flight land before shared memory is released
-                for (int st = 0; st < kStagesTc; ++st)
-                    for (int ph = 0; ph < 2; ++ph) mbar_wait(&full[st], ph, a.status);
+            // Every copy lands before shared memory is released.
+            if (tiles > 0 || !ok) mbar_wait(&q_full, (tiles - (ok ? 1 : 0)) & 1, a.status);
+            for (int j = max(0, it - kStagesTc); j < it; ++j)
+                mbar_wait(&full[j % kStagesTc], (j / kStagesTc) & 1, a.status);
         }
-        if (lane == 0) {  // all products complete before tensor memory is freed
+        __syncwarp();
+    } else if (w == 5) {
+        // ------------------------------------------- products (one thread)
+        if (lane == 0) {
+            constexpr uint32_t idesc_qk = idesc_bf16(kTileRows, kPage / 2, false);
+            constexpr uint32_t idesc_pv = idesc_bf16(kTileRows, kHeadDim, true);
+            // Q and K are K-major (SBO 1024), V is MN-major (one 64-column atom).
+            const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
+            const uint32_t k_lo = sdesc_lo(smem_u32(ring), 16);
+            const uint32_t v_lo = sdesc_lo(smem_u32(ring) + kChunkBytes, 8192);
+            constexpr uint32_t hi = kSdescHi128B, kStep = kStageBytes >> 4;
+            const uint32_t o = tmem + kColO;
+            bool ok = true;
+            int tiles = 0;
+            // Scores of half h of the step in stage st: its keys 32 h .. 32 h + 31.
+            auto scores = [&](int st, int h) {
+                const uint32_t d = tmem + kColS + 32 * h, ka = k_lo + st * kStep + 256 * h;
+                mma_ss2<0>(d, q_lo, hi, ka, hi, idesc_qk);
+                mma_ss2<1>(d, q_lo + 2, hi, ka + 2, hi, idesc_qk);
+                mma_ss2<1>(d, q_lo + 4, hi, ka + 4, hi, idesc_qk);
+                mma_ss2<1>(d, q_lo + 6, hi, ka + 6, hi, idesc_qk);
+                tc_commit(&s_full[h]);
+            };
+            int st = 0, phase = 0;  // stage and parity of step `it`
+            for (; ok && walk.left > 0; walk.next(), ++tiles) {
+                const int n = walk.count();
+                if (!(ok = mbar_wait(&q_full, tiles & 1, a.status))) break;
+                if (!(ok = mbar_wait(&full[st], phase, a.status))) break;
+                tc_fence_after();
+                scores(st, 0);
+                scores(st, 1);
+                if (n == 1) tc_commit(&q_empty);
+                for (int j = 0; j < n; ++j, ++it) {
+                    const int st1 = st + 1 == kStagesTc ? 0 : st + 1;
+                    const int phase1 = st1 == 0 ? phase ^ 1 : phase;
+                    const uint32_t va = v_lo + st * kStep;
+                    if (!(ok = mbar_wait(&p_ready[0], it & 1, a.status))) break;
+                    tc_fence_after();
+                    mma_ts2(o, tmem + kColS, va, hi, idesc_pv, j > 0);
+                    mma_ts2(o, tmem + kColS + 8, va + 128, hi, idesc_pv, 1u);
+                    tc_commit(&pv_done[0]);
+                    // A buffer's next scores overwrite its P.
+                    if (j + 1 < n) {
+                        if (!(ok = mbar_wait(&full[st1], phase1, a.status))) break;
+                        if (!(ok = mbar_wait(&pv_done[0], it & 1, a.status))) break;
+                        tc_fence_after();
+                        scores(st1, 0);
+                    }
+                    if (!(ok = mbar_wait(&p_ready[1], it & 1, a.status))) break;
+                    tc_fence_after();
+                    mma_ts2(o, tmem + kColS + 32, va + 256, hi, idesc_pv, 1u);
+                    mma_ts2(o, tmem + kColS + 40, va + 384, hi, idesc_pv, 1u);
+                    tc_commit(&pv_done[1]);
+                    tc_commit(&empty[st]);
+                    if (j + 1 < n) {
+                        if (!(ok = mbar_wait(&pv_done[1], it & 1, a.status))) break;
+                        tc_fence_after();
+                        scores(st1, 1);
+                        if (j + 2 == n) tc_commit(&q_empty);
+                    }
+                    st = st1;
+                    phase = phase1;
+                }
+            }
+            // All products complete before tensor memory is freed.
             tc_commit(&mma_done);
             mbar_wait(&mma_done, 0, a.status);
         }
@@ -372,109 +387,114 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                                                           a.ep.L) * kLog2e;
             const int32_t *pt = a.page_table + static_cast<size_t>(walk.seq) * a.max_pages;
             RowStats x{-INFINITY, -INFINITY, 0.f, 0.f, 0.f, 0.f};
-            uint32_t bad = 0;  // pages outside the pool, of 32 steps
-            for (int j = 0; j < cnt; ++j, ++it) {
-                if ((j & 31) == 0) {
-                    const int p = s0 + j + lane;
-                    const int id = j + lane < cnt && p < npg ? pt[p] : 0;
-                    bad = __ballot_sync(~0u, id < 0 || id >= a.num_pages);
+            // Half h of step `it` (the tile's first half: O holds nothing yet).
+            // kAll: every row sees all of its keys; else the bits of `mask`.
+            auto half_step = [&](auto kAll, int h, uint32_t mask, bool first) {
+                ok = mbar_wait(&s_full[h], it & 1, a.status);
+                if (!__all_sync(~0u, ok)) { ok = false; return; }
+                tc_fence_after();
+                if (active) {
+                    uint32_t pk[16];
+                    TileSums t;
+                    while (true) {
+                        uint32_t sr[32];
+                        tmem_ld32(tS + 32 * h, sr);
+                        tmem_wait_ld();
+                        const float ref = x.m_ref == -INFINITY ? 0.f : x.m_ref;
+                        t = tile_pass<decltype(kAll)::value>(sr, mask, cl2, ref, pk);
+                        const float zmax = t.top * cl2;
+                        const bool need = zmax > x.m_ref + kRescaleThreshold;
+                        if (!__any_sync(~0u, need)) break;
+                        // The reference was too low for some row: move it, rescale
+                        // what it holds (by 0 where nothing was seen before), and
+                        // form the weights again.
+                        const float r = need ? exp2f(x.m_ref - zmax) : 1.f;
+                        x.l *= r;
+                        x.l2 *= r * r;
+                        if (need) x.m_ref = zmax;
+                        if (first) continue;
+                        // O *= r, once the product before is done.
+                        ok = mbar_wait(&pv_done[h ^ 1], (it + h + 1) & 1, a.status);
+                        if (!__all_sync(~0u, ok)) { ok = false; return; }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + 16 * c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
+                            tmem_st16(tO + 16 * c, o);
+                        }
+                    }
+                    x.m_raw = fmaxf(x.m_raw, t.top);
+                    x.s1 += t.s1;
+                    x.s2 += t.s2;
+                    x.l += t.l;
+                    x.l2 += t.l2;
+                    tmem_st16(tS + 32 * h, pk);
+                    tmem_wait_st();
                 }
-                const bool draft = s0 + j == npg, skip = bad >> (j & 31) & 1u;
-                const int rest = len - (s0 + j) * kPage;  // cached tokens from this step on
-                const uint64_t mask = draft ? seen : skip ? 0ull : first_tokens(rest);
-                const bool whole = !draft && !skip && rest >= kPage;
-                if (!whole) {
-                    // (The copies have landed where the scores have.)
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[h]);
+            };
+            for (int j0 = 0; ok && j0 < cnt; j0 += 32) {
+                const int p = s0 + j0 + lane;
+                const int id = j0 + lane < cnt && p < npg ? pt[p] : 0;
+                const uint32_t bad = __ballot_sync(~0u, id < 0 || id >= a.num_pages);
+                const int j1 = min(j0 + 32, cnt), full_pages = len / kPage - s0;
+                for (int j = j0; ok && j < j1; ++j, ++it) {
+                    const bool skip = bad >> (j - j0) & 1u;  // a page outside the pool
+                    if (j < full_pages && !skip) {
+                        half_step(std::true_type{}, 0, ~0u, j == 0);
+                        if (ok) half_step(std::true_type{}, 1, ~0u, false);
+                        continue;
+                    }
+                    const bool draft = s0 + j == npg;
+                    const uint64_t mask =
+                        draft ? seen : skip ? 0ull : first_tokens(len - (s0 + j) * kPage);
                     // Value rows that no row may see are zeroed, since a zero
                     // weight does not silence what is not finite; drafted
                     // values that are not finite are zeroed and added to the
                     // rows that see them at the end.
                     const int st = it % kStagesTc;
-                    const bool landed = mbar_wait(&full[st], (it / kStagesTc) & 1, a.status);
+                    ok = mbar_wait(&full[st], (it / kStagesTc) & 1, a.status);
+                    if (!__all_sync(~0u, ok)) { ok = false; break; }
                     const uint64_t keep = draft ? drafted : mask;
                     uint32_t odd = 0;
-                    if (landed)
 #pragma unroll 1
-                        for (int e = 0; e < 4; ++e) {
-                            const int r = 16 * w + 4 * e + (lane >> 3);
-                            uint4 *v = reinterpret_cast<uint4 *>(ring + st * kStageBytes +
-                                                                 kChunkBytes + r * 128) + (lane & 7);
-                            if (!(keep >> r & 1)) {
-                                *v = make_uint4(0, 0, 0, 0);
-                            } else if (draft) {
-                                const uint4 y = *v;
-                                uint32_t word[4] = {y.x, y.y, y.z, y.w};
-                                bool found = false;
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = 16 * w + 4 * e + (lane >> 3);
+                        uint4 *v = reinterpret_cast<uint4 *>(ring + st * kStageBytes + kChunkBytes +
+                                                             r * 128) + (lane & 7);
+                        if (!(keep >> r & 1)) {
+                            *v = make_uint4(0, 0, 0, 0);
+                        } else if (draft) {
+                            const uint4 y = *v;
+                            uint32_t word[4] = {y.x, y.y, y.z, y.w};
+                            bool found = false;
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const bool lo = not_finite(word[k]);
-                                    const bool up = not_finite(word[k] >> 16);
-                                    found |= lo | up;
-                                    word[k] = mask_pair(word[k], !lo, !up);
-                                }
-                                if (found) {
-                                    *v = make_uint4(word[0], word[1], word[2], word[3]);
-                                    odd |= 1u << (4 * e + (lane >> 3));
-                                }
+                            for (int k = 0; k < 4; ++k) {
+                                const bool lo = not_finite(word[k]), up = not_finite(word[k] >> 16);
+                                found |= lo | up;
+                                word[k] = mask_pair(word[k], !lo, !up);
+                            }
+                            if (found) {
+                                *v = make_uint4(word[0], word[1], word[2], word[3]);
+                                odd |= 1u << (4 * e + (lane >> 3));
                             }
                         }
+                    }
                     if (odd) atomicOr(&odd_nodes, static_cast<unsigned long long>(odd) << (16 * w));
                     fence_proxy_async_smem();
                     __syncwarp();
-                }
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    ok = mbar_wait(&s_full[h], it & 1, a.status);
-                    if (!__all_sync(~0u, ok)) { ok = false; break; }
-                    tc_fence_after();
-                    if (active) {
-                        const uint32_t bits = static_cast<uint32_t>(mask >> (32 * h));
-                        uint32_t sr[32], pk[16];
-                        tmem_ld32(tS + 32 * h, sr);
-                        tmem_wait_ld();
-                        auto pass = [&](float ref) {
-                            return whole ? tile_pass<true>(sr, bits, cl2, ref, pk)
-                                         : tile_pass<false>(sr, bits, cl2, ref, pk);
-                        };
-                        TileSums t = pass(x.m_ref == -INFINITY ? 0.f : x.m_ref);
-                        const float zmax = t.top * cl2;
-                        const bool need = zmax > x.m_ref + kRescaleThreshold;
-                        if (__any_sync(~0u, need)) {
-                            // 0 where nothing was seen before.
-                            const float r = need ? exp2f(x.m_ref - zmax) : 1.f;
-                            x.l *= r;
-                            x.l2 *= r * r;
-                            if (need) x.m_ref = zmax;
-                            if (j > 0 || h > 0) {  // O *= r, once the product before is done
-                                ok = mbar_wait(&pv_done[h ^ 1], (it + h + 1) & 1, a.status);
-                                if (!__all_sync(~0u, ok)) { ok = false; break; }
-                                tc_fence_after();
-#pragma unroll 1
-                                for (int c = 0; c < 4; ++c) {
-                                    uint32_t o[16];
-                                    tmem_ld16(tO + 16 * c, o);
-                                    tmem_wait_ld();
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e)
-                                        o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
-                                    tmem_st16(tO + 16 * c, o);
-                                }
-                            }
-                            t = pass(x.m_ref == -INFINITY ? 0.f : x.m_ref);
-                        }
-                        x.m_raw = fmaxf(x.m_raw, t.top);
-                        x.s1 += t.s1;
-                        x.s2 += t.s2;
-                        x.l += t.l;
-                        x.l2 += t.l2;
-                        tmem_st16(tS + 32 * h, pk);
-                        tmem_wait_st();
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_ready[h]);
+                    for (int h = 0; ok && h < 2; ++h)
+                        half_step(std::false_type{}, h, static_cast<uint32_t>(mask >> (32 * h)),
+                                  j == 0 && h == 0);
                 }
-                if (!ok) break;
             }
             if (!ok) break;
             // The tile's last product.
@@ -559,7 +579,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (w == 4) tmem_dealloc_128(tmem);
+    if (w == 5) tmem_dealloc_128(tmem);
 }
 
 // Rows of the tiles that several CTAs share: block (CTA in which the tile begins,
