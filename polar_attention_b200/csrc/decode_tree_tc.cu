@@ -25,7 +25,7 @@
 // and equal shares 268 us; the two half buffers XXX us.
 //
 // The reference max of a row moves only when a logit exceeds it by more than
-// 2^8 (kRescaleThreshold): weights are formed against the one at hand in the pass
+// 2^24 (kTcThreshold): weights are formed against the one at hand in the pass
 // that finds the scores' max, and only where that was too low they are formed
 // again, and O rescaled in tensor memory by the row's thread once the product
 // before is done.
@@ -47,6 +47,10 @@ constexpr int kTcPerSm = 3;
 constexpr int kQBytes = kTileRows * kHeadDim * 2;
 constexpr int kSmemTc = kQBytes + kStagesTc * kStageBytes + 1024;  // + alignment slack
 constexpr uint32_t kColS = 0, kColO = 64;
+// How far (log2 units) a logit may exceed a row's reference before it moves: up
+// to 2^24 times 2^18 keys, squared, stays far inside fp32, and bf16 weights keep
+// their relative precision, so a row rarely moves it after its first keys.
+constexpr float kTcThreshold = 24.0f;
 constexpr int kSlotFloats = kTileRows * kPartialFloats;
 
 __device__ __forceinline__ void tmem_alloc_128(uint32_t *dst_smem) {
@@ -61,10 +65,10 @@ __device__ __forceinline__ void tmem_dealloc_128(uint32_t taddr) {
 
 // Steps that a share has at least.
 constexpr int kMinShare = 4;
-constexpr int kMergeRows = 16;  // rows of a merge block
+constexpr int kMergeThreads = 256;
 
 constexpr size_t tc_tiles_bytes(int ctas) {
-    return (static_cast<size_t>(ctas) * 5 * sizeof(int) + 15) / 16 * 16;
+    return (static_cast<size_t>(ctas) * 7 * sizeof(int) + 15) / 16 * 16;
 }
 
 // One pass over a thread's 32 scores against its reference max: the weights
@@ -106,6 +110,7 @@ struct RowStats {  // one row's streaming state, in its thread
 struct SharedTile {
     int seq, head, row0, parts;  // parts 0: none begins here
     int slot;                    // of the first part; part j > 0: slot 2 (cta + j)
+    int nodes, len;              // of the sequence
 };
 
 // A share of the steps, tile by tile.
@@ -128,6 +133,13 @@ struct Walk {
     }
     __device__ __forceinline__ int head() const { return tile / tiles_per_head(); }
     __device__ __forceinline__ int row0() const { return tile % tiles_per_head() * kTileRows; }
+    // First quarter of the 128 lanes that the tile's rows take.  A tile that does
+    // not fill them moves about with the tile's number: a quarter of the lanes
+    // belongs to one scheduler, and all four get their share of such tiles.
+    __device__ __forceinline__ int quarter() const {
+        const int used = (min(G * nodes - row0(), kTileRows) + 31) / 32;
+        return (seq + tile) % (5 - used);
+    }
     // Steps of the current tile in this share.
     __device__ __forceinline__ int count() const {
         return static_cast<int>(min(left, static_cast<long long>(per_tile - step)));
@@ -237,12 +249,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
     if (threadIdx.x == 0) {
         // The tile that begins here and goes on in the next shares, if any: the last.
         Walk<G> x = walk;
-        SharedTile t{0, 0, 0, 0, 2 * cta};
+        SharedTile t{0, 0, 0, 0, 2 * cta, 0, 0};
         long long done = 0;
         for (; x.left > 0; x.next()) {
             if (x.step == 0 && x.left < x.per_tile) {
                 const long long end = first + done + x.per_tile;  // the step behind the tile
                 t.seq = x.seq; t.head = x.head(); t.row0 = x.row0();
+                t.nodes = x.nodes; t.len = x.len;
                 t.parts = static_cast<int>((end - 1) / share) - cta + 1;
                 t.slot = 2 * cta + (done > 0);
             }
@@ -267,7 +280,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                 // The queries, once the tile before has formed its last scores.
                 if (tiles > 0 && !(ok = mbar_wait(&q_empty, (tiles - 1) & 1, a.status))) break;
                 mbar_arrive_expect_tx(&q_full, kQBytes);
-                tma_load_3d(smem, &q_map, 0, g * G, walk.seq * a.tree + walk.row0() / G, &q_full);
+                tma_load_3d(smem, &q_map, 0, g * G, 
+                            walk.seq * a.tree + (walk.row0() - 32 * walk.quarter()) / G, &q_full);
                 for (int j = 0; j < n; ++j, ++it) {
                     const int st = it % kStagesTc;
                     int phys = id;
@@ -369,20 +383,22 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
         __syncwarp();
     } else {
         // ------------------------------------------------- softmax warps
-        const int r_tile = static_cast<int>(threadIdx.x);  // row of the tile = lane of tensor memory
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * w) << 16);
         const uint32_t tS = lane_base + kColS, tO = lane_base + kColO;
         bool ok = true;
         int segment = 0;
         for (; ok && walk.left > 0; walk.next(), ++segment) {
-            const int npg = walk.per_tile - 1, g = walk.head(), row = walk.row0() + r_tile;
+            const int npg = walk.per_tile - 1, g = walk.head();
+            const int r_tile = static_cast<int>(threadIdx.x) - 32 * walk.quarter();  // may be none
+            const int row = walk.row0() + r_tile;
             const int s0 = walk.step, cnt = walk.count(), nodes = walk.nodes, len = walk.len;
             const int R = G * nodes;
-            const bool active = walk.row0() + 32 * w < R;  // the warp has a row at all
+            const bool real = r_tile >= 0 && row < R;
+            const bool active = __any_sync(~0u, real);  // the warp has a row at all
             const uint64_t drafted = first_tokens(nodes);
             const size_t node0 = static_cast<size_t>(walk.seq) * a.tree;
-            const uint64_t seen = row < R ? a.mask[node0 + row / G] & drafted : 0ull;
-            const int n = row < R ? len + __popcll(seen) : 0;
+            const uint64_t seen = real ? a.mask[node0 + row / G] & drafted : 0ull;
+            const int n = real ? len + __popcll(seen) : 0;
             const float cl2 = a.ep.s * length_temperature(static_cast<float>(n), a.ep.alpha,
                                                           a.ep.L) * kLog2e;
             const int32_t *pt = a.page_table + static_cast<size_t>(walk.seq) * a.max_pages;
@@ -403,7 +419,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                         const float ref = x.m_ref == -INFINITY ? 0.f : x.m_ref;
                         t = tile_pass<decltype(kAll)::value>(sr, mask, cl2, ref, pk);
                         const float zmax = t.top * cl2;
-                        const bool need = zmax > x.m_ref + kRescaleThreshold;
+                        const bool need = zmax > x.m_ref + kTcThreshold;
                         if (!__any_sync(~0u, need)) break;
                         // The reference was too low for some row: move it, rescale
                         // what it holds (by 0 where nothing was seen before), and
@@ -556,7 +572,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[16];
                     column(c, o);
-                    if (row >= R) continue;
+                    if (!real) continue;
                     uint32_t y[8];
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
@@ -570,7 +586,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                     dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
                     dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
                 }
-                if (row < R && a.neff) a.neff[out_row] = ne;
+                if (real && a.neff) a.neff[out_row] = ne;
             }
             tc_fence_before();  // O is read before the next tile's first product
         }
@@ -583,36 +599,41 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
 }
 
 // Rows of the tiles that several CTAs share: block (CTA in which the tile begins,
-// sixteen rows); a row's parts go to four groups of eight lanes, whose states
-// are then joined.
+// 32 rows), eight lanes a row.  A tile of many parts gives each row four groups
+// of eight lanes instead, whose states are then joined, and takes four rounds.
 template <int G>
-__global__ void __launch_bounds__(32 * kMergeRows)
+__global__ void __launch_bounds__(kMergeThreads)
 tree_tc_merge_kernel(const TreeArgs a, const SharedTile *__restrict__ shared_tiles) {
-    __shared__ __align__(16) float parts[kMergeRows][4][kPartialFloats];
+    constexpr int kGroups = kMergeThreads / 8;
+    __shared__ __align__(16) float joined[kGroups][kPartialFloats];
     wait_for_previous_kernel();
     const int cta = blockIdx.x;
     const SharedTile t = shared_tiles[cta];
-    if (t.parts == 0) return;
-    const int nodes = tree_nodes(a.seqlens, a.tree_lens, t.seq, a.tree, a.max_pages);
-    const int r0 = kMergeRows * blockIdx.y, rows = G * nodes - t.row0;
-    if (r0 >= rows) return;
-    const int group = threadIdx.x >> 3, r = group % kMergeRows, share = group / kMergeRows;
-    const int row = min(r0 + r, kTileRows - 1);
-    const RowState x = merge_parts((t.parts - share + 3) / 4, [&](int k) {
-        const int j = 4 * k + share;
-        const size_t slot = j == 0 ? t.slot : 2 * (cta + j);
-        return a.partials + slot * kSlotFloats + row * kPartialFloats;
-    });
-    store_part(x, parts[r][share], true);
-    __syncthreads();
-    if (share > 0) return;  // whole warps
-    const int tile_row = t.row0 + r0 + r;
-    const bool real = r0 + r < min(rows, kTileRows);
-    const int node = min(tile_row / G, nodes - 1), h = t.head * G + tile_row % G;
-    const size_t at = static_cast<size_t>(t.seq) * a.tree + node;
-    const int n = a.seqlens[t.seq] + __popcll(a.mask[at] & first_tokens(nodes));
-    finish_row(merge_parts(4, [&](int k) { return parts[r][k]; }), n, a.ep, a.u + h * kHeadDim,
-               a.out + (at * a.Hq + h) * kHeadDim, a.neff ? a.neff + at * a.Hq + h : nullptr, real);
+    const int rows = min(G * t.nodes - t.row0, kTileRows), r0 = kGroups * blockIdx.y;
+    if (t.parts == 0 || r0 >= rows) return;
+    const int shares = t.parts > 16 ? 4 : 1, per_round = kGroups / shares;
+    const int group = threadIdx.x >> 3, share = group / per_round;
+    for (int round = 0; round < shares; ++round) {
+        const int at = r0 + round * per_round;
+        if (at >= rows) break;
+        const int r = at + group % per_round, row = min(r, rows - 1);
+        const int node = (t.row0 + row) / G, h = t.head * G + (t.row0 + row) % G;
+        const size_t seq_node = static_cast<size_t>(t.seq) * a.tree + node;
+        const int n = t.len + __popcll(a.mask[seq_node] & first_tokens(t.nodes));
+        RowState x = merge_parts((t.parts - share + shares - 1) / shares, [&](int k) {
+            const int j = shares * k + share;
+            const size_t slot = j == 0 ? t.slot : 2 * (cta + j);
+            return a.partials + slot * kSlotFloats + row * kPartialFloats;
+        });
+        if (shares > 1) {
+            __syncthreads();  // the round before is read
+            store_part(x, joined[group], true);
+            __syncthreads();
+            x = merge_parts(shares, [&](int k) { return joined[group % per_round + k * per_round]; });
+        }
+        finish_row(x, n, a.ep, a.u + h * kHeadDim, a.out + (seq_node * a.Hq + h) * kHeadDim,
+                   a.neff ? a.neff + seq_node * a.Hq + h : nullptr, share == 0 && r < rows);
+    }
 }
 
 template <int G>
@@ -637,7 +658,8 @@ cudaError_t launch_tc(const CUtensorMap &q, const CUtensorMap &kv, const CUtenso
                   a, tiles);
     if (e != cudaSuccess) return e;
     const int rows = std::min(G * t.tree, kTileRows);
-    return launch_ex(tree_tc_merge_kernel<G>, dim3(ctas, (rows + kMergeRows - 1) / kMergeRows), 32 * kMergeRows, 0, 1, true, stream, a,
+    return launch_ex(tree_tc_merge_kernel<G>, dim3(ctas, (8 * rows + kMergeThreads - 1) / kMergeThreads), kMergeThreads, 0, 1,
+                     true, stream, a,
                      static_cast<const SharedTile *>(tiles));
 }
 
