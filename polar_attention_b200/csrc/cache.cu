@@ -42,34 +42,43 @@ __device__ __forceinline__ T block_scan(T x, T *scratch, T *total) {
 
 // ------------------------------------------------------------------ grow ---
 
-constexpr int kPlanRows = 1024;  // rows whose plan is held in shared memory
+constexpr int kPlanRows = 1024;   // rows whose plan is held in shared memory
+constexpr int kPlanFresh = 2048;  // and new pages
+constexpr int kFusedRows = 256;   // rows up to which one cluster plans and copies
+constexpr int kFusedCluster = 8;
 
 struct ReserveArgs {
     int32_t *refs, *table, *lens, *granted;
     const int32_t *grow;
-    int num_pages, max_pages, num_seqs;
+    uint4 *kv, *bounds;
+    int num_pages, max_pages, num_seqs, Hkv;
     // Workspace: per page the last growing row that writes it and how many do;
-    // the free pages found, in order; per row the running sum of pages taken
-    // and the page that it copies (-1: none), used past kPlanRows; the copies'
-    // source, destination (-1: none) and rows.
-    int *owner, *sharers, *fresh, *end, *copy, *copy_src, *copy_dst, *copy_rows;
+    // the free pages found, in order, used past kPlanFresh; per row the running
+    // sum of pages taken and the page that it copies (-1: none), used past
+    // kPlanRows; the copies.
+    int *owner, *sharers, *fresh, *end, *copy;
+    int3 *copies;    // source page, its copy, rows
+    int *num_copies;
     int *status;
 };
 
-// Plan of a growth step, one block.  Which rows copy their last page; how many
-// pages each row takes (a running sum over the rows); the lowest free ids (a
-// running count over the reference counts that stops once there are enough);
-// then every taken page finds its row by a search in the running sums.  What
-// bounds it is the chain of dependent loads, so the first stretch of reference
-// counts is on its way before the rows are looked at, and the passes over
-// shared pages run only where a last page is shared.
-__global__ void __launch_bounds__(kPlanThreads) cache_reserve_plan_kernel(const ReserveArgs a) {
+// Plan of a growth step, by a block's threads.  Which rows copy their last page;
+// how many pages each row takes (a running sum over the rows); the lowest free
+// ids (a running count over the reference counts that stops once there are
+// enough); then every taken page finds its row by a search in the running sums.
+// What bounds it is the chain of dependent loads, so the first stretch of
+// reference counts is on its way before the rows are looked at, rows and new
+// pages are held in shared memory, and the passes over shared pages run only
+// where a last page is shared.  copies/num_copies get the copies (num_copies is
+// in shared memory), in any order.
+__device__ __forceinline__ void reserve_plan(const ReserveArgs &a, int3 *copies, int *num_copies) {
     __shared__ int scratch[kPlanThreads / 32];
     __shared__ long long wide[kPlanThreads / 32];
-    __shared__ int s_end[kPlanRows], s_copy[kPlanRows];
+    __shared__ int s_end[kPlanRows], s_copy[kPlanRows], s_len[kPlanRows], s_fresh[kPlanFresh];
     const int tid = threadIdx.x, N = a.num_seqs;
     int *const end_of = N <= kPlanRows ? s_end : a.end;
     int *const copy_of = N <= kPlanRows ? s_copy : a.copy;
+    if (tid == 0) *num_copies = 0;
 
     constexpr int kPer = 16;
     int r[kPer];
@@ -161,10 +170,12 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_plan_kernel(const 
         if (i < N) {
             end_of[i] = static_cast<int>(min(end, 0x7fffffffll));
             copy_of[i] = copy;
+            if (N <= kPlanRows) s_len[i] = mine.len;
         }
     }
 
     const int wanted = static_cast<int>(min(asked, 0x7ffffffell));
+    int *const fresh = wanted <= kPlanFresh ? s_fresh : a.fresh;
     int found = 0;
     for (int p0 = 0; p0 < a.num_pages && found < wanted; p0 += kPlanThreads * kPer) {
         const int p = p0 + tid * kPer;
@@ -177,7 +188,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_plan_kernel(const 
 #pragma unroll
         for (int e = 0; e < kPer; ++e)
             if (r[e] == 0) {
-                if (at < wanted) a.fresh[at] = p + e;
+                if (at < wanted) fresh[at] = p + e;
                 ++at;
             }
         found += total;
@@ -194,17 +205,15 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_plan_kernel(const 
             if (end_of[mid] > k) hi = mid; else lo = mid + 1;
         }
         if (end_of[lo] > found) break;  // not served, nor any page after
-        const int j = k - (lo > 0 ? end_of[lo - 1] : 0), copy = copy_of[lo], id = a.fresh[k];
-        const int len = a.lens[lo];
-        const bool copies = copy >= 0 && j == 0;
-        const int c = copies ? len / kPage : pages_of(len) + j - (copy >= 0);
+        const int j = k - (lo > 0 ? end_of[lo - 1] : 0), copy = copy_of[lo], id = fresh[k];
+        const int len = N <= kPlanRows ? s_len[lo] : a.lens[lo];
+        const bool is_copy = copy >= 0 && j == 0;
+        const int c = is_copy ? len / kPage : pages_of(len) + j - (copy >= 0);
         a.table[static_cast<size_t>(lo) * a.max_pages + c] = id;
         a.refs[id] = 1;
-        if (copies) {
+        if (is_copy) {
             atomicSub(&a.refs[copy], 1);
-            a.copy_src[lo] = copy;
-            a.copy_dst[lo] = id;
-            a.copy_rows[lo] = len % kPage;
+            copies[atomicAdd(num_copies, 1)] = make_int3(copy, id, len % kPage);
         }
     }
     __syncthreads();  // the lengths above are the old ones
@@ -212,31 +221,57 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_plan_kernel(const 
         const int len = i == tid ? mine.len : a.lens[i], g = i == tid ? mine.g : a.grow[i];
         const int bad = i == tid ? mine.bad : row(i).bad;
         const bool served = !bad && end_of[i] <= found;
-        if (!served || copy_of[i] < 0) a.copy_dst[i] = -1;
         if (!served && !bad && g > 0) record_error(a.status, POLAR_ERR_NO_PAGES);
         a.granted[i] = served ? g : 0;
         if (served) a.lens[i] = len + g;
     }
 }
 
-// The copies of a growth step: block (row, K|V and head), the valid rows of
-// one 8 KB block; the first 2 * Hkv blocks of a row also copy the bounds.
-__global__ void __launch_bounds__(128)
-cache_reserve_copy_kernel(uint4 *kv, uint4 *bounds,
-                          const int *copy_src, const int *copy_dst, const int *copy_rows, int Hkv) {
-    const int i = blockIdx.x, blk = blockIdx.y;
-    wait_for_previous_kernel();
-    const int dst = copy_dst[i];
-    if (dst < 0) return;
-    const int src = copy_src[i], vecs = copy_rows[i] * kRowVecs;
+// One 8 KB block (K|V and head) of a copied page, by a warp: its valid rows, and
+// its share of the page's bounds.
+__device__ __forceinline__ void copy_block(uint4 *kv, uint4 *bounds, int3 c, int blk, int Hkv,
+                                           int lane) {
     const size_t step = static_cast<size_t>(2) * Hkv;
-    const uint4 *from = kv + (src * step + blk) * (kPage * kRowVecs);
-    uint4 *to = kv + (dst * step + blk) * (kPage * kRowVecs);
-#pragma unroll 4
-    for (int e = threadIdx.x; e < vecs; e += 128) to[e] = from[e];
-    if (bounds && threadIdx.x < kRowVecs)
-        bounds[(dst * step + blk) * kRowVecs + threadIdx.x] =
-            bounds[(src * step + blk) * kRowVecs + threadIdx.x];
+    const size_t src = c.x * step + blk, dst = c.y * step + blk;
+    const uint4 *from = kv + src * (kPage * kRowVecs);
+    uint4 *to = kv + dst * (kPage * kRowVecs);
+    const int vecs = c.z * kRowVecs;
+#pragma unroll 8
+    for (int e = lane; e < vecs; e += 32) to[e] = from[e];
+    if (bounds && lane < kRowVecs)
+        bounds[dst * kRowVecs + lane] = bounds[src * kRowVecs + lane];
+}
+
+// A growth step of few rows: one cluster, whose first block plans and hands the
+// copies to all.  One launch instead of two: what a step without copies, the
+// common one, spends is the launches (append step of 64 rows: XXX us less).
+__global__ void __launch_bounds__(kPlanThreads)
+cache_reserve_fused_kernel(const ReserveArgs a) {
+    __shared__ int3 copies[kFusedRows];
+    __shared__ int num_copies;
+    const int rank = static_cast<int>(cluster_rank());
+    if (rank == 0) reserve_plan(a, copies, &num_copies);
+    cluster_sync();
+    const int n = *cluster_map(&num_copies, 0), per = 2 * a.Hkv;
+    const int3 *list = cluster_map(copies, 0);
+    for (int u = rank * (kPlanThreads / 32) + (threadIdx.x >> 5); u < n * per;
+         u += kFusedCluster * (kPlanThreads / 32))
+        copy_block(a.kv, a.bounds, list[u / per], u % per, a.Hkv, threadIdx.x & 31);
+    cluster_sync();  // the first block stays while its list is read
+}
+
+__global__ void __launch_bounds__(kPlanThreads) cache_reserve_plan_kernel(const ReserveArgs a) {
+    __shared__ int num_copies;
+    reserve_plan(a, a.copies, &num_copies);
+    __syncthreads();
+    if (threadIdx.x == 0) *a.num_copies = num_copies;
+}
+
+__global__ void __launch_bounds__(128) cache_reserve_copy_kernel(const ReserveArgs a) {
+    wait_for_previous_kernel();
+    const int n = *a.num_copies, per = 2 * a.Hkv;
+    for (int u = blockIdx.x * 4 + (threadIdx.x >> 5); u < n * per; u += gridDim.x * 4)
+        copy_block(a.kv, a.bounds, a.copies[u / per], u % per, a.Hkv, threadIdx.x & 31);
 }
 
 // ---------------------------------------------------------------- append ---
@@ -553,17 +588,22 @@ cudaError_t launch_cache_reserve(const CacheLaunch &a, const int32_t *grow, int3
     r.owner = ws; r.sharers = ws + a.num_pages; r.fresh = ws + 2 * static_cast<size_t>(a.num_pages);
     const size_t n = a.num_seqs;
     int *rows = ws + 3 * static_cast<size_t>(a.num_pages);
-    r.end = rows; r.copy = rows + n; r.copy_src = rows + 2 * n; r.copy_dst = rows + 3 * n;
-    r.copy_rows = rows + 4 * n;
+    r.end = rows; r.copy = rows + n;
+    r.copies = reinterpret_cast<int3 *>(rows + 2 * n);
+    r.num_copies = rows + 5 * n;
+    r.kv = static_cast<uint4 *>(a.kv); r.bounds = static_cast<uint4 *>(a.bounds); r.Hkv = a.Hkv;
     r.status = a.status;
+    if (a.num_seqs <= kFusedRows) {
+        count_launches(1);
+        return launch_ex(cache_reserve_fused_kernel, dim3(kFusedCluster), kPlanThreads, 0,
+                         kFusedCluster, false, a.stream, r);
+    }
     cache_reserve_plan_kernel<<<1, kPlanThreads, 0, a.stream>>>(r);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     count_launches(2);
-    return launch_ex(cache_reserve_copy_kernel, dim3(a.num_seqs, 2 * a.Hkv), 128, 0, 1, true,
-                     a.stream, static_cast<uint4 *>(a.kv), static_cast<uint4 *>(a.bounds),
-                     static_cast<const int *>(r.copy_src), static_cast<const int *>(r.copy_dst),
-                     static_cast<const int *>(r.copy_rows), a.Hkv);
+    return launch_ex(cache_reserve_copy_kernel, dim3(std::min(a.num_seqs, 148 * 8)), 128, 0, 1, true,
+                     a.stream, r);
 }
 
 cudaError_t launch_cache_append(const CacheLaunch &a, const void *k, const void *v, int src_tokens,

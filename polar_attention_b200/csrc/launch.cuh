@@ -23,10 +23,11 @@ __device__ __forceinline__ void cluster_sync() {
                      : "memory");
 }
 // The same shared-memory address in the cluster's CTA `rank` (generic).
-__device__ __forceinline__ const float *cluster_map(const float *p, uint32_t rank) {
+template <typename T>
+__device__ __forceinline__ const T *cluster_map(const T *p, uint32_t rank) {
     uint64_t r;
     asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
-    return reinterpret_cast<const float *>(r);
+    return reinterpret_cast<const T *>(r);
 }
 // Programmatic dependent launch: waits until the kernels before this one on the
 // stream are done and their writes visible (nothing to wait for otherwise).

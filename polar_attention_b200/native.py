@@ -582,31 +582,27 @@ class _Scope:
             c.__exit__(*exc)
 
 
-def _need(name, t, dtype, shape, like):
+def _need(name, t, dtype, shape, dev):
     """t's address, once it is a contiguous tensor of this type and shape on the
-    device of `like`."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() \
-            and t.get_device() == like.get_device():
+    CUDA device of this index."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
         return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != like.device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on {like.device}")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on cuda:{dev}, the others' device")
     raise ValueError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
 
 
-def _need_or_none(name, t, dtype, shape, like):
-    return None if t is None else _need(name, t, dtype, shape, like)
-
-
-def _scratch(workspace, need, like):
-    """The workspace, its address and its size; a fresh one of need() bytes where
+def _scratch(workspace, need, dev):
+    """The workspace, its address and its size; a fresh one of `need` bytes where
     the caller gave none."""
     if workspace is None:
-        workspace = torch.empty(max(need(), 16), device=like.device, dtype=torch.uint8)
-        return workspace, workspace.data_ptr(), workspace.numel()
-    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+        need = max(need, 16)
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+        return workspace, workspace.data_ptr(), need
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -636,24 +632,25 @@ def decode_paged_tree(q, k, v, tree_mask, kv_pages, page_table, seqlens, u, out=
     P_, Hkv = _pool_shape(kv_pages, D)
     bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     max_pages = page_table.shape[1]
+    dev = q.get_device()
     with _Scope(q, stream) as st:
-        ptr = (_need("q", q, bf16, (N, M, Hq, D), q), _need("k", k, bf16, (N, M, Hkv, D), q),
-               _need("v", v, bf16, (N, M, Hkv, D), q),
-               _need("tree_mask", tree_mask, torch.int64, (N, M), q),
-               _need_or_none("tree_lens", tree_lens, i32, (N,), q), M,
-               _need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, D), q), P_,
-               _need("page_table", page_table, i32, (N, max_pages), q), max_pages,
-               _need("seqlens", seqlens, i32, (N,), q), N, _need("u", u, f32, (Hq, D), q))
+        ptr = (_need("q", q, bf16, (N, M, Hq, D), dev), _need("k", k, bf16, (N, M, Hkv, D), dev),
+               _need("v", v, bf16, (N, M, Hkv, D), dev),
+               _need("tree_mask", tree_mask, torch.int64, (N, M), dev),
+               None if tree_lens is None else _need("tree_lens", tree_lens, i32, (N,), dev), M,
+               _need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, D), dev), P_,
+               _need("page_table", page_table, i32, (N, max_pages), dev), max_pages,
+               _need("seqlens", seqlens, i32, (N,), dev), N, _need("u", u, f32, (Hq, D), dev))
         _, pp = _decode_params(Hq, Hkv, D, POLAR_BF16, s, alpha, L, beta)
         if out is None:
             out = torch.empty_like(q)
         if neff is None and want_neff:
-            neff = torch.empty((N, M, Hq), device=q.device, dtype=f32)
+            neff = torch.empty((N, M, Hq), device=dev, dtype=f32)
         workspace, wp, wb = _scratch(
-            workspace, lambda: decode_tree_workspace_size(N, max_pages, M, Hq, Hkv), q)
+            workspace, decode_tree_workspace_size(N, max_pages, M, Hq, Hkv), dev)
         _check(lib().polar_attn_decode_paged_tree(
-            *ptr, pp, _need("out", out, bf16, (N, M, Hq, D), q),
-            _need_or_none("neff", neff, f32, (N, M, Hq), q), wp, wb, st),
+            *ptr, pp, _need("out", out, bf16, (N, M, Hq, D), dev),
+            None if neff is None else _need("neff", neff, f32, (N, M, Hq), dev), wp, wb, st),
             "polar_attn_decode_paged_tree")
     return out, neff
 
@@ -678,26 +675,27 @@ def decode_paged_sparse(q, kv_pages, bounds, page_table, seqlens, u, keep, out=N
     keep = int(keep)
     bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     max_pages = page_table.shape[1]
+    dev = q.get_device()
     with _Scope(q, stream) as st:
-        ptr = (_need("q", q, bf16, (N, Hq, D), q),
-               _need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, D), q),
-               _need("bounds", bounds, bf16, (P_, Hkv, 2, D), q), P_,
-               _need("page_table", page_table, i32, (N, max_pages), q), max_pages,
-               _need("seqlens", seqlens, i32, (N,), q), N, keep,
-               _need("u", u, f32, (Hq, D), q))
+        ptr = (_need("q", q, bf16, (N, Hq, D), dev),
+               _need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, D), dev),
+               _need("bounds", bounds, bf16, (P_, Hkv, 2, D), dev), P_,
+               _need("page_table", page_table, i32, (N, max_pages), dev), max_pages,
+               _need("seqlens", seqlens, i32, (N,), dev), N, keep,
+               _need("u", u, f32, (Hq, D), dev))
         _, pp = _decode_params(Hq, Hkv, D, POLAR_BF16, s, alpha, L, beta)
         if out is None:
             out = torch.empty_like(q)
         if neff is None and want_neff:
-            neff = torch.empty((N, Hq), device=q.device, dtype=f32)
+            neff = torch.empty((N, Hq), device=dev, dtype=f32)
         if selected is None and want_selected:
-            selected = torch.empty((N, Hkv, max(keep, 0)), device=q.device, dtype=i32)
+            selected = torch.empty((N, Hkv, max(keep, 0)), device=dev, dtype=i32)
         workspace, wp, wb = _scratch(
-            workspace, lambda: decode_sparse_workspace_size(N, max_pages, keep, Hq, Hkv), q)
+            workspace, decode_sparse_workspace_size(N, max_pages, keep, Hq, Hkv), dev)
         _check(lib().polar_attn_decode_paged_sparse(
-            *ptr, pp, _need("out", out, bf16, (N, Hq, D), q),
-            _need_or_none("neff", neff, f32, (N, Hq), q),
-            _need_or_none("selected", selected, i32, (N, Hkv, keep), q), wp, wb, st),
+            *ptr, pp, _need("out", out, bf16, (N, Hq, D), dev),
+            None if neff is None else _need("neff", neff, f32, (N, Hq), dev),
+            None if selected is None else _need("selected", selected, i32, (N, Hkv, keep), dev), wp, wb, st),
             "polar_attn_decode_paged_sparse")
     return out, neff, selected
 
@@ -708,28 +706,34 @@ class PageCache:
     caller with an allocator of its own, who then only appends) and the pages'
     key bounds [P,Hkv,2,64] bf16 (None: not kept).  Holds the tensors; page
     tables and lengths are arguments of each call."""
-    __slots__ = ("kv_pages", "refs", "bounds", "_c", "_p")
+    __slots__ = ("kv_pages", "refs", "bounds", "_c", "_p", "_dev")
 
     def __init__(self, kv_pages, refs=None, bounds=None):
         P_, Hkv = _pool_shape(kv_pages, 64)
-        dev, bf16 = kv_pages, torch.bfloat16
-        if not kv_pages.is_cuda:
+        dev, bf16 = kv_pages.get_device(), torch.bfloat16
+        if dev < 0:
             raise ValueError("inputs must be contiguous CUDA tensors")
         self.kv_pages, self.refs, self.bounds = kv_pages, refs, bounds
         self._c = Cache(_need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, 64), dev),
-                        _need_or_none("bounds", bounds, bf16, (P_, Hkv, 2, 64), dev),
-                        _need_or_none("refs", refs, torch.int32, (P_,), dev), P_, Hkv, 64,
+                        None if bounds is None else _need("bounds", bounds, bf16, (P_, Hkv, 2, 64), dev),
+                        None if refs is None else _need("refs", refs, torch.int32, (P_,), dev), P_, Hkv, 64,
                         POLAR_BF16)
-        self._p = ctypes.pointer(self._c)
+        self._p, self._dev = ctypes.pointer(self._c), dev
+
+
+@functools.lru_cache(maxsize=256)
+def _cache_workspace(num_pages, Hkv, num_seqs):
+    c = Cache(None, None, None, num_pages, Hkv, 64, POLAR_BF16)
+    return int(lib().polar_attn_cache_workspace_size(ctypes.byref(c), num_seqs))
 
 
 def cache_workspace_size(cache: PageCache, num_seqs: int) -> int:
-    return int(lib().polar_attn_cache_workspace_size(cache._p, num_seqs))
+    return _cache_workspace(cache._c.num_pages, cache._c.Hkv, num_seqs)
 
 
 def _rows(cache, page_table, seqlens):
     """(addresses and sizes of a page table and its lengths), rows, pages a row."""
-    dev, i32 = cache.kv_pages, torch.int32
+    dev, i32 = cache._dev, torch.int32
     N, max_pages = page_table.shape
     return (_need("page_table", page_table, i32, (N, max_pages), dev),
             _need("seqlens", seqlens, i32, (N,), dev), N, max_pages)
@@ -741,13 +745,13 @@ def cache_reserve(cache: PageCache, page_table, seqlens, grow, granted=None, wor
     copies a shared last page) and grows page_table [N,max_pages] and seqlens
     [N] (int32) in place.  Returns granted [N] int32: grow, or 0 from the first
     row on that the pool cannot serve."""
-    dev, i32 = cache.kv_pages, torch.int32
+    dev, i32 = cache._dev, torch.int32
     with _Scope(cache.kv_pages, stream) as st:
         table, lens, N, max_pages = _rows(cache, page_table, seqlens)
         g = _need("grow", grow, i32, (N,), dev)
         if granted is None:
             granted = torch.empty_like(grow)
-        workspace, wp, wb = _scratch(workspace, lambda: cache_workspace_size(cache, N), dev)
+        workspace, wp, wb = _scratch(workspace, _cache_workspace(cache._c.num_pages, cache._c.Hkv, N), dev)
         _check(lib().polar_attn_cache_reserve(cache._p, table, max_pages, lens, g, N,
                                               _need("granted", granted, i32, (N,), dev), wp, wb,
                                               st), "polar_attn_cache_reserve")
@@ -759,7 +763,7 @@ def cache_append(cache: PageCache, k, v, page_table, seqlens, counts=None, pick=
     """Writes the newest tokens of each row: token t < counts[n] (None: all) of
     row n, from k, v [N,T,Hkv,64] row t (pick [N,C] int32: row pick[n,t]), to
     position seqlens[n] - counts[n] + t; the touched pages' bounds are kept."""
-    dev, bf16, i32 = cache.kv_pages, torch.bfloat16, torch.int32
+    dev, bf16, i32 = cache._dev, torch.bfloat16, torch.int32
     with _Scope(cache.kv_pages, stream) as st:
         table, lens, N, max_pages = _rows(cache, page_table, seqlens)
         if k.dim() != 4:
@@ -769,8 +773,8 @@ def cache_append(cache: PageCache, k, v, page_table, seqlens, counts=None, pick=
         _check(lib().polar_attn_cache_append(
             cache._p, _need("k", k, bf16, (N, T, Hkv, 64), dev),
             _need("v", v, bf16, (N, T, Hkv, 64), dev), T,
-            _need_or_none("pick", pick, i32, (N, C), dev), C,
-            _need_or_none("counts", counts, i32, (N,), dev), table, max_pages, lens, N, st),
+            None if pick is None else _need("pick", pick, i32, (N, C), dev), C,
+            None if counts is None else _need("counts", counts, i32, (N,), dev), table, max_pages, lens, N, st),
             "polar_attn_cache_append")
 
 
@@ -779,7 +783,7 @@ def cache_fork(cache: PageCache, src_table, src_lens, src_rows, dst_table, dst_l
     """Row i of dst_table, dst_lens becomes a copy of row src_rows[i] (int32) of
     src_table, src_lens that shares its pages; a negative source leaves the row
     alone.  The two tables may not overlap."""
-    dev, i32 = cache.kv_pages, torch.int32
+    dev, i32 = cache._dev, torch.int32
     with _Scope(cache.kv_pages, stream) as st:
         src, slens, S, width = _rows(cache, src_table, src_lens)
         dst, dlens, N, max_pages = _rows(cache, dst_table, dst_lens)
@@ -793,12 +797,12 @@ def cache_fork(cache: PageCache, src_table, src_lens, src_rows, dst_table, dst_l
 def cache_free(cache: PageCache, page_table, seqlens, keep=None, *, stream=None):
     """Cuts each row to its first keep [N] int32 tokens (None: none; negative:
     the row is left alone) and gives the pages behind them back, in place."""
-    dev = cache.kv_pages
+    dev = cache._dev
     with _Scope(cache.kv_pages, stream) as st:
         table, lens, N, max_pages = _rows(cache, page_table, seqlens)
         _check(lib().polar_attn_cache_free(
             cache._p, table, max_pages, lens,
-            _need_or_none("keep", keep, torch.int32, (N,), dev), N, st), "polar_attn_cache_free")
+            None if keep is None else _need("keep", keep, torch.int32, (N,), dev), N, st), "polar_attn_cache_free")
 
 
 def cache_compact(cache: PageCache, page_table, seqlens, used=None, workspace=None, *,
@@ -806,12 +810,12 @@ def cache_compact(cache: PageCache, page_table, seqlens, used=None, workspace=No
     """Moves the live pages to the front of the pool and rewrites page_table (all
     rows that name pages of this pool) in place.  Returns used [1] int32: the
     number of live pages, which are pages 0 .. used - 1 afterwards."""
-    dev, i32 = cache.kv_pages, torch.int32
+    dev, i32 = cache._dev, torch.int32
     with _Scope(cache.kv_pages, stream) as st:
         table, lens, N, max_pages = _rows(cache, page_table, seqlens)
         if used is None:
-            used = torch.empty(1, device=dev.device, dtype=i32)
-        workspace, wp, wb = _scratch(workspace, lambda: cache_workspace_size(cache, N), dev)
+            used = torch.empty(1, device=dev, dtype=i32)
+        workspace, wp, wb = _scratch(workspace, _cache_workspace(cache._c.num_pages, cache._c.Hkv, N), dev)
         _check(lib().polar_attn_cache_compact(cache._p, table, max_pages, lens, N,
                                               _need("used", used, i32, (1,), dev), wp, wb, st),
                "polar_attn_cache_compact")

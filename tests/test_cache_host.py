@@ -72,7 +72,7 @@ def test_group_sizes(lib, call):
     ({"v": MIS}, INVALID), ({"mask": 0x100004}, INVALID), ({"lens": MIS4}, INVALID),
     ({"kv": MIS}, INVALID), ({"pt": MIS4}, INVALID), ({"sl": MIS4}, INVALID), ({"u": MIS}, INVALID),
     ({"out": MIS}, INVALID), ({"neff": MIS4}, INVALID), ({"ws": MIS}, INVALID),
-    ({"wb": 100}, WORKSPACE), ({"n": 0, "q": None}, OK)])
+    ({"wb": 8}, WORKSPACE), ({"n": 0, "q": None}, OK)])
 def test_tree(lib, kw, code):
     assert tree(lib, **kw) == code
 
