@@ -236,8 +236,15 @@ __device__ __forceinline__ void copy_block(uint4 *kv, uint4 *bounds, int3 c, int
     const uint4 *from = kv + src * (kPage * kRowVecs);
     uint4 *to = kv + dst * (kPage * kRowVecs);
     const int vecs = c.z * kRowVecs;
-#pragma unroll 8
-    for (int e = lane; e < vecs; e += 32) to[e] = from[e];
+    for (int e0 = lane; e0 < vecs; e0 += 32 * 8) {
+        uint4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (e0 + 32 * k < vecs) x[k] = from[e0 + 32 * k];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (e0 + 32 * k < vecs) to[e0 + 32 * k] = x[k];
+    }
     if (bounds && lane < kRowVecs)
         bounds[dst * kRowVecs + lane] = bounds[src * kRowVecs + lane];
 }
@@ -305,21 +312,21 @@ __device__ __forceinline__ uint4 shfl8(uint4 a, int o) {
                       __shfl_xor_sync(0xffffffffu, a.z, o), __shfl_xor_sync(0xffffffffu, a.w, o));
 }
 
-// Block (touched page of the row, kv head, row): thread (row r0 of 16, vector
-// c of 8) moves rows r0, r0 + 16, ... of the page.  Rows before the first new
-// token are read back where the bounds need them.
+// Block (touched page of the row and kv head, row): thread (row r0 of 16, vector
+// c of 8) moves rows r0, r0 + 16, ... of the page.  The heads of a page are
+// neighbours, since a token's rows of all heads lie together in k and v.  Rows
+// before the first new token are read back where the bounds need them.
 __global__ void __launch_bounds__(128) cache_append_kernel(const AppendArgs a) {
     __shared__ uint4 part[2][4][kRowVecs];
-    const int i = blockIdx.z, g = blockIdx.y;
+    const int i = blockIdx.y, g = blockIdx.x % a.Hkv, touched = blockIdx.x / a.Hkv;
     const int len = a.lens[i], cnt = a.counts ? a.counts[i] : a.tokens;
     if (cnt < 0 || cnt > a.tokens || len < cnt ||
         len > static_cast<long long>(a.max_pages) * kPage) {
-        if (blockIdx.x == 0 && g == 0 && threadIdx.x == 0)
-            record_error(a.status, POLAR_ERR_BAD_SEQLEN);
+        if (blockIdx.x == 0 && threadIdx.x == 0) record_error(a.status, POLAR_ERR_BAD_SEQLEN);
         return;
     }
     const int first = len - cnt;  // position of the first new token
-    const int lp = first / kPage + blockIdx.x;
+    const int lp = first / kPage + touched;
     if (cnt == 0 || lp >= pages_of(len)) return;
     const int page = a.table[static_cast<size_t>(i) * a.max_pages + lp];
     if (page < 0 || page >= a.num_pages || (a.refs && a.refs[page] != 1)) {
@@ -529,23 +536,38 @@ __global__ void __launch_bounds__(256) cache_compact_plan_kernel(const CompactAr
     }
 }
 
-// Copies the movers' blocks (8 KB units), then rewrites references and tables.
+// Copies the movers' pages, laid end to end, 32 KB at a time (eight vectors a
+// thread in flight), then rewrites references and tables.
 __global__ void __launch_bounds__(256) cache_compact_move_kernel(const CompactArgs a) {
     const int moves = a.head[0];
-    const int per = 2 * a.Hkv;  // 8 KB blocks of a page
-    const long long units = static_cast<long long>(moves) * per;
-    for (long long unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int k = static_cast<int>(unit / per), blk = static_cast<int>(unit % per);
-        const size_t s = static_cast<size_t>(a.src[k]) * per + blk;
-        const size_t d = static_cast<size_t>(a.dst[k]) * per + blk;
-        const uint4 *from = a.kv + s * (kPage * kRowVecs) + threadIdx.x;
-        uint4 *to = a.kv + d * (kPage * kRowVecs) + threadIdx.x;
-        const uint4 x = __ldg(from), y = __ldg(from + 256);
-        to[0] = x;
-        to[256] = y;
-        if (a.bounds && threadIdx.x < kRowVecs)
-            a.bounds[d * kRowVecs + threadIdx.x] = a.bounds[s * kRowVecs + threadIdx.x];
-        if (blk == 0 && threadIdx.x == 0) {
+    const int page_vecs = 2 * a.Hkv * kPage * kRowVecs;  // a multiple of 1024
+    const long long vecs = static_cast<long long>(moves) * page_vecs;
+    for (long long v0 = static_cast<long long>(blockIdx.x) * 2048; v0 < vecs;
+         v0 += static_cast<long long>(gridDim.x) * 2048) {
+        uint4 x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {  // the 256 threads' vectors lie in one page
+            const long long v = v0 + 256 * e;
+            if (v < vecs)
+                x[e] = __ldcs(a.kv + static_cast<size_t>(a.src[v / page_vecs]) * page_vecs +
+                              v % page_vecs + threadIdx.x);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const long long v = v0 + 256 * e;
+            if (v < vecs)
+                __stcs(a.kv + static_cast<size_t>(a.dst[v / page_vecs]) * page_vecs + v % page_vecs +
+                           threadIdx.x, x[e]);
+        }
+    }
+    const int per = 2 * a.Hkv * kRowVecs;  // vectors of a page's bounds
+    for (long long u = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+         u < static_cast<long long>(moves) * per; u += static_cast<long long>(gridDim.x) * 256) {
+        const int k = static_cast<int>(u / per), e = static_cast<int>(u % per);
+        if (a.bounds)
+            a.bounds[static_cast<size_t>(a.dst[k]) * per + e] =
+                a.bounds[static_cast<size_t>(a.src[k]) * per + e];
+        if (e == 0) {
             a.refs[a.dst[k]] = a.refs[a.src[k]];
             a.refs[a.src[k]] = 0;
         }
@@ -615,9 +637,10 @@ cudaError_t launch_cache_append(const CacheLaunch &a, const void *k, const void 
     p.src_tokens = src_tokens; p.tokens = tokens; p.num_pages = a.num_pages;
     p.max_pages = a.max_pages; p.Hkv = a.Hkv; p.status = a.status;
     // Pages that `tokens` new tokens can touch, from any offset in a page.
-    const int touched = static_cast<int>(
-        std::min<long long>(a.max_pages, (tokens - 1ll + kPage - 1) / kPage + 1));
-    cache_append_kernel<<<dim3(touched, a.Hkv, a.num_seqs), 128, 0, a.stream>>>(p);
+    const long long touched = std::min<long long>(a.max_pages, (tokens - 1ll + kPage - 1) / kPage + 1);
+    if (touched * a.Hkv > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    cache_append_kernel<<<dim3(static_cast<unsigned>(touched * a.Hkv), a.num_seqs), 128, 0,
+                          a.stream>>>(p);
     count_launches(1);
     return cudaGetLastError();
 }

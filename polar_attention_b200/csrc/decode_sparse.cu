@@ -24,7 +24,9 @@ constexpr int kSmem = kRingStages * kStageBytes + 1024;  // + alignment slack
 constexpr int kScoreThreads = 256;
 constexpr int kSelThreads = 512;
 constexpr int kSelKeys = 10240;  // keys that the selection holds in shared memory (40 KB)
-constexpr int kScorePages = 512;  // pages of a score block at most
+constexpr int kScorePages = 512;   // pages of a score block at most
+constexpr int kScoreRing = 8;      // pages that a lane has in flight
+constexpr int kFusedPages = 1024;  // rows up to which the selection's block scores its pages itself
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ bool valid_len(int len, int max_pages) {
@@ -73,43 +75,40 @@ __device__ __forceinline__ uint32_t exact_key(const uint4 *__restrict__ q,
     return __reduce_max_sync(~0u, best);
 }
 
-// Block (pages, kv head, sequence): scores in fp32 and a bound on each one's
-// error, from which the selection sees where 64 bits are needed.  Eight lanes
-// take a page for up to four query heads, eight dimensions each (a group of
-// eight heads takes sixteen lanes).  A product of two bf16 is exact in fp32 (a
-// subnormal one aside), so a score is at most 4 roundings in a lane, one to
-// join its two sums and 3 across lanes from the exact sum: off by at most
-// 8 * 2^-24 * sum_d max_h |q_d| max(|lo_d|, |hi_d|), which with that sum's own
-// roundings is below 12 * 2^-24 of it, and 2^-100 for subnormals.
-template <int G>
-__global__ void __launch_bounds__(kScoreThreads, 3)
-sparse_score_kernel(const uint4 *__restrict__ q, const uint4 *__restrict__ bounds,
-                    const int32_t *__restrict__ page_table, const int32_t *__restrict__ seqlens,
-                    float2 *__restrict__ scores, int num_pages, int max_pages, int Hkv, int keep,
-                    int pages_per_block) {
+__device__ __forceinline__ void copy_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+                 : "memory");
+}
+
+// Scores of pages 0 .. count - 1 of one (sequence, kv head), by a block of
+// kThreads, in fp32 with a bound on each one's error, from which the selection
+// sees where 64 bits are needed: sink(page, score, bound) in one thread per page.
+// phys(p) is the pool's page, or -1 (ranks last).  ring: kScoreRing * 2 * kThreads
+// vectors of shared memory.
+//
+// Eight lanes take a page for up to four query heads, eight dimensions each (a
+// group of eight heads takes sixteen lanes).  A lane copies its part of a page's
+// bounds into its own places of the ring, kScoreRing pages ahead, so that the
+// copies in flight cost no registers and nothing waits for another thread.
+// A product of two bf16 is exact in fp32 (a subnormal one aside), so a score is
+// at most 4 roundings in a lane, one to join its two sums and 3 across lanes
+// from the exact sum: off by at most 8 * 2^-24 * sum_d max_h |q_d| max(|lo_d|,
+// |hi_d|), which with that sum's own roundings is below 12 * 2^-24 of it, and
+// 2^-100 for subnormals.
+template <int G, int kThreads, typename Phys, typename Sink>
+__device__ __forceinline__ void score_pages(const uint4 *__restrict__ q,
+                                            const uint4 *__restrict__ bounds, int g, int Hkv,
+                                            int count, uint4 *ring, Phys &&phys, Sink &&sink) {
     constexpr int GH = G < 4 ? G : 4;       // heads of a lane
     constexpr int kLanes = 8 * (G / GH);    // lanes of a page
-    constexpr int kStep = kScoreThreads / kLanes;
-    constexpr int kDeep = 4;                // pages that a lane has in flight
-    __shared__ int phys[kScorePages];
-    const int g = blockIdx.y, seq = blockIdx.z;
-    const int len = seqlens[seq];
-    if (!valid_len(len, max_pages)) return;  // reported by the selection
-    const int npg = (len + kPage - 1) / kPage;
-    const int first = blockIdx.x * pages_per_block, count = min(npg - first, pages_per_block);
-    if (npg <= keep || count <= 0) return;  // every page is read, or none is here
-    const int32_t *pt = page_table + static_cast<size_t>(seq) * max_pages + first;
-    for (int p = threadIdx.x; p < count; p += kScoreThreads) {
-        const int x = pt[p];
-        phys[p] = x >= 0 && x < num_pages ? x : -1;
-    }
-    const int c = threadIdx.x & 7, part = threadIdx.x % kLanes / 8;
+    constexpr int kStep = kThreads / kLanes;
+    const int tid = threadIdx.x, c = tid & 7, part = tid % kLanes / 8;
     float2 qf[GH][4], qm[4];
 #pragma unroll
     for (int d = 0; d < 4; ++d) qm[d] = make_float2(0.f, 0.f);
 #pragma unroll
     for (int h = 0; h < GH; ++h) {
-        const uint4 x = __ldg(q + ((static_cast<size_t>(seq) * Hkv + g) * G + part * GH + h) * 8 + c);
+        const uint4 x = __ldg(q + (part * GH + h) * 8 + c);
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
@@ -119,83 +118,109 @@ sparse_score_kernel(const uint4 *__restrict__ q, const uint4 *__restrict__ bound
             qm[d] = make_float2(fmaxf(qm[d].x, fabsf(v.x)), fmaxf(qm[d].y, fabsf(v.y)));
         }
     }
-    __syncthreads();
-    float2 *out = scores + (static_cast<size_t>(seq) * Hkv + g) * max_pages + first;
-    for (int p0 = threadIdx.x / kLanes; p0 - static_cast<int>(threadIdx.x) / kLanes < count;
-         p0 += kStep * kDeep) {
-        uint4 lo4[kDeep], hi4[kDeep];
-        bool ok[kDeep];
-#pragma unroll
-        for (int e = 0; e < kDeep; ++e) {
-            const int p = p0 + e * kStep, x = p < count ? phys[p] : -1;
-            ok[e] = x >= 0;
-            if (ok[e]) {
-                const uint4 *b = bounds + (static_cast<size_t>(x) * Hkv + g) * 16;
-                lo4[e] = __ldg(b + c);
-                hi4[e] = __ldg(b + 8 + c);
-            } else {
-                lo4[e] = hi4[e] = make_uint4(0, 0, 0, 0);
-            }
+    const int p0 = tid / kLanes, steps = (count + kStep - 1) / kStep;
+    auto fetch = [&](int step) {
+        const int p = p0 + step * kStep, x = p < count ? phys(p) : -1;
+        if (x >= 0) {
+            const uint4 *b = bounds + (static_cast<size_t>(x) * Hkv + g) * 16 + c;
+            uint4 *dst = ring + step % kScoreRing * 2 * kThreads + tid;
+            copy_async16(dst, b);
+            copy_async16(dst + kThreads, b + 8);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 #pragma unroll
-        for (int e = 0; e < kDeep; ++e) {
-            if (p0 - static_cast<int>(threadIdx.x) / kLanes + e * kStep >= count) break;  // uniform
-            const uint32_t lw[4] = {lo4[e].x, lo4[e].y, lo4[e].z, lo4[e].w};
-            const uint32_t hw[4] = {hi4[e].x, hi4[e].y, hi4[e].z, hi4[e].w};
-            float2 acc[GH], mag = make_float2(0.f, 0.f);
+    for (int e = 0; e < kScoreRing - 1; ++e) fetch(e);
+    for (int step = 0; step < steps; ++step) {  // the same number in every lane: it shuffles
+        fetch(step + kScoreRing - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kScoreRing - 1) : "memory");
+        const int p = p0 + step * kStep;
+        const uint4 *src = ring + step % kScoreRing * 2 * kThreads + tid;
+        const uint4 lo4 = src[0], hi4 = src[kThreads];
+        const uint32_t lw[4] = {lo4.x, lo4.y, lo4.z, lo4.w};
+        const uint32_t hw[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
+        float2 acc[GH], mag = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int h = 0; h < GH; ++h) acc[h] = make_float2(0.f, 0.f);
+        for (int h = 0; h < GH; ++h) acc[h] = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                const float2 lo = make_float2(__uint_as_float(lw[d] << 16),
-                                              __uint_as_float(lw[d] & 0xffff0000u));
-                const float2 hi = make_float2(__uint_as_float(hw[d] << 16),
-                                              __uint_as_float(hw[d] & 0xffff0000u));
-                const float2 m = make_float2(fmaxf(fabsf(lo.x), fabsf(hi.x)),
-                                             fmaxf(fabsf(lo.y), fabsf(hi.y)));
-                mag = f2_fma(qm[d], m, mag);
+        for (int d = 0; d < 4; ++d) {
+            const float2 lo = make_float2(__uint_as_float(lw[d] << 16),
+                                          __uint_as_float(lw[d] & 0xffff0000u));
+            const float2 hi = make_float2(__uint_as_float(hw[d] << 16),
+                                          __uint_as_float(hw[d] & 0xffff0000u));
+            const float2 m = make_float2(fmaxf(fabsf(lo.x), fabsf(hi.x)),
+                                         fmaxf(fabsf(lo.y), fabsf(hi.y)));
+            mag = f2_fma(qm[d], m, mag);
 #pragma unroll
-                for (int h = 0; h < GH; ++h)
-                    acc[h] = f2_add(acc[h], make_float2(fmaxf(qf[h][d].x * lo.x, qf[h][d].x * hi.x),
-                                                        fmaxf(qf[h][d].y * lo.y, qf[h][d].y * hi.y)));
-            }
-            // Sum over the eight lanes; where a lane has several heads, each
-            // step halves them instead of repeating the sum.
-            float err = mag.x + mag.y, best;
-            float s[GH];
+            for (int h = 0; h < GH; ++h)
+                acc[h] = f2_add(acc[h], make_float2(fmaxf(qf[h][d].x * lo.x, qf[h][d].x * hi.x),
+                                                    fmaxf(qf[h][d].y * lo.y, qf[h][d].y * hi.y)));
+        }
+        // Sum over the eight lanes; where a lane has several heads, each step
+        // halves them instead of repeating the sum.
+        float err = mag.x + mag.y, best;
+        float s[GH];
 #pragma unroll
-            for (int h = 0; h < GH; ++h) s[h] = acc[h].x + acc[h].y;
+        for (int h = 0; h < GH; ++h) s[h] = acc[h].x + acc[h].y;
 #pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1)  // over both halves of eight heads: an upper bound
-                err = o < 8 ? err + __shfl_xor_sync(~0u, err, o)
-                            : fmaxf(err, __shfl_xor_sync(~0u, err, o));
-            if constexpr (GH == 4) {
-                const bool up = c & 4, up2 = c & 2;
-                const float s0 = (up ? s[2] : s[0]) + __shfl_xor_sync(~0u, up ? s[0] : s[2], 4);
-                const float s1 = (up ? s[3] : s[1]) + __shfl_xor_sync(~0u, up ? s[1] : s[3], 4);
-                best = (up2 ? s1 : s0) + __shfl_xor_sync(~0u, up2 ? s0 : s1, 2);
-                best += __shfl_xor_sync(~0u, best, 1);
-                best = fmaxf(best, __shfl_xor_sync(~0u, best, 2));
-                best = fmaxf(best, __shfl_xor_sync(~0u, best, 4));
-            } else if constexpr (GH == 2) {
-                const bool up = c & 4;
-                best = (up ? s[1] : s[0]) + __shfl_xor_sync(~0u, up ? s[0] : s[1], 4);
-                best += __shfl_xor_sync(~0u, best, 2);
-                best += __shfl_xor_sync(~0u, best, 1);
-                best = fmaxf(best, __shfl_xor_sync(~0u, best, 4));
-            } else {
-                best = s[0] + __shfl_xor_sync(~0u, s[0], 4);
-                best += __shfl_xor_sync(~0u, best, 2);
-                best += __shfl_xor_sync(~0u, best, 1);
-            }
-            if constexpr (kLanes == 16) best = fmaxf(best, __shfl_xor_sync(~0u, best, 8));
-            // Bounds that are not finite make err so, too: 64 bits then decide.
-            // A page outside the pool ranks last; the split reports it if read.
-            if (threadIdx.x % kLanes == 0 && p0 + e * kStep < count)
-                out[p0 + e * kStep] = ok[e] ? make_float2(best, fmaf(err, 12.0f * 0x1p-24f, 0x1p-100f))
-                                            : make_float2(-INFINITY, 0.f);
+        for (int o = 1; o < kLanes; o <<= 1)  // over both halves of eight heads: an upper bound
+            err = o < 8 ? err + __shfl_xor_sync(~0u, err, o)
+                        : fmaxf(err, __shfl_xor_sync(~0u, err, o));
+        if constexpr (GH == 4) {
+            const bool up = c & 4, up2 = c & 2;
+            const float s0 = (up ? s[2] : s[0]) + __shfl_xor_sync(~0u, up ? s[0] : s[2], 4);
+            const float s1 = (up ? s[3] : s[1]) + __shfl_xor_sync(~0u, up ? s[1] : s[3], 4);
+            best = (up2 ? s1 : s0) + __shfl_xor_sync(~0u, up2 ? s0 : s1, 2);
+            best += __shfl_xor_sync(~0u, best, 1);
+            best = fmaxf(best, __shfl_xor_sync(~0u, best, 2));
+            best = fmaxf(best, __shfl_xor_sync(~0u, best, 4));
+        } else if constexpr (GH == 2) {
+            const bool up = c & 4;
+            best = (up ? s[1] : s[0]) + __shfl_xor_sync(~0u, up ? s[0] : s[1], 4);
+            best += __shfl_xor_sync(~0u, best, 2);
+            best += __shfl_xor_sync(~0u, best, 1);
+            best = fmaxf(best, __shfl_xor_sync(~0u, best, 4));
+        } else {
+            best = s[0] + __shfl_xor_sync(~0u, s[0], 4);
+            best += __shfl_xor_sync(~0u, best, 2);
+            best += __shfl_xor_sync(~0u, best, 1);
+        }
+        if constexpr (kLanes == 16) best = fmaxf(best, __shfl_xor_sync(~0u, best, 8));
+        // Bounds that are not finite make err so, too: 64 bits then decide.
+        if (tid % kLanes == 0 && p < count) {
+            const bool ok = phys(p) >= 0;
+            sink(p, ok ? best : -INFINITY, ok ? fmaf(err, 12.0f * 0x1p-24f, 0x1p-100f) : 0.f);
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Block (pages, kv head, sequence) of long rows.
+template <int G>
+__global__ void __launch_bounds__(kScoreThreads, 3)
+sparse_score_kernel(const uint4 *__restrict__ q, const uint4 *__restrict__ bounds,
+                    const int32_t *__restrict__ page_table, const int32_t *__restrict__ seqlens,
+                    float2 *__restrict__ scores, int num_pages, int max_pages, int Hkv, int keep,
+                    int pages_per_block) {
+    extern __shared__ uint4 score_ring[];
+    __shared__ int pages[kScorePages];
+    const int g = blockIdx.y, seq = blockIdx.z;
+    const int len = seqlens[seq];
+    if (!valid_len(len, max_pages)) return;  // reported by the selection
+    const int npg = (len + kPage - 1) / kPage;
+    const int first = blockIdx.x * pages_per_block, count = min(npg - first, pages_per_block);
+    if (npg <= keep || count <= 0) return;  // every page is read, or none is here
+    const int32_t *pt = page_table + static_cast<size_t>(seq) * max_pages + first;
+    for (int p = threadIdx.x; p < count; p += kScoreThreads) {
+        const int x = pt[p];
+        pages[p] = x >= 0 && x < num_pages ? x : -1;
+    }
+    __syncthreads();
+    const size_t row = static_cast<size_t>(seq) * Hkv + g;
+    float2 *out = scores + row * max_pages + first;
+    score_pages<G, kScoreThreads>(q + row * G * 8, bounds, g, Hkv, count, score_ring,
+                                  [&](int p) { return pages[p]; },
+                                  [&](int p, float s, float e) { out[p] = make_float2(s, e); });
 }
 
 struct SelectArgs {
@@ -218,9 +243,16 @@ struct SelectArgs {
 // is taken and one below T - 2E is not, whatever the roundings.  Where the pages
 // between are not all taken, they get their exact scores, and the selection
 // runs once more on (taken, exact, not taken).
-template <int G>
+//
+// kScores: the block scores its pages itself, for rows short enough that a
+// launch costs more than one block's reading them (measured at 512 pages, one
+// sequence: XXX us against XXX with a launch of its own).
+template <int G, bool kScores>
 __global__ void __launch_bounds__(kSelThreads) sparse_select_kernel(const SelectArgs a) {
-    extern __shared__ uint32_t held[];
+    extern __shared__ uint4 score_ring[];  // kScores: the ring, then the pages and the keys
+    constexpr int kRingVecs = kScores ? kScoreRing * 2 * kSelThreads : 0;
+    int *pages = reinterpret_cast<int *>(score_ring + kRingVecs);
+    uint32_t *held = reinterpret_cast<uint32_t *>(pages) + (kScores ? kFusedPages : 0);
     __shared__ int hist[256];
     __shared__ uint32_t ends[4][kSelThreads / 32];
     __shared__ int counts[2][kSelThreads / 32];
@@ -243,15 +275,31 @@ __global__ void __launch_bounds__(kSelThreads) sparse_select_kernel(const Select
     }
     if (tid == 0) out[a.keep - 1] = npg - 1;  // the newest page, without a score
     if (a.keep == 1) return;
-    const float2 *scores = a.scores + row * a.max_pages;
     const int n = npg - 1, take = a.keep - 1;
     uint32_t *keys = n <= kSelKeys ? held : a.keys + row * a.max_pages;
 
     uint32_t err = 0;  // as bits: in the order of the values, and a NaN above all
-    for (int p = tid; p < n; p += kSelThreads) {
-        const float2 x = scores[p];
-        keys[p] = score_key(x.x);
-        err = max(err, __float_as_uint(x.y) & 0x7fffffffu);
+    if constexpr (kScores) {
+        const int32_t *pt = a.page_table + static_cast<size_t>(seq) * a.max_pages;
+        for (int p = tid; p < n; p += kSelThreads) {
+            const int x = pt[p];
+            pages[p] = x >= 0 && x < a.num_pages ? x : -1;
+        }
+        __syncthreads();
+        score_pages<G, kSelThreads>(a.q + row * G * 8, a.bounds, g, a.Hkv, n, score_ring,
+                                    [&](int p) { return pages[p]; },
+                                    [&](int p, float s, float e) {
+                                        keys[p] = score_key(s);
+                                        err = max(err, __float_as_uint(e) & 0x7fffffffu);
+                                    });
+    } else {
+        const float2 *scores = a.scores + row * a.max_pages;
+#pragma unroll 8
+        for (int p = tid; p < n; p += kSelThreads) {
+            const float2 x = scores[p];
+            keys[p] = score_key(x.x);
+            err = max(err, __float_as_uint(x.y) & 0x7fffffffu);
+        }
     }
     if (tid < 256) hist[tid] = 0;
 
@@ -396,47 +444,36 @@ __global__ void __launch_bounds__(kSelThreads) sparse_select_kernel(const Select
         left = n;
     }
 
-    // Ascending order: thread t has pages t * per .. t * per + per - 1.
-    const int per = (n + kSelThreads - 1) / kSelThreads;
-    const int p0 = min(tid * per, n), p1 = min(p0 + per, n);
-    int gt = 0, eq = 0;
-    for (int p = p0; p < p1; ++p) {
-        const uint32_t k = keys[p] & ~open;
-        gt += k > floor_key;
-        eq += k == floor_key;
-    }
-    int gs = gt, es = eq;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(~0u, gs, o), z = __shfl_up_sync(~0u, es, o);
-        if (lane >= o) {
-            gs += y;
-            es += z;
-        }
+    // Ascending order: warp w has pages w * per .. w * per + per - 1.
+    const int per = (n + kSelThreads - 1) / kSelThreads * 32;
+    const int p0 = min(w * per, n), p1 = min(p0 + per, n);
+    int gs = 0, es = 0;
+    for (int p = p0 + lane; p < p0 + per; p += 32) {
+        const uint32_t k = p < p1 ? keys[p] & ~open : 0u;
+        gs += __popc(__ballot_sync(~0u, p < p1 && k > floor_key));
+        es += __popc(__ballot_sync(~0u, p < p1 && k == floor_key));
     }
     __syncthreads();  // the counts above are read
-    if (lane == 31) {
+    if (lane == 0) {
         counts[0][w] = gs;
         counts[1][w] = es;
     }
     __syncthreads();
-    gs -= gt;
-    es -= eq;
+    gs = es = 0;
     for (int i = 0; i < w; ++i) {
         gs += counts[0][i];
         es += counts[1][i];
     }
-    if (gt + eq > 0)
-        for (int p = p0; p < p1; ++p) {
-            const uint32_t k = keys[p] & ~open;
-            if (k > floor_key) {
-                out[gs + min(es, left)] = p;
-                ++gs;
-            } else if (k == floor_key) {
-                if (es < left) out[gs + es] = p;
-                ++es;
-            }
-        }
+    const uint32_t below_me = (1u << lane) - 1;
+    for (int p = p0 + lane; p < p0 + per; p += 32) {
+        const uint32_t k = p < p1 ? keys[p] & ~open : 0u;
+        const bool gt = p < p1 && k > floor_key, eq = p < p1 && k == floor_key;
+        const uint32_t mg = __ballot_sync(~0u, gt), me = __ballot_sync(~0u, eq);
+        const int gi = gs + __popc(mg & below_me), ei = es + __popc(me & below_me);
+        if (gt || (eq && ei < left)) out[gi + min(ei, left)] = p;
+        gs += __popc(mg);
+        es += __popc(me);
+    }
 }
 
 struct SparseArgs {
@@ -558,6 +595,9 @@ __global__ void __launch_bounds__(128) sparse_merge_kernel(const SparseArgs a, i
                a.out + static_cast<size_t>(row) * kHeadDim, a.neff ? a.neff + row : nullptr, real);
 }
 
+constexpr int kScoreSmem = kScoreRing * 2 * kScoreThreads * 16;
+constexpr int kFusedSmem = kScoreRing * 2 * kSelThreads * 16 + 2 * kFusedPages * 4;
+
 struct Layout {  // the workspace: scores, keys (long rows), selected pages, partials
     size_t keys, selected, partials, total;
     int cluster, splits;  // CTAs of a cluster, clusters of a (sequence, kv head)
@@ -594,6 +634,12 @@ cudaError_t launch_all(const SparseLaunch &a, const CUtensorMap &map, const Layo
     if (!(configured.load() & bit)) {
         e = cudaFuncSetAttribute(sparse_split_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kSmem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(sparse_score_kernel<G>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(sparse_select_kernel<G, true>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kFusedSmem);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
@@ -601,17 +647,19 @@ cudaError_t launch_all(const SparseLaunch &a, const CUtensorMap &map, const Layo
     float2 *scores = reinterpret_cast<float2 *>(ws);
     int32_t *sel = a.selected ? a.selected : reinterpret_cast<int32_t *>(ws + l.selected);
     const uint4 *q = static_cast<const uint4 *>(a.q), *bounds = static_cast<const uint4 *>(a.bounds);
-    const bool scored = a.max_pages > a.keep;
-    if (scored) {
-        // Three blocks fit an SM; about twelve, since lengths differ.  A step is
-        // 32 pages (16 for groups of eight heads).
+    // Rows that may hold more pages than are kept are scored: long ones by a
+    // kernel of many blocks, short ones by the selection's own block.
+    const bool scored = a.max_pages > a.keep, fused = scored && a.max_pages <= kFusedPages;
+    if (scored && !fused) {
+        // Three blocks fit an SM; about six, since lengths differ.  A step is 32
+        // pages (16 for groups of eight heads).
         const int step = kScoreThreads / (G == 8 ? 16 : 8);
         const long long all = static_cast<long long>(a.num_seqs) * a.Hkv *
                               ((a.max_pages + step - 1) / step);
         const int per = step * static_cast<int>(
-            std::clamp<long long>(all / (148 * 12), 1, kScorePages / step));
+            std::clamp<long long>(all / (148 * 6), 1, kScorePages / step));
         sparse_score_kernel<G><<<dim3((a.max_pages + per - 1) / per, a.Hkv, a.num_seqs),
-                                 kScoreThreads, 0, a.stream>>>(
+                                 kScoreThreads, kScoreSmem, a.stream>>>(
             q, bounds, a.page_table, a.seqlens, scores, a.num_pages, a.max_pages, a.Hkv, a.keep,
             per);
         e = cudaGetLastError();
@@ -621,9 +669,12 @@ cudaError_t launch_all(const SparseLaunch &a, const CUtensorMap &map, const Layo
     SelectArgs s{q, bounds, scores, a.page_table, a.seqlens, sel,
                  reinterpret_cast<uint32_t *>(ws + l.keys), a.num_pages, a.max_pages, a.Hkv,
                  a.keep, a.status};
-    const size_t held = std::min(a.max_pages, kSelKeys) * sizeof(uint32_t);
-    e = launch_ex(sparse_select_kernel<G>, dim3(a.Hkv, a.num_seqs), kSelThreads, held, 1, scored,
-                  a.stream, s);
+    if (fused)
+        e = launch_ex(sparse_select_kernel<G, true>, dim3(a.Hkv, a.num_seqs), kSelThreads,
+                      kFusedSmem, 1, false, a.stream, s);
+    else
+        e = launch_ex(sparse_select_kernel<G, false>, dim3(a.Hkv, a.num_seqs), kSelThreads,
+                      std::min(a.max_pages, kSelKeys) * sizeof(uint32_t), 1, scored, a.stream, s);
     if (e != cudaSuccess) return e;
     SparseArgs p;
     p.page_table = a.page_table; p.seqlens = a.seqlens; p.selected = sel;
