@@ -12,7 +12,6 @@ namespace polar {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kChunkPages = 2048;      // reference counts per block of the compaction's plan
 constexpr int kRowVecs = kHeadDim / 8;  // 16-byte vectors of one key or value row
 
 __device__ __forceinline__ int pages_of(int len) { return (len + kPage - 1) / kPage; }
@@ -460,85 +459,88 @@ cache_free_kernel(int32_t *__restrict__ refs, int num_pages, int32_t *__restrict
 
 // --------------------------------------------------------------- compact ---
 
+constexpr int kCompactCluster = 8;
+
 struct CompactArgs {
     int32_t *refs, *table, *used;
     const int32_t *lens;
     uint4 *kv, *bounds;
-    int num_pages, max_pages, num_seqs, Hkv, chunks;
-    // Workspace: live pages per chunk of the counts; [0] pages that move, [1]
-    // live pages; per page its rank among the movers (-1: none); the movers
-    // and their places, by rank.
-    int *counts, *head, *rank, *src, *dst;
+    int num_pages, max_pages, num_seqs, Hkv;
+    // Workspace: [0] pages that move; per page its rank among the movers (-1:
+    // free, -2: stays); the movers and their places, by rank.
+    int *head, *rank, *src, *dst;
     int *status;
 };
 
-__global__ void __launch_bounds__(256) cache_compact_count_kernel(const CompactArgs a) {
-    int live = 0;
-    const int p0 = blockIdx.x * kChunkPages;
-    for (int p = p0 + threadIdx.x; p < min(p0 + kChunkPages, a.num_pages); p += 256)
-        live += a.refs[p] > 0;
-    __shared__ int scratch[8];
-    int total;
-    block_scan(live, scratch, &total);
-    if (threadIdx.x == 0) a.counts[blockIdx.x] = total;
-}
-
 // With n live pages and L(x) live pages below id x: a live page p >= n is the
-// (L(p) - L(n))-th mover, a free id p < n the (p - L(p))-th place.
-__global__ void __launch_bounds__(256) cache_compact_plan_kernel(const CompactArgs a) {
-    __shared__ int scratch[8];
-    const int tid = threadIdx.x;
-    int mine = 0, all = 0;
-    for (int c = tid; c < a.chunks; c += 256) {
-        const int x = a.counts[c];
-        all += x;
-        mine += c < blockIdx.x ? x : 0;
+// (L(p) - L(n))-th mover, a free id p < n the (p - L(p))-th place.  One cluster;
+// each block counts its stretch of the pool, the blocks exchange their counts,
+// and each writes the ranks of its stretch.
+__global__ void __launch_bounds__(kPlanThreads) cache_compact_plan_kernel(const CompactArgs a) {
+    __shared__ int scratch[kPlanThreads / 32];
+    __shared__ int counts[2];  // live pages of this block's stretch; of them, those below n
+    constexpr int kPer = 8;
+    const int tid = threadIdx.x, block = static_cast<int>(cluster_rank());
+    const int stretch = ((a.num_pages + kCompactCluster - 1) / kCompactCluster + 3) / 4 * 4;
+    const int lo = min(block * stretch, a.num_pages), hi = min(lo + stretch, a.num_pages);
+    auto live_in = [&](int from, int to) {
+        int mine = 0, total;
+        for (int p = from + tid; p < to; p += kPlanThreads) mine += a.refs[p] > 0;
+        block_scan(mine, scratch, &total);
+        return total;
+    };
+    const int own = live_in(lo, hi);
+    if (tid == 0) counts[0] = own;
+    cluster_sync();
+    int n = 0, upto = 0;  // upto: L at the place that is next
+    for (int b = 0; b < kCompactCluster; ++b) {
+        const int x = cluster_map(counts, b)[0];
+        n += x;
+        upto += b < block ? x : 0;
     }
-    int n, before;
-    block_scan(all, scratch, &n);
-    block_scan(mine, scratch, &before);
-    // L(n): the chunks below n's, and n's own chunk up to n.
-    const int cn = n / kChunkPages;
-    int below = 0;
-    for (int c = tid; c < cn; c += 256) below += a.counts[c];
-    for (int p = cn * kChunkPages + tid; p < n; p += 256) below += a.refs[p] > 0;
-    int live_below;
-    block_scan(below, scratch, &live_below);
+    const int below = n >= hi ? own : n <= lo ? 0 : live_in(lo, n);
+    if (tid == 0) counts[1] = below;
+    cluster_sync();
+    int live_below = 0;  // L(n)
+    for (int b = 0; b < kCompactCluster; ++b) live_below += cluster_map(counts, b)[1];
 
-    constexpr int kPer = kChunkPages / 256;
-    const int p0 = blockIdx.x * kChunkPages + tid * kPer;
-    bool live[kPer];
-    int count = 0;
+    for (int q0 = lo; q0 < hi; q0 += kPlanThreads * kPer) {
+        const int p0 = q0 + tid * kPer;
+        bool live[kPer];
+        int count = 0, total;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        live[e] = p0 + e < a.num_pages && a.refs[p0 + e] > 0;
-        count += live[e];
-    }
-    int total;
-    int upto = before + block_scan(count, scratch, &total) - count;  // L(p0)
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        const int p = p0 + e;
-        if (p < a.num_pages) {
-            if (p < n) {
-                a.rank[p] = live[e] ? -2 : -1;  // -2: stays
-                if (!live[e]) a.dst[p - upto] = p;
-            } else {
-                a.rank[p] = live[e] ? upto - live_below : -1;
-                if (live[e]) a.src[upto - live_below] = p;
-            }
+        for (int e = 0; e < kPer; ++e) {
+            live[e] = p0 + e < hi && a.refs[p0 + e] > 0;
+            count += live[e];
         }
-        upto += live[e];
+        int at = upto + block_scan(count, scratch, &total) - count;  // L(p0)
+        upto += total;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const int p = p0 + e;
+            if (p < hi) {
+                if (p < n) {
+                    a.rank[p] = live[e] ? -2 : -1;
+                    if (!live[e]) a.dst[p - at] = p;
+                } else {
+                    a.rank[p] = live[e] ? at - live_below : -1;
+                    if (live[e]) a.src[at - live_below] = p;
+                }
+            }
+            at += live[e];
+        }
     }
-    if (blockIdx.x == 0 && tid == 0) {
+    if (block == 0 && tid == 0) {
         a.head[0] = n - live_below;
         a.used[0] = n;
     }
+    cluster_sync();  // no block leaves while its counts are read
 }
 
 // Copies the movers' pages, laid end to end, 32 KB at a time (eight vectors a
 // thread in flight), then rewrites references and tables.
 __global__ void __launch_bounds__(256) cache_compact_move_kernel(const CompactArgs a) {
+    wait_for_previous_kernel();
     const int moves = a.head[0];
     const int page_vecs = 2 * a.Hkv * kPage * kRowVecs;  // a multiple of 1024
     const long long vecs = static_cast<long long>(moves) * page_vecs;
@@ -591,15 +593,13 @@ __global__ void __launch_bounds__(256) cache_compact_move_kernel(const CompactAr
     }
 }
 
-int chunk_count(int num_pages) { return (num_pages + kChunkPages - 1) / kChunkPages; }
-
 }  // namespace
 
 size_t cache_workspace_bytes(int num_pages, int num_seqs) {
     // Three ints a page (reserve: owner, sharers, fresh; compact: rank, src,
-    // dst), five a row, the compaction's chunk counts and its head.
-    return (3 * static_cast<size_t>(num_pages) + 5 * static_cast<size_t>(num_seqs) +
-            chunk_count(num_pages) + 4) * sizeof(int);
+    // dst), five a row, and one more.
+    return (3 * static_cast<size_t>(num_pages) + 5 * static_cast<size_t>(num_seqs) + 4) *
+           sizeof(int);
 }
 
 cudaError_t launch_cache_reserve(const CacheLaunch &a, const int32_t *grow, int32_t *granted) {
@@ -639,27 +639,24 @@ cudaError_t launch_cache_append(const CacheLaunch &a, const void *k, const void 
     // Pages that `tokens` new tokens can touch, from any offset in a page.
     const long long touched = std::min<long long>(a.max_pages, (tokens - 1ll + kPage - 1) / kPage + 1);
     if (touched * a.Hkv > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    cache_append_kernel<<<dim3(static_cast<unsigned>(touched * a.Hkv), a.num_seqs), 128, 0,
-                          a.stream>>>(p);
     count_launches(1);
-    return cudaGetLastError();
+    return launch_ex(cache_append_kernel, dim3(static_cast<unsigned>(touched * a.Hkv), a.num_seqs),
+                     128, 0, 1, false, a.stream, p);
 }
 
 cudaError_t launch_cache_fork(const CacheLaunch &a, const int32_t *src_table,
                               const int32_t *src_lens, int num_src, const int32_t *src_rows) {
     const int blocks = std::min((a.max_pages + 255) / 256, 64);
-    cache_fork_kernel<<<dim3(blocks, a.num_seqs), 256, 0, a.stream>>>(
-        a.refs, a.num_pages, src_table, src_lens, num_src, src_rows, a.table, a.lens, a.max_pages,
-        a.status);
     count_launches(1);
-    return cudaGetLastError();
+    return launch_ex(cache_fork_kernel, dim3(blocks, a.num_seqs), 256, 0, 1, false, a.stream, a.refs,
+                     a.num_pages, src_table, src_lens, num_src, src_rows, a.table, a.lens,
+                     a.max_pages, a.status);
 }
 
 cudaError_t launch_cache_free(const CacheLaunch &a, const int32_t *keep) {
-    cache_free_kernel<<<a.num_seqs, 256, 0, a.stream>>>(a.refs, a.num_pages, a.table, a.max_pages,
-                                                       a.lens, keep, a.status);
     count_launches(1);
-    return cudaGetLastError();
+    return launch_ex(cache_free_kernel, dim3(a.num_seqs), 256, 0, 1, false, a.stream, a.refs,
+                     a.num_pages, a.table, a.max_pages, a.lens, keep, a.status);
 }
 
 cudaError_t launch_cache_compact(const CacheLaunch &a, int32_t *used) {
@@ -668,20 +665,14 @@ cudaError_t launch_cache_compact(const CacheLaunch &a, int32_t *used) {
     c.refs = a.refs; c.table = a.table; c.lens = a.lens; c.used = used;
     c.kv = static_cast<uint4 *>(a.kv); c.bounds = static_cast<uint4 *>(a.bounds);
     c.num_pages = a.num_pages; c.max_pages = a.max_pages; c.num_seqs = a.num_seqs; c.Hkv = a.Hkv;
-    c.chunks = chunk_count(a.num_pages);
     c.rank = ws; c.src = ws + a.num_pages; c.dst = ws + 2 * static_cast<size_t>(a.num_pages);
-    c.counts = ws + 3 * static_cast<size_t>(a.num_pages);
-    c.head = c.counts + c.chunks;
+    c.head = ws + 3 * static_cast<size_t>(a.num_pages);
     c.status = a.status;
-    cache_compact_count_kernel<<<c.chunks, 256, 0, a.stream>>>(c);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_ex(cache_compact_plan_kernel, dim3(kCompactCluster), kPlanThreads, 0,
+                              kCompactCluster, false, a.stream, c);
     if (e != cudaSuccess) return e;
-    cache_compact_plan_kernel<<<c.chunks, 256, 0, a.stream>>>(c);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    cache_compact_move_kernel<<<148 * 8, 256, 0, a.stream>>>(c);
-    count_launches(3);
-    return cudaGetLastError();
+    count_launches(2);
+    return launch_ex(cache_compact_move_kernel, dim3(148 * 8), 256, 0, 1, true, a.stream, c);
 }
 
 }  // namespace polar

@@ -21,12 +21,12 @@ namespace polar {
 namespace {
 
 constexpr int kSmem = kRingStages * kStageBytes + 1024;  // + alignment slack
-constexpr int kScoreThreads = 256;
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 256;
+constexpr int kSelCluster = 8;
+constexpr int kFew = 64;  // pages in doubt that are ranked by comparing all
 constexpr int kSelKeys = 10240;  // keys that the selection holds in shared memory (40 KB)
-constexpr int kScorePages = 512;   // pages of a score block at most
-constexpr int kScoreRing = 8;      // pages that a lane has in flight
-constexpr int kFusedPages = 1024;  // rows up to which the selection's block scores its pages itself
+constexpr int kScorePages = 512;  // page ids that a block holds
+constexpr int kScoreRing = 2;     // pages that a lane has in flight
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ bool valid_len(int len, int max_pages) {
@@ -81,51 +81,48 @@ __device__ __forceinline__ void copy_async16(void *dst, const void *src) {
 }
 
 // Scores of pages 0 .. count - 1 of one (sequence, kv head), by a block of
-// kThreads, in fp32 with a bound on each one's error, from which the selection
-// sees where 64 bits are needed: sink(page, score, bound) in one thread per page.
-// phys(p) is the pool's page, or -1 (ranks last).  ring: kScoreRing * 2 * kThreads
-// vectors of shared memory.
+// kThreads, with a bound on each one's error, from which the selection sees where
+// 64 bits are needed: sink(page, score, bound) in one thread per page.  phys(p)
+// is the pool's page, or -1 (ranks last).  ring: kScoreRing * 4 * kThreads vectors
+// of shared memory.
 //
-// Eight lanes take a page for up to four query heads, eight dimensions each (a
-// group of eight heads takes sixteen lanes).  A lane copies its part of a page's
-// bounds into its own places of the ring, kScoreRing pages ahead, so that the
-// copies in flight cost no registers and nothing waits for another thread.
-// A product of two bf16 is exact in fp32 (a subnormal one aside), so a score is
-// at most 4 roundings in a lane, one to join its two sums and 3 across lanes
-// from the exact sum: off by at most 8 * 2^-24 * sum_d max_h |q_d| max(|lo_d|,
-// |hi_d|), which with that sum's own roundings is below 12 * 2^-24 of it, and
-// 2^-100 for subnormals.
+// With q = q+ + q-, max(q lo, q hi) is q+ hi + q- lo, so the scores are a product
+// of the heads' [q+ q-] with the pages' [hi lo], which a warp forms for eight
+// pages by mma.sync (bf16 in, fp32 accumulate); the same of absolute values is
+// the sum of the terms' magnitudes.  The order of the 128 terms is free: a lane's
+// operands are the 16-byte pieces that it copies itself, a step ahead, so that
+// nothing waits for another thread.  (In fp32 on the CUDA cores the scores of 16
+// sequences of 1024 to 4096 pages took 30 us, bound by the instructions; this
+// XXX us, 42 MB being 6.4 us.)  Products are exact; an instruction adds 16 of them
+// and the sum so far, each cut off no higher than at 2^-24 of the largest, eight
+// times: below 8 * 17 * 2^-24 of the terms' magnitudes, of which 256 * 2^-24 is
+// taken, and 2^-100 for subnormals.
 template <int G, int kThreads, typename Phys, typename Sink>
 __device__ __forceinline__ void score_pages(const uint4 *__restrict__ q,
                                             const uint4 *__restrict__ bounds, int g, int Hkv,
                                             int count, uint4 *ring, Phys &&phys, Sink &&sink) {
-    constexpr int GH = G < 4 ? G : 4;       // heads of a lane
-    constexpr int kLanes = 8 * (G / GH);    // lanes of a page
-    constexpr int kStep = kThreads / kLanes;
-    const int tid = threadIdx.x, c = tid & 7, part = tid % kLanes / 8;
-    float2 qf[GH][4], qm[4];
+    constexpr int kStep = kThreads / 4;  // pages of a step: eight a warp
+    const int tid = threadIdx.x, n = tid & 31, c = n & 3, head = n >> 2;
+    uint32_t qp[2][4], qn[2][4];  // the row's positive and negative parts, dims 8 (c + 4 j) ..
 #pragma unroll
-    for (int d = 0; d < 4; ++d) qm[d] = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int h = 0; h < GH; ++h) {
-        const uint4 x = __ldg(q + (part * GH + h) * 8 + c);
+    for (int j = 0; j < 2; ++j) {
+        const uint4 x = head < G ? __ldg(q + head * 8 + c + 4 * j) : make_uint4(0, 0, 0, 0);
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            const float2 v = make_float2(__uint_as_float(w[d] << 16),
-                                         __uint_as_float(w[d] & 0xffff0000u));
-            qf[h][d] = v;
-            qm[d] = make_float2(fmaxf(qm[d].x, fabsf(v.x)), fmaxf(qm[d].y, fabsf(v.y)));
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t negative = (w[e] >> 15 & 0x00010001u) * 0xffffu;
+            qp[j][e] = w[e] & ~negative;
+            qn[j][e] = w[e] & negative;
         }
     }
-    const int p0 = tid / kLanes, steps = (count + kStep - 1) / kStep;
+    const int p0 = tid / 4, steps = (count + kStep - 1) / kStep;
     auto fetch = [&](int step) {
         const int p = p0 + step * kStep, x = p < count ? phys(p) : -1;
         if (x >= 0) {
             const uint4 *b = bounds + (static_cast<size_t>(x) * Hkv + g) * 16 + c;
-            uint4 *dst = ring + step % kScoreRing * 2 * kThreads + tid;
-            copy_async16(dst, b);
-            copy_async16(dst + kThreads, b + 8);
+            uint4 *dst = ring + step % kScoreRing * 4 * kThreads + tid;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) copy_async16(dst + e * kThreads, b + 4 * e);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -134,98 +131,44 @@ __device__ __forceinline__ void score_pages(const uint4 *__restrict__ q,
     for (int step = 0; step < steps; ++step) {  // the same number in every lane: it shuffles
         fetch(step + kScoreRing - 1);
         asm volatile("cp.async.wait_group %0;" ::"n"(kScoreRing - 1) : "memory");
-        const int p = p0 + step * kStep;
-        const uint4 *src = ring + step % kScoreRing * 2 * kThreads + tid;
-        const uint4 lo4 = src[0], hi4 = src[kThreads];
-        const uint32_t lw[4] = {lo4.x, lo4.y, lo4.z, lo4.w};
-        const uint32_t hw[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
-        float2 acc[GH], mag = make_float2(0.f, 0.f);
+        const uint4 *src = ring + step % kScoreRing * 4 * kThreads + tid;
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int h = 0; h < GH; ++h) acc[h] = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            const float2 lo = make_float2(__uint_as_float(lw[d] << 16),
-                                          __uint_as_float(lw[d] & 0xffff0000u));
-            const float2 hi = make_float2(__uint_as_float(hw[d] << 16),
-                                          __uint_as_float(hw[d] & 0xffff0000u));
-            const float2 m = make_float2(fmaxf(fabsf(lo.x), fabsf(hi.x)),
-                                         fmaxf(fabsf(lo.y), fabsf(hi.y)));
-            mag = f2_fma(qm[d], m, mag);
-#pragma unroll
-            for (int h = 0; h < GH; ++h)
-                acc[h] = f2_add(acc[h], make_float2(fmaxf(qf[h][d].x * lo.x, qf[h][d].x * hi.x),
-                                                    fmaxf(qf[h][d].y * lo.y, qf[h][d].y * hi.y)));
+        for (int e = 0; e < 4; ++e) {  // lo, lo, hi, hi
+            const uint4 x = src[e * kThreads];
+            const uint32_t(&a)[4] = e < 2 ? qn[e] : qp[e - 2];
+            constexpr uint32_t kAbs = 0x7fff7fffu;
+            mma_bf16(s, a[0], 0u, a[1], 0u, x.x, x.y);
+            mma_bf16(s, a[2], 0u, a[3], 0u, x.z, x.w);
+            mma_bf16(m, a[0] & kAbs, 0u, a[1] & kAbs, 0u, x.x & kAbs, x.y & kAbs);
+            mma_bf16(m, a[2] & kAbs, 0u, a[3] & kAbs, 0u, x.z & kAbs, x.w & kAbs);
         }
-        // Sum over the eight lanes; where a lane has several heads, each step
-        // halves them instead of repeating the sum.
-        float err = mag.x + mag.y, best;
-        float s[GH];
+        // Row `head`, pages 2 c and 2 c + 1 of the warp's eight: the heads' largest.
+        // What is not finite makes m so, too: 64 bits then decide.
 #pragma unroll
-        for (int h = 0; h < GH; ++h) s[h] = acc[h].x + acc[h].y;
+        for (int o = 1; o < G; o <<= 1)
 #pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1)  // over both halves of eight heads: an upper bound
-            err = o < 8 ? err + __shfl_xor_sync(~0u, err, o)
-                        : fmaxf(err, __shfl_xor_sync(~0u, err, o));
-        if constexpr (GH == 4) {
-            const bool up = c & 4, up2 = c & 2;
-            const float s0 = (up ? s[2] : s[0]) + __shfl_xor_sync(~0u, up ? s[0] : s[2], 4);
-            const float s1 = (up ? s[3] : s[1]) + __shfl_xor_sync(~0u, up ? s[1] : s[3], 4);
-            best = (up2 ? s1 : s0) + __shfl_xor_sync(~0u, up2 ? s0 : s1, 2);
-            best += __shfl_xor_sync(~0u, best, 1);
-            best = fmaxf(best, __shfl_xor_sync(~0u, best, 2));
-            best = fmaxf(best, __shfl_xor_sync(~0u, best, 4));
-        } else if constexpr (GH == 2) {
-            const bool up = c & 4;
-            best = (up ? s[1] : s[0]) + __shfl_xor_sync(~0u, up ? s[0] : s[1], 4);
-            best += __shfl_xor_sync(~0u, best, 2);
-            best += __shfl_xor_sync(~0u, best, 1);
-            best = fmaxf(best, __shfl_xor_sync(~0u, best, 4));
-        } else {
-            best = s[0] + __shfl_xor_sync(~0u, s[0], 4);
-            best += __shfl_xor_sync(~0u, best, 2);
-            best += __shfl_xor_sync(~0u, best, 1);
-        }
-        if constexpr (kLanes == 16) best = fmaxf(best, __shfl_xor_sync(~0u, best, 8));
-        // Bounds that are not finite make err so, too: 64 bits then decide.
-        if (tid % kLanes == 0 && p < count) {
-            const bool ok = phys(p) >= 0;
-            sink(p, ok ? best : -INFINITY, ok ? fmaf(err, 12.0f * 0x1p-24f, 0x1p-100f) : 0.f);
+            for (int e = 0; e < 2; ++e) {
+                s[e] = fmaxf(s[e], __shfl_xor_sync(~0u, s[e], 4 * o));
+                const uint32_t y = __float_as_uint(m[e]);  // in bit order: a NaN stays
+                m[e] = __uint_as_float(max(y, __shfl_xor_sync(~0u, y, 4 * o)));
+            }
+        if (head == 0) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int p = step * kStep + (tid >> 5) * 8 + 2 * c + e;
+                if (p < count) {
+                    const bool ok = phys(p) >= 0;
+                    sink(p, ok ? s[e] : -INFINITY, ok ? fmaf(m[e], 0x1p-16f, 0x1p-100f) : 0.f);
+                }
+            }
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Block (pages, kv head, sequence) of long rows.
-template <int G>
-__global__ void __launch_bounds__(kScoreThreads, 3)
-sparse_score_kernel(const uint4 *__restrict__ q, const uint4 *__restrict__ bounds,
-                    const int32_t *__restrict__ page_table, const int32_t *__restrict__ seqlens,
-                    float2 *__restrict__ scores, int num_pages, int max_pages, int Hkv, int keep,
-                    int pages_per_block) {
-    extern __shared__ uint4 score_ring[];
-    __shared__ int pages[kScorePages];
-    const int g = blockIdx.y, seq = blockIdx.z;
-    const int len = seqlens[seq];
-    if (!valid_len(len, max_pages)) return;  // reported by the selection
-    const int npg = (len + kPage - 1) / kPage;
-    const int first = blockIdx.x * pages_per_block, count = min(npg - first, pages_per_block);
-    if (npg <= keep || count <= 0) return;  // every page is read, or none is here
-    const int32_t *pt = page_table + static_cast<size_t>(seq) * max_pages + first;
-    for (int p = threadIdx.x; p < count; p += kScoreThreads) {
-        const int x = pt[p];
-        pages[p] = x >= 0 && x < num_pages ? x : -1;
-    }
-    __syncthreads();
-    const size_t row = static_cast<size_t>(seq) * Hkv + g;
-    float2 *out = scores + row * max_pages + first;
-    score_pages<G, kScoreThreads>(q + row * G * 8, bounds, g, Hkv, count, score_ring,
-                                  [&](int p) { return pages[p]; },
-                                  [&](int p, float s, float e) { out[p] = make_float2(s, e); });
-}
-
 struct SelectArgs {
     const uint4 *q, *bounds;
-    const float2 *scores;
     const int32_t *page_table, *seqlens;
     int32_t *selected;  // [num_seqs, Hkv, keep]: ascending pages, then -1
     uint32_t *keys;     // per (sequence, head) row of max_pages: past kSelKeys pages
@@ -233,75 +176,83 @@ struct SelectArgs {
     int *status;
 };
 
-// Block (kv head, sequence): the pages with the highest scores, ascending.
+// Cluster along x per (kv head, sequence): the pages with the highest scores,
+// ascending.  The blocks score a share of the pages each and write the keys to
+// the first block's shared memory (past kSelKeys pages: to the workspace), which
+// selects.  One launch: a kernel for the scores and one for the selection took
+// 25.6 us a call where one sequence has 512 pages and 85 us at 16 sequences of
+// 1024 to 4096, this takes XXX and XXX.
 //
 // A radix selection over keys in the scores' order finds the k-th highest.
 // Scores lie close together, so its digits begin at the highest bit in which
-// two keys differ, and it ends as soon as a bin is taken whole.  Scores come in
-// fp32 with error bounds; with E the largest of them and T the k-th highest
+// two keys differ, and it ends as soon as a bin is taken whole.  Scores come
+// with error bounds; with E the largest of them and T the k-th highest
 // score, the k-th highest exact score is within E of T, so a page above T + 2E
 // is taken and one below T - 2E is not, whatever the roundings.  Where the pages
 // between are not all taken, they get their exact scores, and the selection
 // runs once more on (taken, exact, not taken).
-//
-// kScores: the block scores its pages itself, for rows short enough that a
-// launch costs more than one block's reading them (measured at 512 pages, one
-// sequence: XXX us against XXX with a launch of its own).
-template <int G, bool kScores>
+template <int G>
 __global__ void __launch_bounds__(kSelThreads) sparse_select_kernel(const SelectArgs a) {
-    extern __shared__ uint4 score_ring[];  // kScores: the ring, then the pages and the keys
-    constexpr int kRingVecs = kScores ? kScoreRing * 2 * kSelThreads : 0;
-    int *pages = reinterpret_cast<int *>(score_ring + kRingVecs);
-    uint32_t *held = reinterpret_cast<uint32_t *>(pages) + (kScores ? kFusedPages : 0);
+    extern __shared__ uint4 score_ring[];  // then the keys
+    uint32_t *held = reinterpret_cast<uint32_t *>(score_ring + kScoreRing * 4 * kSelThreads);
+    __shared__ int pages[kScorePages];
     __shared__ int hist[256];
-    __shared__ uint32_t ends[4][kSelThreads / 32];
+    __shared__ uint32_t ends[3][kSelThreads / 32];
     __shared__ int counts[2][kSelThreads / 32];
     __shared__ int s_bin, s_left, s_whole;
-    const int g = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x;
+    __shared__ uint32_t s_err;
+    __shared__ int2 few[kFew];  // page, exact key
+    const int g = blockIdx.y, seq = blockIdx.z, tid = threadIdx.x;
     const int lane = tid & 31, w = tid >> 5;
+    const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
     constexpr int kWarps = kSelThreads / 32;
     const int len = a.seqlens[seq];
-    wait_for_previous_kernel();  // every block, so that a later kernel's wait covers the scores
     if (!valid_len(len, a.max_pages)) {
-        if (g == 0 && tid == 0) record_error(a.status, POLAR_ERR_BAD_SEQLEN);
+        if (rank == 0 && g == 0 && tid == 0) record_error(a.status, POLAR_ERR_BAD_SEQLEN);
         return;
     }
     const int npg = (len + kPage - 1) / kPage;
     const size_t row = static_cast<size_t>(seq) * a.Hkv + g;
     int32_t *out = a.selected + row * a.keep;
     if (npg <= a.keep) {
-        for (int i = tid; i < a.keep; i += kSelThreads) out[i] = i < npg ? i : -1;
+        if (rank == 0)
+            for (int i = tid; i < a.keep; i += kSelThreads) out[i] = i < npg ? i : -1;
         return;
     }
-    if (tid == 0) out[a.keep - 1] = npg - 1;  // the newest page, without a score
+    if (rank == 0 && tid == 0) out[a.keep - 1] = npg - 1;  // the newest page, without a score
     if (a.keep == 1) return;
     const int n = npg - 1, take = a.keep - 1;
     uint32_t *keys = n <= kSelKeys ? held : a.keys + row * a.max_pages;
+    if (tid == 0) s_err = 0;
+    if (tid < 256) hist[tid] = 0;
+    if (C > 1) cluster_sync(); else __syncthreads();
 
+    // This block's share of the scores.
     uint32_t err = 0;  // as bits: in the order of the values, and a NaN above all
-    if constexpr (kScores) {
-        const int32_t *pt = a.page_table + static_cast<size_t>(seq) * a.max_pages;
-        for (int p = tid; p < n; p += kSelThreads) {
-            const int x = pt[p];
+    const uint4 *q = a.q + row * G * 8;
+    const int32_t *pt = a.page_table + static_cast<size_t>(seq) * a.max_pages;
+    uint32_t *to = n <= kSelKeys ? const_cast<uint32_t *>(cluster_map(held, 0)) : keys;
+    const int share = (n + C - 1) / C, last = min(n, (rank + 1) * share);
+    for (int first = rank * share; first < last; first += kScorePages) {
+        const int count = min(last - first, kScorePages);
+        __syncthreads();  // the pages before are done
+        for (int p = tid; p < count; p += kSelThreads) {
+            const int x = pt[first + p];
             pages[p] = x >= 0 && x < a.num_pages ? x : -1;
         }
         __syncthreads();
-        score_pages<G, kSelThreads>(a.q + row * G * 8, a.bounds, g, a.Hkv, n, score_ring,
+        score_pages<G, kSelThreads>(q, a.bounds, g, a.Hkv, count, score_ring,
                                     [&](int p) { return pages[p]; },
                                     [&](int p, float s, float e) {
-                                        keys[p] = score_key(s);
+                                        to[first + p] = score_key(s);
                                         err = max(err, __float_as_uint(e) & 0x7fffffffu);
                                     });
-    } else {
-        const float2 *scores = a.scores + row * a.max_pages;
-#pragma unroll 8
-        for (int p = tid; p < n; p += kSelThreads) {
-            const float2 x = scores[p];
-            keys[p] = score_key(x.x);
-            err = max(err, __float_as_uint(x.y) & 0x7fffffffu);
-        }
     }
-    if (tid < 256) hist[tid] = 0;
+    err = __reduce_max_sync(~0u, err);
+    if (lane == 0 && err) atomicMax(const_cast<uint32_t *>(cluster_map(&s_err, 0)), err);
+    if (C > 1) cluster_sync(); else __syncthreads();
+    if (rank > 0) return;
+    err = s_err;
 
     // Keys above floor_key are taken, and the first `left` of those equal to it;
     // `open`: low bits that do not count.
@@ -372,12 +323,9 @@ __global__ void __launch_bounds__(kSelThreads) sparse_select_kernel(const Select
         }
         open = bits > 0 ? (1u << bits) - 1 : 0u;
     };
-    __syncthreads();
     radix();
 
     // The pages whose place the roundings could change.
-    err = __reduce_max_sync(~0u, err);
-    if (lane == 0) ends[2][w] = err;
     // T: the lowest key that is taken (with a bin taken whole, the lowest in it).
     uint32_t lowest = ~0u;
     for (int p = tid; p < n; p += kSelThreads) {
@@ -385,11 +333,10 @@ __global__ void __launch_bounds__(kSelThreads) sparse_select_kernel(const Select
         if ((k & ~open) >= floor_key) lowest = min(lowest, k);
     }
     lowest = __reduce_min_sync(~0u, lowest);
-    if (lane == 0) ends[3][w] = lowest;
+    if (lane == 0) ends[2][w] = lowest;
     __syncthreads();
     for (int i = 0; i < kWarps; ++i) {
-        lowest = min(lowest, ends[3][i]);
-        err = max(err, ends[2][i]);
+        lowest = min(lowest, ends[2][i]);
     }
     const float E = __uint_as_float(err);
     const float T = key_score(lowest);
@@ -420,9 +367,40 @@ __global__ void __launch_bounds__(kSelThreads) sparse_select_kernel(const Select
         mid += counts[0][i];
         sure += counts[1][i];
     }
-    if (sure + mid != take) {
-        const int32_t *pt = a.page_table + static_cast<size_t>(seq) * a.max_pages;
-        const uint4 *q = a.q + row * G * 8;
+    if (sure + mid == take) {  // all of `mid` are taken
+        floor_key = lowest;
+        open = 0;
+        left = n;
+    } else if (mid <= kFew) {  // the usual case: they are ranked among themselves
+        if (tid == 0) s_left = 0;
+        __syncthreads();
+        for (int p = tid; p < n; p += kSelThreads) {
+            const int c = place(keys[p]);
+            if (c == 1) few[atomicAdd(&s_left, 1)].x = p;  // in any order
+            keys[p] = c == 2 ? 0xffffffffu : 0u;
+        }
+        __syncthreads();
+        for (int i = w; i < mid; i += kWarps) {
+            const int phys = pt[few[i].x];
+            const uint32_t k = phys >= 0 && phys < a.num_pages
+                ? exact_key<G>(q, a.bounds + (static_cast<size_t>(phys) * a.Hkv + g) * 16, lane) : 0u;
+            if (lane == 0) few[i].y = static_cast<int>(k);
+        }
+        __syncthreads();
+        if (tid < mid) {
+            const uint32_t k = few[tid].y;
+            int before = 0;
+            for (int i = 0; i < mid; ++i) {
+                const uint32_t o = few[i].y;
+                before += o > k || (o == k && few[i].x < few[tid].x);
+            }
+            if (before < take - sure) keys[few[tid].x] = 0xffffffffu;
+        }
+        __syncthreads();
+        floor_key = 0xffffffffu;
+        open = 0;
+        left = n;
+    } else {
         for (int first = 32 * w; first < n; first += kSelThreads) {
             const int p = first + lane, c = p < n ? place(keys[p]) : 0;
             const int phys = c == 1 ? pt[p] : -1;
@@ -438,10 +416,6 @@ __global__ void __launch_bounds__(kSelThreads) sparse_select_kernel(const Select
         }
         __syncthreads();
         radix();
-    } else {  // all of `mid` are taken
-        floor_key = lowest;
-        open = 0;
-        left = n;
     }
 
     // Ascending order: warp w has pages w * per .. w * per + per - 1.
@@ -595,11 +569,10 @@ __global__ void __launch_bounds__(128) sparse_merge_kernel(const SparseArgs a, i
                a.out + static_cast<size_t>(row) * kHeadDim, a.neff ? a.neff + row : nullptr, real);
 }
 
-constexpr int kScoreSmem = kScoreRing * 2 * kScoreThreads * 16;
-constexpr int kFusedSmem = kScoreRing * 2 * kSelThreads * 16 + 2 * kFusedPages * 4;
+constexpr int kRingBytes = kScoreRing * 4 * kSelThreads * 16;
 
-struct Layout {  // the workspace: scores, keys (long rows), selected pages, partials
-    size_t keys, selected, partials, total;
+struct Layout {  // the workspace: keys (long rows), selected pages, partials
+    size_t selected, partials, total;
     int cluster, splits;  // CTAs of a cluster, clusters of a (sequence, kv head)
 };
 
@@ -616,8 +589,7 @@ Layout layout(int num_seqs, int max_pages, int keep, int Hq, int Hkv) {
            l.cluster * l.splits * kMaxSteps < pages)
         l.splits *= 2;
     auto pad = [](size_t x) { return (x + 15) / 16 * 16; };
-    l.keys = pad(heads * max_pages * 8);
-    l.selected = l.keys + (max_pages > kSelKeys ? pad(heads * max_pages * 4) : 0);
+    l.selected = max_pages > kSelKeys ? pad(heads * max_pages * 4) : 0;
     l.partials = l.selected + pad(heads * keep * 4);
     l.total = l.partials + (l.splits > 1 ? static_cast<size_t>(num_seqs) * Hq * l.splits *
                                                kPartialFloats * sizeof(float) : 0);
@@ -635,46 +607,25 @@ cudaError_t launch_all(const SparseLaunch &a, const CUtensorMap &map, const Layo
         e = cudaFuncSetAttribute(sparse_split_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kSmem);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(sparse_score_kernel<G>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(sparse_select_kernel<G, true>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kFusedSmem);
+            e = cudaFuncSetAttribute(sparse_select_kernel<G>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kRingBytes + kSelKeys * sizeof(uint32_t));
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
     char *ws = static_cast<char *>(a.workspace);
-    float2 *scores = reinterpret_cast<float2 *>(ws);
     int32_t *sel = a.selected ? a.selected : reinterpret_cast<int32_t *>(ws + l.selected);
     const uint4 *q = static_cast<const uint4 *>(a.q), *bounds = static_cast<const uint4 *>(a.bounds);
-    // Rows that may hold more pages than are kept are scored: long ones by a
-    // kernel of many blocks, short ones by the selection's own block.
-    const bool scored = a.max_pages > a.keep, fused = scored && a.max_pages <= kFusedPages;
-    if (scored && !fused) {
-        // Three blocks fit an SM; about six, since lengths differ.  A step is 32
-        // pages (16 for groups of eight heads).
-        const int step = kScoreThreads / (G == 8 ? 16 : 8);
-        const long long all = static_cast<long long>(a.num_seqs) * a.Hkv *
-                              ((a.max_pages + step - 1) / step);
-        const int per = step * static_cast<int>(
-            std::clamp<long long>(all / (148 * 6), 1, kScorePages / step));
-        sparse_score_kernel<G><<<dim3((a.max_pages + per - 1) / per, a.Hkv, a.num_seqs),
-                                 kScoreThreads, kScoreSmem, a.stream>>>(
-            q, bounds, a.page_table, a.seqlens, scores, a.num_pages, a.max_pages, a.Hkv, a.keep,
-            per);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-        count_launches(1);
-    }
-    SelectArgs s{q, bounds, scores, a.page_table, a.seqlens, sel,
-                 reinterpret_cast<uint32_t *>(ws + l.keys), a.num_pages, a.max_pages, a.Hkv,
-                 a.keep, a.status};
-    if (fused)
-        e = launch_ex(sparse_select_kernel<G, true>, dim3(a.Hkv, a.num_seqs), kSelThreads,
-                      kFusedSmem, 1, false, a.stream, s);
-    else
-        e = launch_ex(sparse_select_kernel<G, false>, dim3(a.Hkv, a.num_seqs), kSelThreads,
-                      std::min(a.max_pages, kSelKeys) * sizeof(uint32_t), 1, scored, a.stream, s);
+    SelectArgs s{q, bounds, a.page_table, a.seqlens, sel, reinterpret_cast<uint32_t *>(ws),
+                 a.num_pages, a.max_pages, a.Hkv, a.keep, a.status};
+    // Blocks of a row: enough for four on each SM, with two steps of the ring each.
+    const int step = kSelThreads / 4;
+    int blocks = 1;
+    while (blocks < kSelCluster && blocks * step * 2 < a.max_pages && a.max_pages > a.keep)
+        blocks *= 2;
+    const size_t held = std::min(a.max_pages, kSelKeys) * sizeof(uint32_t);
+    e = launch_ex(sparse_select_kernel<G>, dim3(blocks, a.Hkv, a.num_seqs), kSelThreads,
+                  kRingBytes + held, blocks, false, a.stream, s);
     if (e != cudaSuccess) return e;
     SparseArgs p;
     p.page_table = a.page_table; p.seqlens = a.seqlens; p.selected = sel;
