@@ -2,9 +2,9 @@
 // pages, shared by the tree and the page-selecting decode.
 //
 // A CTA has four computing warps; warp w takes tokens 16w .. 16w+15 of every page that
-// the CTA streams, for all of the CTA's rows.  Rows sit in m16 tiles of
-// mma.sync m16n8k16 (bf16 in, fp32 accumulate): lane (gq, tq) of a tile owns
-// rows gq and, with two row sets, gq + 8.  Each row keeps the method's state:
+// the CTA streams, for all of the CTA's rows.  Rows sit in an m16 tile of
+// mma.sync m16n8k16 (bf16 in, fp32 accumulate): lane (gq, tq) owns row gq and,
+// with two row sets, gq + 8.  Each row keeps the method's state:
 // reference max m_ref (log2 units, moved lazily), l, l2 (rescaled by r and
 // r^2 when it moves), the raw dots' sums S1, S2 and max, and the value
 // accumulator.  The S fragments are the P operand of the second product.
@@ -153,10 +153,10 @@ __device__ __forceinline__ void mask_values(uint32_t (&v)[4], uint32_t tok4) {
     v[3] = mask_pair(v[3], tok4 & 4u, tok4 & 8u);
 }
 
-// One page over the CTA's tiles.  mask: the page's valid tokens (the same for
+// One page over the CTA's rows.  mask: the page's valid tokens (the same for
 // every row).
-template <int MT, int kHR>
-__device__ __forceinline__ void page_step(RowTile<kHR> (&tile)[MT], uint32_t kb, uint32_t vb, int w,
+template <int kHR>
+__device__ __forceinline__ void page_step(RowTile<kHR> &tile, uint32_t kb, uint32_t vb, int w,
                                           int lane, uint64_t mask) {
     uint32_t kf[2][2][4];
     load_keys(kb, w, lane, kf);
@@ -165,20 +165,16 @@ __device__ __forceinline__ void page_step(RowTile<kHR> (&tile)[MT], uint32_t kb,
     uint32_t bits[kHR];
 #pragma unroll
     for (int hr = 0; hr < kHR; ++hr) bits[hr] = tok4;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        if (all)
-            tile[m].template score<true>(kf, bits);
-        else
-            tile[m].template score<false>(kf, bits);
-    }
+    if (all)
+        tile.template score<true>(kf, bits);
+    else
+        tile.template score<false>(kf, bits);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t v[4];
         load_values(vb, w, lane, i, v);
         if (!all) mask_values(v, tok4);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) tile[m].weigh(i, v);
+        tile.weigh(i, v);
     }
 }
 
@@ -319,34 +315,30 @@ __device__ __forceinline__ void finish_row(const RowState &x, int n, const Epilo
 
 // Writes each warp's states of all the CTA's rows to shared memory, one partial
 // per (row, warp): parts [rows][4][kPartialFloats].
-template <int MT, int kHR>
-__device__ __forceinline__ void spill_states(RowTile<kHR> (&tile)[MT], float *parts, int w,
-                                             int lane) {
+template <int kHR>
+__device__ __forceinline__ void spill_states(RowTile<kHR> &t, float *parts, int w, int lane) {
     const int gq = lane >> 2, tq = lane & 3;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int hr = 0; hr < kHR; ++hr) {
 #pragma unroll
-        for (int hr = 0; hr < kHR; ++hr) {
-            RowTile<kHR> &t = tile[m];
-#pragma unroll
-            for (int o = 1; o <= 2; o <<= 1) {
-                t.l[hr] += __shfl_xor_sync(0xffffffffu, t.l[hr], o);
-                t.l2[hr] += __shfl_xor_sync(0xffffffffu, t.l2[hr], o);
-                t.s1[hr] += __shfl_xor_sync(0xffffffffu, t.s1[hr], o);
-                t.s2[hr] += __shfl_xor_sync(0xffffffffu, t.s2[hr], o);
-                t.m_raw[hr] = fmaxf(t.m_raw[hr], __shfl_xor_sync(0xffffffffu, t.m_raw[hr], o));
-            }
-            float *p = parts + ((m * 8 * kHR + 8 * hr + gq) * 4 + w) * kPartialFloats;
-            if (tq == 0) {
-                *reinterpret_cast<float4 *>(p + 64) =
-                    make_float4(t.m_ref[hr], t.m_raw[hr], t.l[hr], t.l2[hr]);
-                *reinterpret_cast<float2 *>(p + 68) = make_float2(t.s1[hr], t.s2[hr]);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<float2 *>(p + 8 * i + 2 * tq) =
-                    make_float2(t.acc[i][2 * hr], t.acc[i][2 * hr + 1]);
+        for (int o = 1; o <= 2; o <<= 1) {
+            t.l[hr] += __shfl_xor_sync(0xffffffffu, t.l[hr], o);
+            t.l2[hr] += __shfl_xor_sync(0xffffffffu, t.l2[hr], o);
+            t.s1[hr] += __shfl_xor_sync(0xffffffffu, t.s1[hr], o);
+            t.s2[hr] += __shfl_xor_sync(0xffffffffu, t.s2[hr], o);
+            t.m_raw[hr] = fmaxf(t.m_raw[hr], __shfl_xor_sync(0xffffffffu, t.m_raw[hr], o));
         }
+        float *p = parts + ((8 * hr + gq) * 4 + w) * kPartialFloats;
+        if (tq == 0) {
+            *reinterpret_cast<float4 *>(p + 64) =
+                make_float4(t.m_ref[hr], t.m_raw[hr], t.l[hr], t.l2[hr]);
+            *reinterpret_cast<float2 *>(p + 68) = make_float2(t.s1[hr], t.s2[hr]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float2 *>(p + 8 * i + 2 * tq) =
+                make_float2(t.acc[i][2 * hr], t.acc[i][2 * hr + 1]);
+    }
 }
 
 // Reduces the rows' states over the CTA's warps and the cluster's CTAs and
@@ -354,12 +346,12 @@ __device__ __forceinline__ void spill_states(RowTile<kHR> (&tile)[MT], float *pa
 // the cluster (lanes past the last row get it with real = false).  parts:
 // 5 * kRows partials of shared memory, at the same place in every CTA; all
 // threads of the cluster are here.
-template <int MT, int kHR, typename Final>
-__device__ __forceinline__ void reduce_rows(RowTile<kHR> (&tile)[MT], float *parts, int nrows,
-                                            int w, int lane, Final &&fin) {
-    constexpr int kRows = 8 * kHR * MT;
+template <int kHR, typename Final>
+__device__ __forceinline__ void reduce_rows(RowTile<kHR> &tile, float *parts, int nrows, int w,
+                                            int lane, Final &&fin) {
+    constexpr int kRows = 8 * kHR;
     __syncthreads();  // the page ring is free
-    if (w < kRowWarps) spill_states<MT, kHR>(tile, parts, w, lane);
+    if (w < kRowWarps) spill_states(tile, parts, w, lane);
     __syncthreads();
     float *own = parts + kRows * 4 * kPartialFloats;
     const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());

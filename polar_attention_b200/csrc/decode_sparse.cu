@@ -491,10 +491,10 @@ sparse_split_kernel(const __grid_constant__ CUtensorMap kv_map, const SparseArgs
     const int p0 = min(static_cast<int>(blockIdx.x) * per, nsel);
     const int np = min(nsel, p0 + per) - p0;
 
-    RowTile<1> tile[1];
-    tile[0].clear();
+    RowTile<1> tile;
+    tile.clear();
     if (w < kRowWarps)
-        tile[0].load_row(0,
+        tile.load_row(0,
                          gq < G ? a.q + (static_cast<size_t>(seq) * a.Hq + g * G + gq) * kHeadDim
                                 : nullptr,
                          tq,
@@ -538,12 +538,12 @@ sparse_split_kernel(const __grid_constant__ CUtensorMap kv_map, const SparseArgs
         compute_steps(ring, np, lane, a.status, [&](int kk, int st) {
             const uint32_t kb = sbase + st * kStageBytes;
             if (ring.page[kk] >= 0)
-                page_step<1, 1>(tile, kb, kb + kChunkBytes, w, lane,
+                page_step(tile, kb, kb + kChunkBytes, w, lane,
                                 p0 + kk == nsel - 1 ? newest : ~0ull);
         });
     }
     let_next_kernel_start();
-    reduce_rows<1, 1>(tile, reinterpret_cast<float *>(smem), G, w, lane,
+    reduce_rows(tile, reinterpret_cast<float *>(smem), G, w, lane,
                       [&](int r, bool real, const RowState &x) {
         const size_t row = static_cast<size_t>(seq) * a.Hq + g * G + r;
         if (a.splits > 1)

@@ -20,19 +20,22 @@ namespace {
 
 constexpr int kSmem = kRingStages * kStageBytes + 1024;  // + alignment slack
 constexpr int kMaxCluster = 8;
+constexpr int kTcSteps = 8192;
 
 // CTA (part and row tile, kv head, sequence); the parts are equal shares of the
 // sequence's steps.  A cluster along x merges its CTAs' states; with one
-// cluster per row tile it writes the rows, else partials.
-template <int G, int MT, int kHR>
-__global__ void __launch_bounds__(kRowThreads)
+// cluster per row tile it writes the rows, else partials.  Tiles of 8 or 16
+// rows: 32 rows read a page half as often but left half as many CTAs for the
+// same work (1 sequence of 1500 tokens, 64 rows: 16.5 us, 16 rows 12.4).
+template <int G, int kHR>
+__global__ void __launch_bounds__(kRowThreads, kHR == 2 ? 3 : 4)
 tree_split_kernel(const __grid_constant__ CUtensorMap kv_map,
                   const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map, const TreeArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    constexpr int kRows = 8 * kHR * MT;
+    constexpr int kRows = 8 * kHR;
     __shared__ __align__(8) PageRing ring;
     // The rows' states go to the page ring once every page is consumed.
     static_assert(5 * kRows * kPartialFloats * sizeof(float) <= kRingStages * kStageBytes,
@@ -75,7 +78,7 @@ tree_split_kernel(const __grid_constant__ CUtensorMap kv_map,
     const uint32_t sbase = smem_u32(smem);
     const uint64_t drafted = first_tokens(nodes);
     const uint64_t *masks = a.mask + static_cast<size_t>(seq) * a.tree;
-    RowTile<kHR> tile[MT];
+    RowTile<kHR> tile;
     if (w == kRowWarps) {
         if (lane == 0)
             copy_steps(ring, np, a.status, [&](int kk, int st, uint64_t *bar) {
@@ -98,30 +101,27 @@ tree_split_kernel(const __grid_constant__ CUtensorMap kv_map,
         __syncwarp();
     }
     const bool computes = w < kRowWarps;
+    tile.clear();
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        tile[m].clear();
-#pragma unroll
-        for (int hr = 0; hr < kHR; ++hr) {
-            const int r = row0 + m * 8 * kHR + 8 * hr + gq;
-            const int t = r / G, hh = r % G;
-            const bool real = computes && r < R;
-            const int n = real ? len + __popcll(masks[t] & drafted) : 0;
-            tile[m].load_row(hr,
-                             real ? a.q + ((static_cast<size_t>(seq) * a.tree + t) * a.Hq + g * G +
-                                           hh) * kHeadDim
-                                  : nullptr,
-                             tq,
-                             a.ep.s * length_temperature(static_cast<float>(n), a.ep.alpha, a.ep.L) *
-                                 kLog2e);
-        }
+    for (int hr = 0; hr < kHR; ++hr) {
+        const int r = row0 + 8 * hr + gq;
+        const int t = r / G, hh = r % G;
+        const bool real = computes && r < R;
+        const int n = real ? len + __popcll(masks[t] & drafted) : 0;
+        tile.load_row(hr,
+                      real ? a.q + ((static_cast<size_t>(seq) * a.tree + t) * a.Hq + g * G + hh) *
+                                       kHeadDim
+                           : nullptr,
+                      tq,
+                      a.ep.s * length_temperature(static_cast<float>(n), a.ep.alpha, a.ep.L) *
+                          kLog2e);
     }
 
     if (computes) compute_steps(ring, np, lane, a.status, [&](int kk, int st) {
         const uint32_t kb = sbase + st * kStageBytes, vb = kb + kChunkBytes;
         if (p0 + kk < npg) {
             if (ring.page[kk] >= 0)
-                page_step<MT, kHR>(tile, kb, vb, w, lane, first_tokens(len - (p0 + kk) * kPage));
+                page_step(tile, kb, vb, w, lane, first_tokens(len - (p0 + kk) * kPage));
         } else {
             // The drafted rows: a mask for each row.  A value row that is not
             // finite may count only for the rows that see it, and a product
@@ -131,16 +131,13 @@ tree_split_kernel(const __grid_constant__ CUtensorMap kv_map,
             uint32_t kf[2][2][4];
             load_keys(kb, w, lane, kf);
             const uint32_t tok4 = lane_tokens(drafted, w, tq);
+            uint32_t bits[kHR];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                uint32_t bits[kHR];
-#pragma unroll
-                for (int hr = 0; hr < kHR; ++hr) {
-                    const int r = row0 + m * 8 * kHR + 8 * hr + gq;
-                    bits[hr] = r < R ? lane_tokens(masks[r / G] & drafted, w, tq) : 0u;
-                }
-                tile[m].template score<false>(kf, bits);
+            for (int hr = 0; hr < kHR; ++hr) {
+                const int r = row0 + 8 * hr + gq;
+                bits[hr] = r < R ? lane_tokens(masks[r / G] & drafted, w, tq) : 0u;
             }
+            tile.template score<false>(kf, bits);
             bool odd = false;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -153,33 +150,30 @@ tree_split_kernel(const __grid_constant__ CUtensorMap kv_map,
                     odd |= lo | hi;
                     v[e] = mask_pair(v[e], !lo, !hi);
                 }
-#pragma unroll
-                for (int m = 0; m < MT; ++m) tile[m].weigh(i, v);
+                tile.weigh(i, v);
             }
             if (__any_sync(0xffffffffu, odd)) {
                 const uint8_t *vs = smem + st * kStageBytes + kChunkBytes;
                 for (int j = 16 * w; j < min(16 * w + 16, nodes); ++j)
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
+                    for (int hr = 0; hr < kHR; ++hr) {
+                        const int r = row0 + 8 * hr + gq;
+                        if (r >= R || !(masks[r / G] >> j & 1)) continue;
 #pragma unroll
-                        for (int hr = 0; hr < kHR; ++hr) {
-                            const int r = row0 + m * 8 * kHR + 8 * hr + gq;
-                            if (r >= R || !(masks[r / G] >> j & 1)) continue;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const uint32_t x = *reinterpret_cast<const uint32_t *>(
-                                    vs + swz(j, i) + 4 * tq);
-                                if (not_finite(x))
-                                    tile[m].acc[i][2 * hr] += __uint_as_float(x << 16);
-                                if (not_finite(x >> 16))
-                                    tile[m].acc[i][2 * hr + 1] += __uint_as_float(x & 0xffff0000u);
-                            }
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t x =
+                                *reinterpret_cast<const uint32_t *>(vs + swz(j, i) + 4 * tq);
+                            if (not_finite(x))
+                                tile.acc[i][2 * hr] += __uint_as_float(x << 16);
+                            if (not_finite(x >> 16))
+                                tile.acc[i][2 * hr + 1] += __uint_as_float(x & 0xffff0000u);
                         }
+                    }
             }
         }
     });
     let_next_kernel_start();
-    reduce_rows<MT, kHR>(tile, reinterpret_cast<float *>(smem), min(kRows, R - row0), w, lane,
+    reduce_rows(tile, reinterpret_cast<float *>(smem), min(kRows, R - row0), w, lane,
                          [&](int r, bool real, const RowState &x) {
         const int t = (row0 + r) / G, h = g * G + (row0 + r) % G;
         const size_t row = (static_cast<size_t>(seq) * a.tree + t) * a.Hq + h;
@@ -209,7 +203,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeArgs a, long 
                a.neff ? a.neff + row : nullptr, real);
 }
 
-template <int G, int MT, int kHR>
+template <int G, int kHR>
 cudaError_t launch_split(const CUtensorMap &kv, const CUtensorMap &k, const CUtensorMap &v,
                          const TreeArgs &t, const TreePlan &plan, int num_seqs,
                          cudaStream_t stream) {
@@ -219,12 +213,12 @@ cudaError_t launch_split(const CUtensorMap &kv, const CUtensorMap &k, const CUte
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(configured.load() & bit)) {
-        e = cudaFuncSetAttribute(tree_split_kernel<G, MT, kHR>,
+        e = cudaFuncSetAttribute(tree_split_kernel<G, kHR>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
-    return launch_ex(tree_split_kernel<G, MT, kHR>,
+    return launch_ex(tree_split_kernel<G, kHR>,
                      dim3(plan.cluster * plan.splits * plan.row_tiles, t.Hkv, num_seqs),
                      kRowThreads, kSmem, plan.cluster, false, stream, kv, k, v, t);
 }
@@ -233,37 +227,51 @@ template <int G>
 cudaError_t launch_split_rows(const CUtensorMap &kv, const CUtensorMap &k, const CUtensorMap &v,
                               const TreeArgs &t, const TreePlan &plan, int num_seqs,
                               cudaStream_t stream) {
-    if (plan.tile_rows == 8) return launch_split<G, 1, 1>(kv, k, v, t, plan, num_seqs, stream);
-    if (plan.tile_rows == 16) return launch_split<G, 1, 2>(kv, k, v, t, plan, num_seqs, stream);
-    return launch_split<G, 2, 2>(kv, k, v, t, plan, num_seqs, stream);
+    if (plan.tile_rows == 8) return launch_split<G, 1>(kv, k, v, t, plan, num_seqs, stream);
+    return launch_split<G, 2>(kv, k, v, t, plan, num_seqs, stream);
 }
 
 TreePlan tree_plan(int num_seqs, int max_pages, int tree, int Hq, int Hkv) {
     TreePlan p;
     const int R = Hq / Hkv * tree;
-    p.tile_rows = R <= 8 ? 8 : R <= 16 ? 16 : 32;
+    p.tile_rows = R <= 8 ? 8 : 16;
     p.row_tiles = (R + p.tile_rows - 1) / p.tile_rows;
     const long long tiles = static_cast<long long>(num_seqs) * Hkv * p.row_tiles;
     const int steps = max_pages + 1;
     p.cluster = 1;
-    while (p.cluster < kMaxCluster && tiles * p.cluster < 148 * 4 && p.cluster * 2 <= steps)
+    // No more CTAs than fit at once: 512 of which 444 fit took 19.4 us, 256 of them
+    // 10.3 (16 sequences of 200 .. 400 tokens, 16 rows).
+    const int at_once = 148 * (p.tile_rows == 8 ? 4 : 3);
+    while (p.cluster < kMaxCluster && tiles * p.cluster * 2 <= at_once && p.cluster * 2 <= steps)
         p.cluster *= 2;
     p.splits = 1;
-    while ((tiles * p.cluster * p.splits * 2 <= 148 * 8 && p.cluster * p.splits * 16 <= steps) ||
+    while ((tiles * p.cluster * p.splits * 2 <= at_once && p.cluster * p.splits * 16 <= steps) ||
            p.cluster * p.splits * kMaxSteps < steps)
         p.splits *= 2;
     return p;
 }
 
-// Above 32 rows the 128-row tiles of the tensor cores are faster, though most of
-// a tile may be padding.
-bool uses_tc(int tree, int Hq, int Hkv) { return Hq / Hkv * tree > 32; }
+// Rows of more than one m16 tile read every page again here; the 128-row tiles of
+// tcgen05 read it once, though most of a tile may be padding and its pipeline
+// takes longer to fill.  Up to 16 rows this kernel is faster at any size (16
+// sequences of 4096 .. 16384 tokens, 4 kv heads, 16 rows: 55 us, tcgen05 65).
+// Above, it depends on the steps over all m16 tiles (us here, us by tcgen05):
+//   rows 32, 1 sequence of 1500: 10.7, 20.5; of 16000 (4000 steps): 22.6, 24.4
+//   rows 128, 1 sequence of 8000 (4100): 21.4, 24.7; of 16000 (8000): 32.8, 28.8
+//   rows 64, 16 sequences of 500 .. 2000 (8400): 30.8, 31.4
+//   rows 24, 1 sequence of 60000 (7500): 33.0, 37.0; rows 64 (15000): 54, 43
+//   rows 32, 16 sequences of 4096 .. 16384 (33000): 98, 65.
+bool uses_tc(int num_seqs, int max_pages, int tree, int Hq, int Hkv) {
+    const int R = Hq / Hkv * tree;
+    return R > 16 &&
+           static_cast<long long>(num_seqs) * Hkv * ((R + 15) / 16) * (max_pages + 1) >= kTcSteps;
+}
 
 }  // namespace
 
 size_t tree_workspace_bytes(int num_seqs, int max_pages, int tree, int Hq, int Hkv) {
-    if (uses_tc(tree, Hq, Hkv))
-        return tree_tc_workspace_bytes(tree_tc_ctas(num_seqs, max_pages, tree, Hq, Hkv));
+    if (uses_tc(num_seqs, max_pages, tree, Hq, Hkv))
+        return tree_tc_workspace_bytes(num_seqs, max_pages, tree, Hq, Hkv);
     const TreePlan p = tree_plan(num_seqs, max_pages, tree, Hq, Hkv);
     if (p.splits == 1) return 16;  // none is used
     return static_cast<size_t>(num_seqs) * tree * Hq * p.splits * kPartialFloats * sizeof(float);
@@ -303,7 +311,7 @@ cudaError_t launch_decode_tree(const TreeLaunch &a) {
     const float L = static_cast<float>(a.L);
     t.ep = Epilogue{a.s, a.alpha, L, a.beta, 1.0f / logf(L)};
     cudaError_t e;
-    if (uses_tc(a.tree, a.Hq, a.Hkv)) {
+    if (uses_tc(a.num_seqs, a.max_pages, a.tree, a.Hq, a.Hkv)) {
         count_launches(2);
         return launch_tree_tc(kv, k, v, t,
                               tree_tc_ctas(a.num_seqs, a.max_pages, a.tree, a.Hq, a.Hkv), a.stream);

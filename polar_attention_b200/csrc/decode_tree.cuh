@@ -28,7 +28,7 @@ struct TreePlan {  // the mma.sync kernel's grid
 // The tcgen05 kernel (128-row tiles): its CTAs, the workspace they need, and
 // the launch, given the tensor maps over the page pool and the drafted rows.
 int tree_tc_ctas(int num_seqs, int max_pages, int tree, int Hq, int Hkv);
-size_t tree_tc_workspace_bytes(int ctas);
+size_t tree_tc_workspace_bytes(int num_seqs, int max_pages, int tree, int Hq, int Hkv);
 cudaError_t launch_tree_tc(const CUtensorMap &kv, const CUtensorMap &k, const CUtensorMap &v,
                            const TreeArgs &t, int ctas, cudaStream_t stream);
 

@@ -10,25 +10,30 @@
 // holds whole it finishes, of a tile it shares it stores the rows' states, which
 // tree_tc_merge_kernel joins (at most two such tiles a CTA: its first and last).
 //
-// A step goes in two halves of 32 keys, in two buffers that take turns:
-//   S = Q K^T   tcgen05.mma M=128 N=32 K=64, operands in shared memory
-//   P, stats    one thread per row reads its scores from tensor memory, keeps
-//               max, l, l2, S1 and S2 in registers and writes the weights back
-//               as bf16 (P lies in its S's columns)
-//   O += P V    tcgen05.mma M=128 N=64 K=32, P from tensor memory
-// While the softmax warps work on one half, the other's product and the next
-// scores in its buffer are formed.  128 columns (S0 S1 O) and three 16 KB stages
-// are all a CTA needs: three share an SM.  What bounds the kernel is the
-// exponentials (16 an SM and clock: 512 clocks a step of a full tile).  Measured
-// on the widest tree (64 nodes, 8 sequences of 32K-64K): eight softmax warps a
-// CTA, two CTAs an SM and clusters of eight 330 us; one 64-key buffer, four CTAs
-// and equal shares 268 us; the two half buffers XXX us.
+// A step is a page, 64 keys:
+//   S = Q K^T   tcgen05.mma M=128 N=64 K=64, operands in shared memory
+//   P, stats    one thread per row reads its scores from tensor memory 32 at a
+//               time, keeps max, l, l2, S1 and S2 in registers and writes the
+//               weights back as bf16 (P lies in S's columns)
+//   O += P V    tcgen05.mma M=128 N=64 K=64, P from tensor memory
+// A CTA's step is one chain; 128 columns (S, O) and two 16 KB stages are all it
+// needs, so four CTAs share an SM and cover each other's waits.
+//
+// What bounds it (64 nodes, 8 sequences of 32K-64K, 228 us): per SM and step of a
+// full tile about 1200 clocks, of which the products alone take 750 (measured with
+// the softmax left out: their operands' reads, at N=64) and the softmax warps'
+// instructions about as much (16 exponentials an SM and clock are 512 of them); the
+// two overlap only as far as the four chains are out of step.  Measured besides:
+// two threads a row in clusters of eight CTAs, two an SM, 310-330 us; equal shares
+// with a 64-key buffer and one thread for copies and products 268 us, with two
+// 32-key buffers 255 us, with 128-key steps and two CTAs an SM 283 us; before the
+// rotation of partial tiles 257 us; two 64-key buffers and two CTAs an SM 235 us.
 //
 // The reference max of a row moves only when a logit exceeds it by more than
-// 2^24 (kTcThreshold): weights are formed against the one at hand in the pass
-// that finds the scores' max, and only where that was too low they are formed
-// again, and O rescaled in tensor memory by the row's thread once the product
-// before is done.
+// 2^24 (kTcThreshold), and then to a whole number of log2 units: weights are
+// formed against the one at hand in the pass that finds the scores' max, and only
+// where that was too low they are formed again, and O and the step's weights so
+// far multiplied by a power of two in tensor memory by the row's thread.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -41,9 +46,9 @@ namespace polar {
 namespace {
 
 constexpr int kTileRows = 128;
-constexpr int kStagesTc = 3;
+constexpr int kStagesTc = 2;
 constexpr int kTcThreads = 192;  // four softmax warps, one that copies, one that issues products
-constexpr int kTcPerSm = 3;
+constexpr int kTcPerSm = 4;
 constexpr int kQBytes = kTileRows * kHeadDim * 2;
 constexpr int kSmemTc = kQBytes + kStagesTc * kStageBytes + 1024;  // + alignment slack
 constexpr uint32_t kColS = 0, kColO = 64;
@@ -67,8 +72,13 @@ __device__ __forceinline__ void tmem_dealloc_128(uint32_t taddr) {
 constexpr int kMinShare = 4;
 constexpr int kMergeThreads = 256;
 
-constexpr size_t tc_tiles_bytes(int ctas) {
-    return (static_cast<size_t>(ctas) * 7 * sizeof(int) + 15) / 16 * 16;
+// Tiles that the sequences can have.
+int num_tiles(int num_seqs, int tree, int Hq, int Hkv) {
+    return num_seqs * Hkv * ((Hq / Hkv * tree + kTileRows - 1) / kTileRows);
+}
+
+constexpr size_t record_bytes(int tiles) {
+    return (static_cast<size_t>(tiles) * 3 * sizeof(int) + 15) / 16 * 16;
 }
 
 // One pass over a thread's 32 scores against its reference max: the weights
@@ -102,15 +112,40 @@ __device__ __forceinline__ TileSums tile_pass(const uint32_t (&sr)[32], uint32_t
     return TileSums{fmaxf(mx[0], mx[1]), a1.x + a1.y, a2.x + a2.y, la.x + la.y, l2a.x + l2a.y};
 }
 
+// 16 n columns of fp32 of this thread's lane of tensor memory, times r.
+__device__ __forceinline__ void scale_columns(uint32_t t, int n, float r) {
+#pragma unroll 1
+    for (int c = 0; c < n; ++c) {
+        uint32_t o[16];
+        tmem_ld16(t + 16 * c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
+        tmem_st16(t + 16 * c, o);
+    }
+}
+
+// The weights of a step's first half (16 columns of bf16 pairs), times a power
+// of two.
+__device__ __forceinline__ void scale_weights(uint32_t t, float r) {
+    uint32_t o[16];
+    tmem_wait_st();
+    tmem_ld16(t, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        o[e] = pack_bf16(__uint_as_float(o[e] << 16) * r, __uint_as_float(o[e] & 0xffff0000u) * r);
+    tmem_st16(t, o);
+}
+
 struct RowStats {  // one row's streaming state, in its thread
     float m_ref, m_raw, l, l2, s1, s2;
 };
 
-// What a share's last tile leaves to the merge: where a shared tile begins.
+// What the CTA in which a tile begins leaves to the merge.
 struct SharedTile {
-    int seq, head, row0, parts;  // parts 0: none begins here
-    int slot;                    // of the first part; part j > 0: slot 2 (cta + j)
-    int nodes, len;              // of the sequence
+    int parts;      // CTAs that hold steps of the tile; 1: it is finished
+    int cta, slot;  // part 0 is in this slot, part j > 0 in slot 2 (cta + j)
 };
 
 // A share of the steps, tile by tile.
@@ -171,7 +206,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *ring = smem + kQBytes;
-    __shared__ __align__(8) uint64_t q_full, q_empty, full[kStagesTc], empty[kStagesTc], s_full[2], p_ready[2], pv_done[2], mma_done;
+    __shared__ __align__(8) uint64_t q_full, q_empty, full[kStagesTc], empty[kStagesTc], s_full, p_ready, pv_done, mma_done;
     __shared__ unsigned long long odd_nodes;  // drafted nodes with values that are not finite
     __shared__ uint32_t tmem_base_sh;
     __shared__ long long wide[kTcThreads / 32];
@@ -186,11 +221,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
             mbar_init(&full[st], 1);
             mbar_init(&empty[st], 1);
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&s_full[b], 1);
-            mbar_init(&p_ready[b], 4);
-            mbar_init(&pv_done[b], 1);
-        }
+        mbar_init(&s_full, 1);
+        mbar_init(&p_ready, 4);
+        mbar_init(&pv_done, 1);
         mbar_init(&mma_done, 1);
         odd_nodes = 0;
         fence_barrier_init();
@@ -210,10 +243,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
     for (int i = 0; i < kTcThreads / 32; ++i) all += wide[i];
     const long long share = max((all + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinShare));
     const long long first = min(cta * share, all), count = min(share, all - first);
-    if (count == 0) {
-        if (threadIdx.x == 0) shared_tiles[cta].parts = 0;
-        return;
-    }
+    if (count == 0) return;
     long long before = 0;
     for (int s0 = 0; s0 < a.num_seqs; s0 += kTcThreads) {
         const int s = s0 + threadIdx.x;
@@ -247,21 +277,19 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
     walk.tile = static_cast<int>(s_offset / walk.per_tile);
     walk.step = static_cast<int>(s_offset % walk.per_tile);
     if (threadIdx.x == 0) {
-        // The tile that begins here and goes on in the next shares, if any: the last.
+        // The tiles that begin here.
         Walk<G> x = walk;
-        SharedTile t{0, 0, 0, 0, 2 * cta, 0, 0};
         long long done = 0;
         for (; x.left > 0; x.next()) {
-            if (x.step == 0 && x.left < x.per_tile) {
+            if (x.step == 0) {
                 const long long end = first + done + x.per_tile;  // the step behind the tile
-                t.seq = x.seq; t.head = x.head(); t.row0 = x.row0();
-                t.nodes = x.nodes; t.len = x.len;
-                t.parts = static_cast<int>((end - 1) / share) - cta + 1;
-                t.slot = 2 * cta + (done > 0);
+                const SharedTile t{static_cast<int>((end - 1) / share) - cta + 1, cta,
+                                   2 * cta + (done > 0)};
+                shared_tiles[(static_cast<size_t>(x.seq) * a.Hkv + x.head()) * a.row_tiles +
+                             x.row0() / kTileRows] = t;
             }
             done += x.count();
         }
-        shared_tiles[cta] = t;
     }
 
     int it = 0;     // steps so far, for the barriers' phases
@@ -316,7 +344,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
     } else if (w == 5) {
         // ------------------------------------------- products (one thread)
         if (lane == 0) {
-            constexpr uint32_t idesc_qk = idesc_bf16(kTileRows, kPage / 2, false);
+            constexpr uint32_t idesc_qk = idesc_bf16(kTileRows, kPage, false);
             constexpr uint32_t idesc_pv = idesc_bf16(kTileRows, kHeadDim, true);
             // Q and K are K-major (SBO 1024), V is MN-major (one 64-column atom).
             const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
@@ -326,54 +354,34 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
             const uint32_t o = tmem + kColO;
             bool ok = true;
             int tiles = 0;
-            // Scores of half h of the step in stage st: its keys 32 h .. 32 h + 31.
-            auto scores = [&](int st, int h) {
-                const uint32_t d = tmem + kColS + 32 * h, ka = k_lo + st * kStep + 256 * h;
-                mma_ss2<0>(d, q_lo, hi, ka, hi, idesc_qk);
-                mma_ss2<1>(d, q_lo + 2, hi, ka + 2, hi, idesc_qk);
-                mma_ss2<1>(d, q_lo + 4, hi, ka + 4, hi, idesc_qk);
-                mma_ss2<1>(d, q_lo + 6, hi, ka + 6, hi, idesc_qk);
-                tc_commit(&s_full[h]);
-            };
             int st = 0, phase = 0;  // stage and parity of step `it`
             for (; ok && walk.left > 0; walk.next(), ++tiles) {
                 const int n = walk.count();
                 if (!(ok = mbar_wait(&q_full, tiles & 1, a.status))) break;
-                if (!(ok = mbar_wait(&full[st], phase, a.status))) break;
-                tc_fence_after();
-                scores(st, 0);
-                scores(st, 1);
-                if (n == 1) tc_commit(&q_empty);
                 for (int j = 0; j < n; ++j, ++it) {
-                    const int st1 = st + 1 == kStagesTc ? 0 : st + 1;
-                    const int phase1 = st1 == 0 ? phase ^ 1 : phase;
-                    const uint32_t va = v_lo + st * kStep;
-                    if (!(ok = mbar_wait(&p_ready[0], it & 1, a.status))) break;
+                    if (!(ok = mbar_wait(&full[st], phase, a.status))) break;
+                    // The scores overwrite the weights of the step before.
+                    if (it > 0 && !(ok = mbar_wait(&pv_done, (it - 1) & 1, a.status))) break;
                     tc_fence_after();
-                    mma_ts2(o, tmem + kColS, va, hi, idesc_pv, j > 0);
-                    mma_ts2(o, tmem + kColS + 8, va + 128, hi, idesc_pv, 1u);
-                    tc_commit(&pv_done[0]);
-                    // A buffer's next scores overwrite its P.
-                    if (j + 1 < n) {
-                        if (!(ok = mbar_wait(&full[st1], phase1, a.status))) break;
-                        if (!(ok = mbar_wait(&pv_done[0], it & 1, a.status))) break;
-                        tc_fence_after();
-                        scores(st1, 0);
-                    }
-                    if (!(ok = mbar_wait(&p_ready[1], it & 1, a.status))) break;
+                    const uint32_t d = tmem + kColS, ka = k_lo + st * kStep, va = v_lo + st * kStep;
+                    mma_ss2<0>(d, q_lo, hi, ka, hi, idesc_qk);
+                    mma_ss2<1>(d, q_lo + 2, hi, ka + 2, hi, idesc_qk);
+                    mma_ss2<1>(d, q_lo + 4, hi, ka + 4, hi, idesc_qk);
+                    mma_ss2<1>(d, q_lo + 6, hi, ka + 6, hi, idesc_qk);
+                    tc_commit(&s_full);
+                    if (j == n - 1) tc_commit(&q_empty);
+                    if (!(ok = mbar_wait(&p_ready, it & 1, a.status))) break;
                     tc_fence_after();
-                    mma_ts2(o, tmem + kColS + 32, va + 256, hi, idesc_pv, 1u);
-                    mma_ts2(o, tmem + kColS + 40, va + 384, hi, idesc_pv, 1u);
-                    tc_commit(&pv_done[1]);
+                    mma_ts2(o, d, va, hi, idesc_pv, j > 0);
+                    mma_ts2(o, d + 8, va + 128, hi, idesc_pv, 1u);
+                    mma_ts2(o, d + 16, va + 256, hi, idesc_pv, 1u);
+                    mma_ts2(o, d + 24, va + 384, hi, idesc_pv, 1u);
+                    tc_commit(&pv_done);
                     tc_commit(&empty[st]);
-                    if (j + 1 < n) {
-                        if (!(ok = mbar_wait(&pv_done[1], it & 1, a.status))) break;
-                        tc_fence_after();
-                        scores(st1, 1);
-                        if (j + 2 == n) tc_commit(&q_empty);
+                    if (++st == kStagesTc) {
+                        st = 0;
+                        phase ^= 1;
                     }
-                    st = st1;
-                    phase = phase1;
                 }
             }
             // All products complete before tensor memory is freed.
@@ -403,58 +411,52 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                                                           a.ep.L) * kLog2e;
             const int32_t *pt = a.page_table + static_cast<size_t>(walk.seq) * a.max_pages;
             RowStats x{-INFINITY, -INFINITY, 0.f, 0.f, 0.f, 0.f};
-            // Half h of step `it` (the tile's first half: O holds nothing yet).
-            // kAll: every row sees all of its keys; else the bits of `mask`.
-            auto half_step = [&](auto kAll, int h, uint32_t mask, bool first) {
-                ok = mbar_wait(&s_full[h], it & 1, a.status);
+            // Step `it` (`first`: the tile's, O holds nothing yet).  kAll: every row
+            // sees all of its keys; else the bits of `mask`.
+            auto soft_step = [&](auto kAll, uint64_t mask, bool first) {
+                ok = mbar_wait(&s_full, it & 1, a.status);
                 if (!__all_sync(~0u, ok)) { ok = false; return; }
                 tc_fence_after();
                 if (active) {
-                    uint32_t pk[16];
-                    TileSums t;
-                    while (true) {
-                        uint32_t sr[32];
-                        tmem_ld32(tS + 32 * h, sr);
-                        tmem_wait_ld();
-                        const float ref = x.m_ref == -INFINITY ? 0.f : x.m_ref;
-                        t = tile_pass<decltype(kAll)::value>(sr, mask, cl2, ref, pk);
-                        const float zmax = t.top * cl2;
-                        const bool need = zmax > x.m_ref + kTcThreshold;
-                        if (!__any_sync(~0u, need)) break;
-                        // The reference was too low for some row: move it, rescale
-                        // what it holds (by 0 where nothing was seen before), and
-                        // form the weights again.
-                        const float r = need ? exp2f(x.m_ref - zmax) : 1.f;
-                        x.l *= r;
-                        x.l2 *= r * r;
-                        if (need) x.m_ref = zmax;
-                        if (first) continue;
-                        // O *= r, once the product before is done.
-                        ok = mbar_wait(&pv_done[h ^ 1], (it + h + 1) & 1, a.status);
-                        if (!__all_sync(~0u, ok)) { ok = false; return; }
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t o[16];
-                            tmem_ld16(tO + 16 * c, o);
-                            tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
-                            tmem_st16(tO + 16 * c, o);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[16];
+                        TileSums t;
+                        while (true) {
+                            uint32_t sr[32];
+                            tmem_ld32(tS + 32 * h, sr);
+                            tmem_wait_ld();
+                            const float ref = x.m_ref == -INFINITY ? 0.f : x.m_ref;
+                            t = tile_pass<decltype(kAll)::value>(
+                                sr, static_cast<uint32_t>(mask >> (32 * h)), cl2, ref, pk);
+                            const float zmax = t.top * cl2;
+                            const bool need = zmax > x.m_ref + kTcThreshold;
+                            if (!__any_sync(~0u, need)) break;
+                            // The reference was too low for some row: move it,
+                            // rescale what it holds, by a power of two (0 where
+                            // nothing was seen before), and form the weights again.
+                            const float to = ceilf(zmax);
+                            const float r = need ? exp2f(x.m_ref - to) : 1.f;
+                            x.l *= r;
+                            x.l2 *= r * r;
+                            if (need) x.m_ref = to;
+                            // (The product before is done: its weights lay where
+                            // these scores do.)
+                            if (!first) scale_columns(tO, 4, r);
+                            if (h > 0) scale_weights(tS, r);
                         }
+                        x.m_raw = fmaxf(x.m_raw, t.top);
+                        x.s1 += t.s1;
+                        x.s2 += t.s2;
+                        x.l += t.l;
+                        x.l2 += t.l2;
+                        tmem_st16(tS + 16 * h, pk);
                     }
-                    x.m_raw = fmaxf(x.m_raw, t.top);
-                    x.s1 += t.s1;
-                    x.s2 += t.s2;
-                    x.l += t.l;
-                    x.l2 += t.l2;
-                    tmem_st16(tS + 32 * h, pk);
                     tmem_wait_st();
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_ready[h]);
+                if (lane == 0) mbar_arrive(&p_ready);
             };
             for (int j0 = 0; ok && j0 < cnt; j0 += 32) {
                 const int p = s0 + j0 + lane;
@@ -464,8 +466,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                 for (int j = j0; ok && j < j1; ++j, ++it) {
                     const bool skip = bad >> (j - j0) & 1u;  // a page outside the pool
                     if (j < full_pages && !skip) {
-                        half_step(std::true_type{}, 0, ~0u, j == 0);
-                        if (ok) half_step(std::true_type{}, 1, ~0u, false);
+                        soft_step(std::true_type{}, ~0ull, j == 0);
                         continue;
                     }
                     const bool draft = s0 + j == npg;
@@ -506,15 +507,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                     if (odd) atomicOr(&odd_nodes, static_cast<unsigned long long>(odd) << (16 * w));
                     fence_proxy_async_smem();
                     __syncwarp();
-#pragma unroll 1
-                    for (int h = 0; ok && h < 2; ++h)
-                        half_step(std::false_type{}, h, static_cast<uint32_t>(mask >> (32 * h)),
-                                  j == 0 && h == 0);
+                    soft_step(std::false_type{}, mask, j == 0);
                 }
             }
             if (!ok) break;
             // The tile's last product.
-            ok = mbar_wait(&pv_done[1], (it - 1) & 1, a.status);
+            ok = mbar_wait(&pv_done, (it - 1) & 1, a.status);
             if (!__all_sync(~0u, ok)) { ok = false; break; }
             tc_fence_after();
             if (!active) continue;
@@ -598,42 +596,43 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
     if (w == 5) tmem_dealloc_128(tmem);
 }
 
-// Rows of the tiles that several CTAs share: block (CTA in which the tile begins,
-// 32 rows), eight lanes a row.  A tile of many parts gives each row four groups
-// of eight lanes instead, whose states are then joined, and takes four rounds.
+// Rows of the tiles that several CTAs share: block (tile, some of its rows).
+// A row's parts go to `shares` groups of eight lanes, whose states are then
+// joined; the host takes more shares where there are few tiles of many parts, so
+// that about as many blocks do the work (1 sequence of 60000 tokens, 48 rows: one
+// group of eight lanes per row 94 us in all, this 43).
 template <int G>
 __global__ void __launch_bounds__(kMergeThreads)
-tree_tc_merge_kernel(const TreeArgs a, const SharedTile *__restrict__ shared_tiles) {
+tree_tc_merge_kernel(const TreeArgs a, const SharedTile *__restrict__ shared_tiles, int shares) {
     constexpr int kGroups = kMergeThreads / 8;
     __shared__ __align__(16) float joined[kGroups][kPartialFloats];
+    const int tile = blockIdx.x, rt = tile % a.row_tiles, head = tile / a.row_tiles % a.Hkv;
+    const int seq = tile / a.row_tiles / a.Hkv, row0 = rt * kTileRows;
+    const int nodes = tree_nodes(a.seqlens, a.tree_lens, seq, a.tree, a.max_pages);
+    const int per_block = kGroups / shares, r0 = per_block * blockIdx.y;
+    const int rows = min(G * nodes - row0, kTileRows);
     wait_for_previous_kernel();
-    const int cta = blockIdx.x;
-    const SharedTile t = shared_tiles[cta];
-    const int rows = min(G * t.nodes - t.row0, kTileRows), r0 = kGroups * blockIdx.y;
-    if (t.parts == 0 || r0 >= rows) return;
-    const int shares = t.parts > 16 ? 4 : 1, per_round = kGroups / shares;
-    const int group = threadIdx.x >> 3, share = group / per_round;
-    for (int round = 0; round < shares; ++round) {
-        const int at = r0 + round * per_round;
-        if (at >= rows) break;
-        const int r = at + group % per_round, row = min(r, rows - 1);
-        const int node = (t.row0 + row) / G, h = t.head * G + (t.row0 + row) % G;
-        const size_t seq_node = static_cast<size_t>(t.seq) * a.tree + node;
-        const int n = t.len + __popcll(a.mask[seq_node] & first_tokens(t.nodes));
-        RowState x = merge_parts((t.parts - share + shares - 1) / shares, [&](int k) {
-            const int j = shares * k + share;
-            const size_t slot = j == 0 ? t.slot : 2 * (cta + j);
-            return a.partials + slot * kSlotFloats + row * kPartialFloats;
-        });
-        if (shares > 1) {
-            __syncthreads();  // the round before is read
-            store_part(x, joined[group], true);
-            __syncthreads();
-            x = merge_parts(shares, [&](int k) { return joined[group % per_round + k * per_round]; });
-        }
-        finish_row(x, n, a.ep, a.u + h * kHeadDim, a.out + (seq_node * a.Hq + h) * kHeadDim,
-                   a.neff ? a.neff + seq_node * a.Hq + h : nullptr, share == 0 && r < rows);
+    if (r0 >= rows) return;  // also a tile that no sequence has
+    const SharedTile t = shared_tiles[tile];
+    if (t.parts == 1) return;
+    const int group = threadIdx.x >> 3, share = group / per_block, r = r0 + group % per_block;
+    const int row = min(r, rows - 1);
+    const int node = (row0 + row) / G, h = head * G + (row0 + row) % G;
+    const size_t seq_node = static_cast<size_t>(seq) * a.tree + node;
+    const int n = a.seqlens[seq] + __popcll(a.mask[seq_node] & first_tokens(nodes));
+    RowState x = merge_parts(share < t.parts ? (t.parts - share + shares - 1) / shares : 0,
+                             [&](int k) {
+        const int j = shares * k + share;
+        const size_t slot = j == 0 ? t.slot : 2 * (t.cta + j);
+        return a.partials + slot * kSlotFloats + row * kPartialFloats;
+    });
+    if (shares > 1) {
+        store_part(x, joined[group], true);
+        __syncthreads();
+        x = merge_parts(shares, [&](int k) { return joined[group % per_block + k * per_block]; });
     }
+    finish_row(x, n, a.ep, a.u + h * kHeadDim, a.out + (seq_node * a.Hq + h) * kHeadDim,
+               a.neff ? a.neff + seq_node * a.Hq + h : nullptr, share == 0 && r < rows);
 }
 
 template <int G>
@@ -650,30 +649,35 @@ cudaError_t launch_tc(const CUtensorMap &q, const CUtensorMap &kv, const CUtenso
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
-    // The workspace: the CTAs' shared tiles, then two slots of row states each.
-    SharedTile *tiles = reinterpret_cast<SharedTile *>(t.partials);
+    // The workspace: the tiles' records, then two slots of row states for each CTA.
+    const int tiles = num_tiles(t.num_seqs, t.tree, t.Hq, t.Hkv);
+    SharedTile *records = reinterpret_cast<SharedTile *>(t.partials);
     TreeArgs a = t;
-    a.partials = t.partials + tc_tiles_bytes(ctas) / sizeof(float);
+    a.partials = t.partials + record_bytes(tiles) / sizeof(float);
+    a.row_tiles = (G * t.tree + kTileRows - 1) / kTileRows;
     e = launch_ex(tree_tc_kernel<G>, dim3(ctas), kTcThreads, kSmemTc, 1, false, stream, q, kv, k, v,
-                  a, tiles);
+                  a, records);
     if (e != cudaSuccess) return e;
-    const int rows = std::min(G * t.tree, kTileRows);
-    return launch_ex(tree_tc_merge_kernel<G>, dim3(ctas, (8 * rows + kMergeThreads - 1) / kMergeThreads), kMergeThreads, 0, 1,
-                     true, stream, a,
-                     static_cast<const SharedTile *>(tiles));
+    int shares = 1;  // of the parts of a row: four each
+    while (shares < kMergeThreads / 8 && shares * 8 * tiles <= ctas) shares *= 2;
+    const int rows = std::min(G * t.tree, kTileRows), per_block = kMergeThreads / 8 / shares;
+    return launch_ex(tree_tc_merge_kernel<G>, dim3(tiles, (rows + per_block - 1) / per_block),
+                     kMergeThreads, 0, 1, true, stream, a,
+                     static_cast<const SharedTile *>(records), shares);
 }
 
 }  // namespace
 
 int tree_tc_ctas(int num_seqs, int max_pages, int tree, int Hq, int Hkv) {
-    const long long tiles = static_cast<long long>(num_seqs) * Hkv *
-                            ((Hq / Hkv * tree + kTileRows - 1) / kTileRows);
-    const long long most = (tiles * (max_pages + 1ll) + kMinShare - 1) / kMinShare;
+    const long long most = (num_tiles(num_seqs, tree, Hq, Hkv) * (max_pages + 1ll) + kMinShare - 1) /
+                           kMinShare;
     return static_cast<int>(std::min<long long>(148 * kTcPerSm, most));
 }
 
-size_t tree_tc_workspace_bytes(int ctas) {
-    return tc_tiles_bytes(ctas) + static_cast<size_t>(2 * ctas) * kSlotFloats * sizeof(float);
+size_t tree_tc_workspace_bytes(int num_seqs, int max_pages, int tree, int Hq, int Hkv) {
+    return record_bytes(num_tiles(num_seqs, tree, Hq, Hkv)) +
+           static_cast<size_t>(2 * tree_tc_ctas(num_seqs, max_pages, tree, Hq, Hkv)) * kSlotFloats *
+               sizeof(float);
 }
 
 cudaError_t launch_tree_tc(const CUtensorMap &kv, const CUtensorMap &k, const CUtensorMap &v,
