@@ -141,6 +141,71 @@ def test_shared_tails(cuda_ok):
     p.grow([1, 1, 1, 1])
 
 
+def test_many_rows_share_tails(cuda_ok):
+    """More rows than one launch plans and copies: forks of few rows, grown."""
+    N = 300
+    p = Pair(700, 1, N, 3, seed=13)
+    p.grow([70, 10, 64] + [0] * (N - 3))
+    p.fork(np.arange(N) % 3)
+    p.grow(np.arange(N) % 5 % 3)
+    p.fork(np.arange(N)[::-1] // 2)
+    got = p.reserve(np.ones(N, np.int32))
+    assert got.all()
+    p.append(got)
+    p.fork(np.zeros(N, np.int32))
+    p.host.refs[p.host.refs == 0] = 9  # no free page
+    p.dev.refs.copy_(torch.from_numpy(p.host.refs.astype(np.int32)))
+    assert not p.reserve(np.ones(N, np.int32), status=NO_PAGES).any()
+
+
+def test_pages_past_32_bits(cuda_ok):
+    """The last pages of a pool of more than 2^32 bytes and 2^31 values."""
+    P, Hkv, N, T = 70000, 4, 3, 150
+    cache = pa.PageCache(torch.zeros((P, 2, Hkv, 64, 64), dtype=torch.bfloat16, device="cuda"),
+                         torch.ones(P, dtype=torch.int32, device="cuda"),
+                         torch.zeros((P, Hkv, 2, 64), dtype=torch.bfloat16, device="cuda"))
+    small = pa.PageCache(torch.zeros((20, 2, Hkv, 64, 64), dtype=torch.bfloat16, device="cuda"),
+                         torch.zeros(20, dtype=torch.int32, device="cuda"),
+                         torch.zeros((20, Hkv, 2, 64), dtype=torch.bfloat16, device="cuda"))
+    cache.refs[P - 20:] = 0
+    rng = np.random.default_rng(14)
+    k, v = unit(rng, 2, 2 * N, T, Hkv, 64).cuda().unbind(0)
+    k, v = k.contiguous(), v.contiguous()
+    q = unit(rng, 2 * N, 9, 16, 64).cuda()
+    mask = torch.tensor([2 ** (t + 1) - 1 for t in range(9)]).repeat(2 * N, 1).cuda()
+    u = torch.zeros((16, 64), device="cuda")
+
+    def run(c, max_pages):
+        def rows():
+            return (torch.full((2 * N, max_pages), -1, dtype=torch.int32, device="cuda"),
+                    torch.zeros(2 * N, dtype=torch.int32, device="cuda"))
+        (t0, l0), (t, n) = rows(), rows()
+        grow = torch.tensor([T] * N + [0] * N, dtype=torch.int32).cuda()
+        got = pa.cache_reserve(c, t0, l0, grow)
+        pa.cache_append(c, k, v, t0, l0, got)
+        src = (torch.arange(2 * N) % N).int().cuda()
+        pa.cache_fork(c, t0, l0, src, t, n)
+        pa.cache_free(c, t0, l0)
+        got = pa.cache_reserve(c, t, n, torch.full((2 * N,), 2, dtype=torch.int32).cuda())
+        pa.cache_append(c, k, v, t, n, got)  # N copies of tails
+        def decodes():
+            return [*pa.decode_paged_tree(q, k[:, :9].contiguous(), v[:, :9].contiguous(), mask,
+                                          c.kv_pages, t, n, u),
+                    *pa.decode_paged_sparse(q[:, 0].contiguous(), c.kv_pages, c.bounds, t, n, u, 2)]
+        first = decodes()
+        top = t.max().item()
+        c.refs[:-20] = 0  # the others' pages
+        used = pa.cache_compact(c, t, n).item()
+        assert used == 4 * N and t.max().item() == used - 1 and (c.refs[used:] == 0).all()
+        return first, decodes(), top
+
+    want, wagain, _ = run(small, 3)
+    got, again, top = run(cache, 3)
+    assert pa.get_status() == OK and top == P - 20 + 4 * N - 1
+    for a, b, c, d in zip(want, wagain, got, again):
+        assert torch.equal(a, b) and torch.equal(a, c) and torch.equal(a, d)
+
+
 def test_pool_runs_out(cuda_ok):
     """From the first row that cannot be served on, no row is; what was served
     is whole, and a row that needs no page waits with the others."""

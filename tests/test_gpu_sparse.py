@@ -119,6 +119,42 @@ def test_ties_go_to_the_lower_page(cuda_ok):
     assert sel[0, 0].tolist() == [0, 1, 2, 30] and sel[1, 1].tolist() == [0, 1, 2, 11]
 
 
+def test_many_ties(cuda_ok):
+    """More pages in question than get exact scores one by one; some above them."""
+    x = inputs([64 * 500 + 5], 8, 2, seed=11)
+    x["bounds"][:] = x["bounds"][0].clone()
+    above = [400, 7, 130]
+    x["bounds"][x["table"][0, above].long()] *= 2
+    for keep in (1, 3, 100, 400):
+        out, neff, sel = call(cuda(x), keep)
+        assert pa.get_status() == 0
+        check(x, keep, out, neff, sel)
+
+
+def test_scores_closer_than_their_roundings(cuda_ok):
+    """Bounds whose large terms cancel: the order is in the small ones, below the
+    rounding of an fp32 sum."""
+    x = inputs([64 * 300], 2, 2, seed=12)
+    x["q"][:], x["bounds"][:] = 0, 0
+    x["q"][..., :3] = torch.tensor([1.0, 1.0, 2.0 ** -26]).bfloat16()
+    g = torch.Generator().manual_seed(0)
+    x["bounds"][..., 0], x["bounds"][..., 1] = 3.0, -3.0
+    small = torch.randperm(300, generator=g)[:, None].expand(300, 2)
+    x["bounds"][:, :, 1, 2] = (small % 256).bfloat16()  # ties, too
+    for keep in (5, 80):
+        out, neff, sel = call(cuda(x), keep)
+        check(x, keep, out, neff, sel)
+
+
+def test_longer_than_the_shared_keys(cuda_ok):
+    """A sequence whose scores do not fit in shared memory beside a short one."""
+    x = inputs([64 * 10500 + 9, 200], 4, 1, seed=13)
+    for keep in (3, 300):
+        out, neff, sel = call(cuda(x), keep, L=2048)
+        assert pa.get_status() == 0
+        check(x, keep, out, neff, sel, L=2048)
+
+
 def test_scores_that_are_not_finite(cuda_ok):
     """A NaN score ranks above every number, an infinite one where it belongs."""
     x = inputs([64 * 20], 8, 2, seed=6)

@@ -93,15 +93,21 @@ def check(x, out, neff, tree_lens, rows=None, what="", **kw):
                  list(refs.values()), what)
 
 
+# Columns of a page table.  Above 16 rows per kv head a wide table's call runs on
+# the tensor cores' 128-row tiles; up to 16 rows it is split over many CTAs.
+WIDE = 5000
+
+
 # Rows per kv head from one to 512, in and across row tiles.
+@pytest.mark.parametrize("max_pages", [13, WIDE])
 @pytest.mark.parametrize("G,M", [(1, 1), (4, 1), (2, 3), (8, 1), (4, 3), (2, 8), (1, 17), (4, 8),
                                  (8, 5), (1, 64), (4, 17), (2, 63), (4, 33), (8, 17), (4, 64),
                                  (8, 64)])
-def test_small_ragged(cuda_ok, G, M):
+def test_small_ragged(cuda_ok, G, M, max_pages):
     """Lengths of zero, one, a page's edge and several splits, with node counts
     from none to all of a padded batch."""
     lens = [0, 1, 63, 64, 65, 130, 700, 0]
-    x = inputs(lens, M, 2 * G, 2, seed=G * 100 + M, max_pages=13)
+    x = inputs(lens, M, 2 * G, 2, seed=G * 100 + M, max_pages=max_pages)
     rng = np.random.default_rng(M)
     tl = rng.integers(0, M + 1, len(lens)).astype(np.int32)
     tl[[0, 5]], tl[7] = M, min(1, M)
@@ -118,40 +124,65 @@ def test_all_nodes_without_lens(cuda_ok):
     check(x, out, neff, [5, 5])
 
 
-def test_long_many_splits(cuda_ok):
+@pytest.mark.parametrize("M", [1, 2, 4, 5, 23])
+def test_long_many_splits(cuda_ok, M):
     """Tens of thousands of cached tokens over many splits, temperature active;
     a sample of rows."""
-    x = inputs([40001, 5000], 23, 16, 4, seed=5)
+    x = inputs([40001, 5000], M, 16, 4, seed=5)
     out, neff = call(cuda(x), L=2048)
     assert pa.get_status() == 0
     rng = np.random.default_rng(0)
-    rows = {(int(rng.integers(2)), int(rng.integers(23)), int(rng.integers(16)))
-            for _ in range(24)} | {(0, 22, 15), (1, 0, 0)}
-    check(x, out, neff, [23, 23], rows, L=2048)
+    rows = {(int(rng.integers(2)), int(rng.integers(M)), int(rng.integers(16)))
+            for _ in range(24)} | {(0, M - 1, 15), (1, 0, 0)}
+    check(x, out, neff, [M, M], rows, L=2048)
 
 
-def test_high_scale(cuda_ok):
+@pytest.mark.parametrize("G,M", [(1, 3), (4, 9), (2, 64)])
+def test_many_sequences_few_with_work(cuda_ok, G, M):
+    """A padded batch: most sequences have no nodes, some of those that have see
+    no cache."""
+    rng = np.random.default_rng(14)
+    lens, tl = np.zeros(400, np.int64), np.zeros(400, np.int32)
+    busy = np.sort(rng.choice(400, 12, replace=False))
+    lens[busy], tl[busy] = rng.integers(0, 300, 12), rng.integers(1, M + 1, 12)
+    lens[rng.choice(400, 50)] = 130  # cached, without nodes
+    x = inputs(lens, M, 2 * G, 2, seed=14, max_pages=40)
+    d = cuda(x)
+    out = torch.full_like(d["q"], 7.0)
+    neff = torch.full(out.shape[:3], 7.0, device="cuda")
+    pa.decode_paged_tree(d["q"], d["k"], d["v"], d["mask"], d["kv"], d["table"], d["lens"], d["u"],
+                         out, neff, tree_lens=torch.from_numpy(tl).cuda(), **ARGS)
+    assert pa.get_status() == 0
+    check(x, out, neff, tl)
+    behind = torch.arange(M)[None] >= torch.from_numpy(tl)[:, None]
+    assert (out[behind.cuda()] == 7).all() and (neff[behind.cuda()] == 7).all()
+
+
+@pytest.mark.parametrize("max_pages", [5, WIDE])
+def test_high_scale(cuda_ok, max_pages):
     """Logits up to 60: weights over a range of 2^170."""
-    x = inputs([300, 70], 20, 8, 2, seed=6)
+    x = inputs([300, 70], 20, 8, 2, seed=6, max_pages=max_pages)
     out, neff = call(cuda(x), s=60.0)
     check(x, out, neff, [20, 20], s=60.0)
 
 
-def test_rows_that_see_nothing(cuda_ok):
+@pytest.mark.parametrize("G,max_pages", [(4, 2), (4, WIDE), (8, WIDE)])
+def test_rows_that_see_nothing(cuda_ok, G, max_pages):
     """No cache and an empty mask: zeros; an empty mask over a cache: the cache
     alone; bits past the node count are ignored."""
     masks = np.zeros((3, 4), np.int64)
     masks[1] = [1, 0, 7 << 1, -1]
     masks[2] = -16  # bits 4 and up only
-    x = inputs([0, 0, 70], 4, 8, 2, seed=7, masks=masks)
+    x = inputs([0, 0, 70], 4, 2 * G, 2, seed=7, masks=masks, max_pages=max_pages)
     out, neff = call(cuda(x))
     assert pa.get_status() == 0
     check(x, out, neff, [4, 4, 4])
     assert not out[0].any() and not neff[0].any() and not out[1, 1].any()
 
 
-def test_rows_behind_a_sequence_are_left(cuda_ok):
-    x = inputs([10, 200, 0], 6, 8, 2, seed=8)
+@pytest.mark.parametrize("max_pages", [4, WIDE])
+def test_rows_behind_a_sequence_are_left(cuda_ok, max_pages):
+    x = inputs([10, 200, 0], 6, 8, 2, seed=8, max_pages=max_pages)
     d = cuda(x)
     tl = torch.tensor([2, 0, 6], dtype=torch.int32).cuda()
     out = torch.full_like(d["q"], 7.0)
@@ -165,14 +196,15 @@ def test_rows_behind_a_sequence_are_left(cuda_ok):
     check(x, out, neff, [2, 0, 6])
 
 
-@pytest.mark.parametrize("G,M", [(4, 2), (4, 8), (4, 40)])
+@pytest.mark.parametrize("G,M,max_pages", [(4, 2, 2), (4, 8, 2), (4, 40, 2), (2, 9, WIDE),
+                                           (4, 40, WIDE)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_what_is_not_seen_does_not_count(cuda_ok, G, M, bad):
+def test_what_is_not_seen_does_not_count(cuda_ok, G, M, max_pages, bad):
     """Stale rows behind the cache's end and behind a sequence's nodes, and a
     drafted node that only some rows see: their values, finite or not, reach
     the rows that see them and no others."""
     lens, tl = [70, 5], [M, M - 1]
-    x = inputs(lens, M, 2 * G, 2, seed=9)
+    x = inputs(lens, M, 2 * G, 2, seed=9, max_pages=max_pages)
     for i, n in enumerate(lens):
         page = x["table"][i, n // 64]
         x["kv"][page, :, :, n % 64:] = bad
@@ -192,11 +224,12 @@ def test_what_is_not_seen_does_not_count(cuda_ok, G, M, bad):
             assert not torch.isfinite(out[0, t]).all()
 
 
+@pytest.mark.parametrize("max_pages", [3, WIDE])
 @pytest.mark.parametrize("M", [2, 9, 40])
-def test_values_not_finite_reach_their_rows(cuda_ok, M):
+def test_values_not_finite_reach_their_rows(cuda_ok, M, max_pages):
     """A finite key with a value that is infinite in one column: the rows that
     see it have no direction there, the others do not notice."""
-    x = inputs([130], M, 8, 2, seed=10)
+    x = inputs([130], M, 8, 2, seed=10, max_pages=max_pages)
     clean = {k: t.clone() for k, t in x.items()}
     x["v"][0, M - 1, :, 5] = float("inf")
     out, neff = call(cuda(x))
@@ -226,11 +259,12 @@ def test_chain_is_a_chunk(cuda_ok):
     check(x, want, nwant, [C], L=2048)
 
 
-def test_twice_and_captured(cuda_ok):
+@pytest.mark.parametrize("max_pages", [11, WIDE])
+def test_twice_and_captured(cuda_ok, max_pages):
     """The same bits twice, on another stream, and from a replayed graph whose
     lengths, masks and drafts change between replays."""
-    x = inputs([700, 64, 3], 12, 16, 4, seed=11)
-    y = inputs([600, 1, 128], 12, 16, 4, seed=12, max_pages=11)
+    x = inputs([700, 64, 3], 12, 16, 4, seed=11, max_pages=max_pages)
+    y = inputs([600, 1, 128], 12, 16, 4, seed=12, max_pages=max_pages)
     d = cuda(x)
     a, na = call(d)
     b, nb = call(d)
@@ -255,15 +289,16 @@ def test_twice_and_captured(cuda_ok):
     check({**y, "u": x["u"]}, o, no, [12, 12, 12])
 
 
-def test_bad_pages_and_lengths_are_reported(cuda_ok):
-    x = inputs([130, 130, 130, 50], 3, 8, 2, seed=13)
+@pytest.mark.parametrize("M,max_pages", [(3, 3), (3, WIDE), (30, WIDE)])
+def test_bad_pages_and_lengths_are_reported(cuda_ok, M, max_pages):
+    x = inputs([130, 130, 130, 50], M, 8, 2, seed=13, max_pages=max_pages)
     x["table"][1, 1] = 10 ** 6
     d = cuda(x)
     call(d)
     assert pa.get_status() == 4
-    for field, value in (("lens", 10 ** 5), ("lens", -1), ("nodes", 4), ("nodes", -1)):
-        d = cuda(inputs([130, 130, 130, 50], 3, 8, 2, seed=13))
-        tl = torch.full((4,), 3, dtype=torch.int32).cuda()
+    for field, value in (("lens", 10 ** 6), ("lens", -1), ("nodes", M + 1), ("nodes", -1)):
+        d = cuda(inputs([130, 130, 130, 50], M, 8, 2, seed=13, max_pages=max_pages))
+        tl = torch.full((4,), M, dtype=torch.int32).cuda()
         (d["lens"] if field == "lens" else tl)[2] = value
         out = torch.full_like(d["q"], 7.0)
         pa.decode_paged_tree(d["q"], d["k"], d["v"], d["mask"], d["kv"], d["table"], d["lens"],
@@ -271,3 +306,27 @@ def test_bad_pages_and_lengths_are_reported(cuda_ok):
         assert pa.get_status() == 7, (field, value)
         assert (out[2] == 7).all() and (out[[0, 1, 3]] != 7).any(-1).all()
     assert pa.get_status() == 0
+
+
+def test_two_graphs_and_eager_calls(cuda_ok):
+    """Two captured graphs replayed at once on two streams, and calls between
+    them: each has its own workspace."""
+    x = [inputs([5000, 900], M, 16, 4, seed=M, max_pages=500) for M in (4, 30)]
+    d = [cuda(t) for t in x]
+    want = [call(t) for t in d]
+    graphs, got, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for t in d:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.append(call(t))
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        again = [call(t) for t in d]
+    torch.cuda.synchronize()
+    assert pa.get_status() == 0
+    for w, *others in zip(want, got, again):
+        assert all(torch.equal(w[i], o[i]) for o in others for i in (0, 1))
