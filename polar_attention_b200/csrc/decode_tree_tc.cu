@@ -19,15 +19,19 @@
 // A CTA's step is one chain; 128 columns (S, O) and two 16 KB stages are all it
 // needs, so four CTAs share an SM and cover each other's waits.
 //
-// What bounds it (64 nodes, 8 sequences of 32K-64K, 228 us): per SM and step of a
-// full tile about 1200 clocks, of which the products alone take 750 (measured with
-// the softmax left out: their operands' reads, at N=64) and the softmax warps'
-// instructions about as much (16 exponentials an SM and clock are 512 of them); the
-// two overlap only as far as the four chains are out of step.  Measured besides:
-// two threads a row in clusters of eight CTAs, two an SM, 310-330 us; equal shares
-// with a 64-key buffer and one thread for copies and products 268 us, with two
-// 32-key buffers 255 us, with 128-key steps and two CTAs an SM 283 us; before the
-// rotation of partial tiles 257 us; two 64-key buffers and two CTAs an SM 235 us.
+// What bounds it (64 nodes, 8 sequences of 32K-64K, 216 us): per SM and step of a
+// full tile about 1100 clocks.  Alone on its SM a chain takes 2100 for a step: 270
+// and 180 to issue the products, about 300 until each is seen, 900 for the weights
+// and sums, of which 512 are exponentials (16 an SM and clock), 200 to reach tensor
+// memory and back.  Four chains come to 1100, not to a quarter of 2100: products,
+// weights and issue slots are each taken for 45 % of the time, and wait for one
+// another.  Loads do not bound it (half of them left out, or all from one page: the
+// same time).  Measured besides: two threads a row in clusters of eight CTAs, two an
+// SM, 310-330 us; equal shares with a 64-key buffer and one thread for copies and
+// products 268 us, with two 32-key buffers 255 us, with 128-key steps and two CTAs
+// an SM 283 us; two 64-key buffers and two CTAs an SM 235 us; three chains with the
+// next scores formed during a step's weights (160 columns a chain, one CTA of 480
+// threads) 230-240 us.
 //
 // The reference max of a row moves only when a logit exceeds it by more than
 // 2^24 (kTcThreshold), and then to a whole number of log2 units: weights are
@@ -66,6 +70,15 @@ __device__ __forceinline__ void tmem_alloc_128(uint32_t *dst_smem) {
 }
 __device__ __forceinline__ void tmem_dealloc_128(uint32_t taddr) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(taddr) : "memory");
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
 }
 
 // Steps that a share has at least.
@@ -342,53 +355,64 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
         }
         __syncwarp();
     } else if (w == 5) {
-        // ------------------------------------------- products (one thread)
-        if (lane == 0) {
-            constexpr uint32_t idesc_qk = idesc_bf16(kTileRows, kPage, false);
-            constexpr uint32_t idesc_pv = idesc_bf16(kTileRows, kHeadDim, true);
-            // Q and K are K-major (SBO 1024), V is MN-major (one 64-column atom).
-            const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
-            const uint32_t k_lo = sdesc_lo(smem_u32(ring), 16);
-            const uint32_t v_lo = sdesc_lo(smem_u32(ring) + kChunkBytes, 8192);
-            constexpr uint32_t hi = kSdescHi128B, kStep = kStageBytes >> 4;
-            const uint32_t o = tmem + kColO;
-            bool ok = true;
-            int tiles = 0;
-            int st = 0, phase = 0;  // stage and parity of step `it`
-            for (; ok && walk.left > 0; walk.next(), ++tiles) {
-                const int n = walk.count();
-                if (!(ok = mbar_wait(&q_full, tiles & 1, a.status))) break;
-                for (int j = 0; j < n; ++j, ++it) {
-                    if (!(ok = mbar_wait(&full[st], phase, a.status))) break;
-                    // The scores overwrite the weights of the step before.
-                    if (it > 0 && !(ok = mbar_wait(&pv_done, (it - 1) & 1, a.status))) break;
-                    tc_fence_after();
-                    const uint32_t d = tmem + kColS, ka = k_lo + st * kStep, va = v_lo + st * kStep;
+        // ---------------------------------------------------------- products
+        // The warp goes through the loop as one, so that what the instructions
+        // take from its registers is the same in all lanes, and one lane issues: two
+        // products of four instructions take 450 clocks to issue (in a branch of one
+        // lane 760).
+        constexpr uint32_t idesc_qk = idesc_bf16(kTileRows, kPage, false);
+        constexpr uint32_t idesc_pv = idesc_bf16(kTileRows, kHeadDim, true);
+        // Q and K are K-major (SBO 1024), V is MN-major (one 64-column atom).
+        const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
+        const uint32_t k_lo = sdesc_lo(smem_u32(ring), 16);
+        const uint32_t v_lo = sdesc_lo(smem_u32(ring) + kChunkBytes, 8192);
+        constexpr uint32_t hi = kSdescHi128B, kStep = kStageBytes >> 4;
+        const uint32_t t = __shfl_sync(~0u, tmem, 0), o = t + kColO;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(~0u, mbar_wait(bar, parity, a.status)) != 0;
+        };
+        bool ok = true;
+        int tiles = 0;
+        int st = 0, phase = 0;  // stage and parity of step `it`
+        for (; ok && walk.left > 0; walk.next(), ++tiles) {
+            const int n = walk.count();
+            if (!(ok = wait(&q_full, tiles & 1))) break;
+            for (int j = 0; j < n; ++j, ++it) {
+                if (!(ok = wait(&full[st], phase))) break;
+                // The scores overwrite the weights of the step before.
+                if (it > 0 && !(ok = wait(&pv_done, (it - 1) & 1))) break;
+                tc_fence_after();
+                const uint32_t d = t + kColS, ka = k_lo + st * kStep, va = v_lo + st * kStep;
+                if (elect_one()) {
                     mma_ss2<0>(d, q_lo, hi, ka, hi, idesc_qk);
                     mma_ss2<1>(d, q_lo + 2, hi, ka + 2, hi, idesc_qk);
                     mma_ss2<1>(d, q_lo + 4, hi, ka + 4, hi, idesc_qk);
                     mma_ss2<1>(d, q_lo + 6, hi, ka + 6, hi, idesc_qk);
                     tc_commit(&s_full);
                     if (j == n - 1) tc_commit(&q_empty);
-                    if (!(ok = mbar_wait(&p_ready, it & 1, a.status))) break;
-                    tc_fence_after();
+                }
+                __syncwarp();
+                if (!(ok = wait(&p_ready, it & 1))) break;
+                tc_fence_after();
+                if (elect_one()) {
                     mma_ts2(o, d, va, hi, idesc_pv, j > 0);
                     mma_ts2(o, d + 8, va + 128, hi, idesc_pv, 1u);
                     mma_ts2(o, d + 16, va + 256, hi, idesc_pv, 1u);
                     mma_ts2(o, d + 24, va + 384, hi, idesc_pv, 1u);
                     tc_commit(&pv_done);
                     tc_commit(&empty[st]);
-                    if (++st == kStagesTc) {
-                        st = 0;
-                        phase ^= 1;
-                    }
+                }
+                __syncwarp();
+                if (++st == kStagesTc) {
+                    st = 0;
+                    phase ^= 1;
                 }
             }
-            // All products complete before tensor memory is freed.
-            tc_commit(&mma_done);
-            mbar_wait(&mma_done, 0, a.status);
         }
+        // All products complete before tensor memory is freed.
+        if (elect_one()) tc_commit(&mma_done);
         __syncwarp();
+        wait(&mma_done, 0);
     } else {
         // ------------------------------------------------- softmax warps
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * w) << 16);
