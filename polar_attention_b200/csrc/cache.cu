@@ -314,8 +314,11 @@ __device__ __forceinline__ uint4 shfl8(uint4 a, int o) {
 // Block (touched page of the row and kv head, row): thread (row r0 of 16, vector
 // c of 8) moves rows r0, r0 + 16, ... of the page.  The heads of a page are
 // neighbours, since a token's rows of all heads lie together in k and v.  Rows
-// before the first new token are read back where the bounds need them.
-__global__ void __launch_bounds__(128) cache_append_kernel(const AppendArgs a) {
+// before the first new token are read back where the bounds need them.  Bound by
+// memory: 405 MB in 71 us (5.7 TB/s), the rows read and written once and so kept
+// out of the caches' way (plain loads and stores: 73.2 us; without the bound on
+// registers, 8 or 16 blocks an SM: 73.6, 77 and 74.5).
+__global__ void __launch_bounds__(128, 12) cache_append_kernel(const AppendArgs a) {
     __shared__ uint4 part[2][4][kRowVecs];
     const int i = blockIdx.y, g = blockIdx.x % a.Hkv, touched = blockIdx.x / a.Hkv;
     const int len = a.lens[i], cnt = a.counts ? a.counts[i] : a.tokens;
@@ -354,8 +357,8 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendArgs a) {
             } else {
                 const size_t at =
                     ((static_cast<size_t>(i) * a.src_tokens + from) * a.Hkv + g) * kRowVecs + c;
-                kx[e] = __ldg(a.k + at);
-                vx[e] = __ldg(a.v + at);
+                kx[e] = __ldcs(a.k + at);
+                vx[e] = __ldcs(a.v + at);
             }
         }
         if (have[e] && !write[e] && a.bounds) kx[e] = kp[r * kRowVecs + c];
@@ -363,8 +366,8 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
         if (write[e]) {
-            kp[(r0 + 16 * e) * kRowVecs + c] = kx[e];
-            vp[(r0 + 16 * e) * kRowVecs + c] = vx[e];
+            __stcs(kp + (r0 + 16 * e) * kRowVecs + c, kx[e]);
+            __stcs(vp + (r0 + 16 * e) * kRowVecs + c, vx[e]);
         }
     if (!a.bounds) return;
     const uint32_t inf = 0x7f807f80u, ninf = 0xff80ff80u;
@@ -538,29 +541,29 @@ __global__ void __launch_bounds__(kPlanThreads) cache_compact_plan_kernel(const 
 }
 
 // Copies the movers' pages, laid end to end, 32 KB at a time (eight vectors a
-// thread in flight), then rewrites references and tables.
+// thread in flight), then rewrites references and tables.  Bound by memory: 1.07 GB
+// moved and read in 168 us (6.4 TB/s).  Many short blocks: 8 an SM that loop took
+// 178 us, 32 an SM 171, 256 an SM 172.
 __global__ void __launch_bounds__(256) cache_compact_move_kernel(const CompactArgs a) {
     wait_for_previous_kernel();
     const int moves = a.head[0];
-    const int page_vecs = 2 * a.Hkv * kPage * kRowVecs;  // a multiple of 1024
-    const long long vecs = static_cast<long long>(moves) * page_vecs;
-    for (long long v0 = static_cast<long long>(blockIdx.x) * 2048; v0 < vecs;
-         v0 += static_cast<long long>(gridDim.x) * 2048) {
-        uint4 x[8];
+    const int units = moves * a.Hkv;  // of 16 KB: Hkv of them a page
+    for (int u0 = 2 * blockIdx.x; u0 < units; u0 += 2 * gridDim.x) {
+        uint4 x[2][4];
+        size_t to[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {  // the 256 threads' vectors lie in one page
-            const long long v = v0 + 256 * e;
-            if (v < vecs)
-                x[e] = __ldcs(a.kv + static_cast<size_t>(a.src[v / page_vecs]) * page_vecs +
-                              v % page_vecs + threadIdx.x);
+        for (int h = 0; h < 2; ++h) {
+            const int u = min(u0 + h, units - 1), k = u / a.Hkv, at = u % a.Hkv;
+            const uint4 *from = a.kv + (static_cast<size_t>(a.src[k]) * a.Hkv + at) * 1024;
+            to[h] = (static_cast<size_t>(a.dst[k]) * a.Hkv + at) * 1024 + threadIdx.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[h][e] = __ldcs(from + 256 * e + threadIdx.x);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const long long v = v0 + 256 * e;
-            if (v < vecs)
-                __stcs(a.kv + static_cast<size_t>(a.dst[v / page_vecs]) * page_vecs + v % page_vecs +
-                           threadIdx.x, x[e]);
-        }
+        for (int h = 0; h < 2; ++h)
+            if (u0 + h < units)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) __stcs(a.kv + to[h] + 256 * e, x[h][e]);
     }
     const int per = 2 * a.Hkv * kRowVecs;  // vectors of a page's bounds
     for (long long u = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
@@ -672,7 +675,10 @@ cudaError_t launch_cache_compact(const CacheLaunch &a, int32_t *used) {
                               kCompactCluster, false, a.stream, c);
     if (e != cudaSuccess) return e;
     count_launches(2);
-    return launch_ex(cache_compact_move_kernel, dim3(148 * 8), 256, 0, 1, true, a.stream, c);
+    // At most half of the pages move.
+    const int blocks = static_cast<int>(
+        std::min<long long>(148 * 64, static_cast<long long>(a.num_pages) * a.Hkv / 4 + 1));
+    return launch_ex(cache_compact_move_kernel, dim3(blocks), 256, 0, 1, true, a.stream, c);
 }
 
 }  // namespace polar
