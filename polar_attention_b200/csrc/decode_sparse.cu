@@ -495,12 +495,11 @@ sparse_split_kernel(const __grid_constant__ CUtensorMap kv_map, const SparseArgs
     tile.clear();
     if (w < kRowWarps)
         tile.load_row(0,
-                         gq < G ? a.q + (static_cast<size_t>(seq) * a.Hq + g * G + gq) * kHeadDim
-                                : nullptr,
-                         tq,
-                         a.ep.s * length_temperature(
-                             static_cast<float>(selected_tokens(len, a.keep)), a.ep.alpha,
-                             a.ep.L) * kLog2e);
+                      gq < G ? a.q + (static_cast<size_t>(seq) * a.Hq + g * G + gq) * kHeadDim
+                             : nullptr,
+                      tq,
+                      a.ep.s * length_temperature(static_cast<float>(selected_tokens(len, a.keep)),
+                                                  a.ep.alpha, a.ep.L) * kLog2e);
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&kv_map);
         init_ring(ring);
@@ -539,12 +538,12 @@ sparse_split_kernel(const __grid_constant__ CUtensorMap kv_map, const SparseArgs
             const uint32_t kb = sbase + st * kStageBytes;
             if (ring.page[kk] >= 0)
                 page_step(tile, kb, kb + kChunkBytes, w, lane,
-                                p0 + kk == nsel - 1 ? newest : ~0ull);
+                          p0 + kk == nsel - 1 ? newest : ~0ull);
         });
     }
     let_next_kernel_start();
     reduce_rows(tile, reinterpret_cast<float *>(smem), G, w, lane,
-                      [&](int r, bool real, const RowState &x) {
+                [&](int r, bool real, const RowState &x) {
         const size_t row = static_cast<size_t>(seq) * a.Hq + g * G + r;
         if (a.splits > 1)
             store_part(x, a.partials + (row * a.splits + blockIdx.x / cluster_size()) *

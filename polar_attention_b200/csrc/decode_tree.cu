@@ -174,7 +174,7 @@ tree_split_kernel(const __grid_constant__ CUtensorMap kv_map,
     });
     let_next_kernel_start();
     reduce_rows(tile, reinterpret_cast<float *>(smem), min(kRows, R - row0), w, lane,
-                         [&](int r, bool real, const RowState &x) {
+                [&](int r, bool real, const RowState &x) {
         const int t = (row0 + r) / G, h = g * G + (row0 + r) % G;
         const size_t row = (static_cast<size_t>(seq) * a.tree + t) * a.Hq + h;
         if (a.splits > 1)

@@ -23,9 +23,9 @@
 // full tile about 1100 clocks.  Alone on its SM a chain takes 2100 for a step: 270
 // and 180 to issue the products, about 300 until each is seen, 900 for the weights
 // and sums, of which 512 are exponentials (16 an SM and clock), 200 to reach tensor
-// memory and back.  Four chains come to 1100, not to a quarter of 2100: products,
-// weights and issue slots are each taken for 45 % of the time, and wait for one
-// another.  Loads do not bound it (half of them left out, or all from one page: the
+// memory and back.  Four chains come to 1100, not to a quarter of 2100: the
+// products' pipe is busy for 36 % of the time, exponentials 46 %, issue slots 47 %,
+// and they wait for one another.  Loads do not bound it (half of them left out, or all from one page: the
 // same time).  Measured besides: two threads a row in clusters of eight CTAs, two an
 // SM, 310-330 us; equal shares with a 64-key buffer and one thread for copies and
 // products 268 us, with two 32-key buffers 255 us, with 128-key steps and two CTAs
@@ -86,11 +86,11 @@ constexpr int kMinShare = 4;
 constexpr int kMergeThreads = 256;
 
 // Tiles that the sequences can have.
-int num_tiles(int num_seqs, int tree, int Hq, int Hkv) {
-    return num_seqs * Hkv * ((Hq / Hkv * tree + kTileRows - 1) / kTileRows);
+long long num_tiles(int num_seqs, int tree, int Hq, int Hkv) {
+    return static_cast<long long>(num_seqs) * Hkv * ((Hq / Hkv * tree + kTileRows - 1) / kTileRows);
 }
 
-constexpr size_t record_bytes(int tiles) {
+constexpr size_t record_bytes(long long tiles) {
     return (static_cast<size_t>(tiles) * 3 * sizeof(int) + 15) / 16 * 16;
 }
 
@@ -219,7 +219,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *ring = smem + kQBytes;
-    __shared__ __align__(8) uint64_t q_full, q_empty, full[kStagesTc], empty[kStagesTc], s_full, p_ready, pv_done, mma_done;
+    __shared__ __align__(8) uint64_t q_full, q_empty, full[kStagesTc], empty[kStagesTc], s_full,
+        p_ready, pv_done, mma_done;
     __shared__ unsigned long long odd_nodes;  // drafted nodes with values that are not finite
     __shared__ uint32_t tmem_base_sh;
     __shared__ long long wide[kTcThreads / 32];
@@ -321,7 +322,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                 // The queries, once the tile before has formed its last scores.
                 if (tiles > 0 && !(ok = mbar_wait(&q_empty, (tiles - 1) & 1, a.status))) break;
                 mbar_arrive_expect_tx(&q_full, kQBytes);
-                tma_load_3d(smem, &q_map, 0, g * G, 
+                tma_load_3d(smem, &q_map, 0, g * G,
                             walk.seq * a.tree + (walk.row0() - 32 * walk.quarter()) / G, &q_full);
                 for (int j = 0; j < n; ++j, ++it) {
                     const int st = it % kStagesTc;
@@ -674,7 +675,7 @@ cudaError_t launch_tc(const CUtensorMap &q, const CUtensorMap &kv, const CUtenso
         configured.fetch_or(bit);
     }
     // The workspace: the tiles' records, then two slots of row states for each CTA.
-    const int tiles = num_tiles(t.num_seqs, t.tree, t.Hq, t.Hkv);
+    const long long tiles = num_tiles(t.num_seqs, t.tree, t.Hq, t.Hkv);
     SharedTile *records = reinterpret_cast<SharedTile *>(t.partials);
     TreeArgs a = t;
     a.partials = t.partials + record_bytes(tiles) / sizeof(float);
@@ -685,15 +686,15 @@ cudaError_t launch_tc(const CUtensorMap &q, const CUtensorMap &kv, const CUtenso
     int shares = 1;  // of the parts of a row: four each
     while (shares < kMergeThreads / 8 && shares * 8 * tiles <= ctas) shares *= 2;
     const int rows = std::min(G * t.tree, kTileRows), per_block = kMergeThreads / 8 / shares;
-    return launch_ex(tree_tc_merge_kernel<G>, dim3(tiles, (rows + per_block - 1) / per_block),
-                     kMergeThreads, 0, 1, true, stream, a,
+    const dim3 grid(static_cast<unsigned>(tiles), (rows + per_block - 1) / per_block);
+    return launch_ex(tree_tc_merge_kernel<G>, grid, kMergeThreads, 0, 1, true, stream, a,
                      static_cast<const SharedTile *>(records), shares);
 }
 
 }  // namespace
 
 int tree_tc_ctas(int num_seqs, int max_pages, int tree, int Hq, int Hkv) {
-    const long long most = (num_tiles(num_seqs, tree, Hq, Hkv) * (max_pages + 1ll) + kMinShare - 1) /
+    const long long most = (num_tiles(num_seqs, tree, Hq, Hkv) * (max_pages + 1) + kMinShare - 1) /
                            kMinShare;
     return static_cast<int>(std::min<long long>(148 * kTcPerSm, most));
 }

@@ -695,8 +695,8 @@ def decode_paged_sparse(q, kv_pages, bounds, page_table, seqlens, u, keep, out=N
         _check(lib().polar_attn_decode_paged_sparse(
             *ptr, pp, _need("out", out, bf16, (N, Hq, D), dev),
             None if neff is None else _need("neff", neff, f32, (N, Hq), dev),
-            None if selected is None else _need("selected", selected, i32, (N, Hkv, keep), dev), wp, wb, st),
-            "polar_attn_decode_paged_sparse")
+            None if selected is None else _need("selected", selected, i32, (N, Hkv, keep), dev), wp,
+            wb, st), "polar_attn_decode_paged_sparse")
     return out, neff, selected
 
 
@@ -714,10 +714,11 @@ class PageCache:
         if dev < 0:
             raise ValueError("inputs must be contiguous CUDA tensors")
         self.kv_pages, self.refs, self.bounds = kv_pages, refs, bounds
-        self._c = Cache(_need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, 64), dev),
-                        None if bounds is None else _need("bounds", bounds, bf16, (P_, Hkv, 2, 64), dev),
-                        None if refs is None else _need("refs", refs, torch.int32, (P_,), dev), P_, Hkv, 64,
-                        POLAR_BF16)
+        self._c = Cache(
+            _need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, 64), dev),
+            None if bounds is None else _need("bounds", bounds, bf16, (P_, Hkv, 2, 64), dev),
+            None if refs is None else _need("refs", refs, torch.int32, (P_,), dev), P_, Hkv, 64,
+            POLAR_BF16)
         self._p, self._dev = ctypes.pointer(self._c), dev
 
 
@@ -751,7 +752,7 @@ def cache_reserve(cache: PageCache, page_table, seqlens, grow, granted=None, wor
         g = _need("grow", grow, i32, (N,), dev)
         if granted is None:
             granted = torch.empty_like(grow)
-        workspace, wp, wb = _scratch(workspace, _cache_workspace(cache._c.num_pages, cache._c.Hkv, N), dev)
+        workspace, wp, wb = _scratch(workspace, cache_workspace_size(cache, N), dev)
         _check(lib().polar_attn_cache_reserve(cache._p, table, max_pages, lens, g, N,
                                               _need("granted", granted, i32, (N,), dev), wp, wb,
                                               st), "polar_attn_cache_reserve")
@@ -774,8 +775,8 @@ def cache_append(cache: PageCache, k, v, page_table, seqlens, counts=None, pick=
             cache._p, _need("k", k, bf16, (N, T, Hkv, 64), dev),
             _need("v", v, bf16, (N, T, Hkv, 64), dev), T,
             None if pick is None else _need("pick", pick, i32, (N, C), dev), C,
-            None if counts is None else _need("counts", counts, i32, (N,), dev), table, max_pages, lens, N, st),
-            "polar_attn_cache_append")
+            None if counts is None else _need("counts", counts, i32, (N,), dev), table, max_pages,
+            lens, N, st), "polar_attn_cache_append")
 
 
 def cache_fork(cache: PageCache, src_table, src_lens, src_rows, dst_table, dst_lens, *,
@@ -802,7 +803,8 @@ def cache_free(cache: PageCache, page_table, seqlens, keep=None, *, stream=None)
         table, lens, N, max_pages = _rows(cache, page_table, seqlens)
         _check(lib().polar_attn_cache_free(
             cache._p, table, max_pages, lens,
-            None if keep is None else _need("keep", keep, torch.int32, (N,), dev), N, st), "polar_attn_cache_free")
+            None if keep is None else _need("keep", keep, torch.int32, (N,), dev), N, st),
+            "polar_attn_cache_free")
 
 
 def cache_compact(cache: PageCache, page_table, seqlens, used=None, workspace=None, *,
@@ -815,7 +817,7 @@ def cache_compact(cache: PageCache, page_table, seqlens, used=None, workspace=No
         table, lens, N, max_pages = _rows(cache, page_table, seqlens)
         if used is None:
             used = torch.empty(1, device=dev, dtype=i32)
-        workspace, wp, wb = _scratch(workspace, _cache_workspace(cache._c.num_pages, cache._c.Hkv, N), dev)
+        workspace, wp, wb = _scratch(workspace, cache_workspace_size(cache, N), dev)
         _check(lib().polar_attn_cache_compact(cache._p, table, max_pages, lens, N,
                                               _need("used", used, i32, (1,), dev), wp, wb, st),
                "polar_attn_cache_compact")

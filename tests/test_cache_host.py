@@ -81,7 +81,7 @@ def test_tree(lib, kw, code):
     ({"keep": 0}, INVALID), ({"keep": -1}, INVALID), ({"pages": 0}, INVALID), ({"mp": 0}, INVALID),
     ({"n": -1}, INVALID), ({"q": None}, INVALID), ({"b": None}, INVALID), ({"kv": None}, INVALID),
     ({"b": MIS}, INVALID), ({"kv": MIS}, INVALID), ({"sel": MIS4}, INVALID), ({"out": MIS}, INVALID),
-    ({"ws": None}, INVALID), ({"wb": 64}, WORKSPACE), ({"n": 0, "b": None}, OK)])
+    ({"ws": None}, INVALID), ({"wb": 8}, WORKSPACE), ({"n": 0, "b": None}, OK)])
 def test_sparse(lib, kw, code):
     assert sparse(lib, **kw) == code
 
