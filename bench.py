@@ -734,7 +734,7 @@ def run_ours(args):
         gbs = kv_bytes / dec_launch_s / 1e9 if do_dec else 0.0
         sha_p = source_sha("fwd_tc.cu", "fwd_moments.cu", "polar_common.cuh", "tc_common.cuh",
                            "bwd_coef.cuh")
-        sha_d = source_sha("decode.cu", "polar_common.cuh")
+        sha_d = source_sha("decode.cu", "mma_common.cuh", "polar_common.cuh")
         value = aggregate_throughput(PREFILL.flops * K, world, t_pre_max) / 1e12 if do_pre else 0.0
         dec_value = aggregate_throughput(kv_bytes * K, world, t_dec_max) / 1e9 if do_dec else 0.0
         result = {

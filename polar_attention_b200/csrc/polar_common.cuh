@@ -19,7 +19,6 @@ namespace polar {
 
 constexpr int kHeadDim = 64;
 constexpr int kPage = 64;               // tokens per KV page
-constexpr int kMaxTree = 64;            // drafted nodes of a sequence: one mask word, one page step
 constexpr float kLog2e = 1.4426950408889634f;
 // Lazy rescale threshold, log2 units: the reference max of the streaming
 // softmax only moves when a new logit exceeds it by more than 2^8, so every

@@ -86,6 +86,8 @@ struct GdeltaStepLaunch {          // one decode token per sequence, in place
     cudaStream_t stream;
 };
 
+constexpr int kMaxTree = 64;       // drafted nodes of a sequence: one mask word, one page step
+
 struct TreeLaunch {                // a tree of drafted tokens over the paged cache
     const void *q;                 // [num_seqs, tree, Hq, 64]
     const void *k, *v;             // drafted rows [num_seqs, tree, Hkv, 64]
