@@ -329,8 +329,8 @@ polar_status_t polar_attn_decode_paged_chunk(const void *q, const void *kv_pages
  *             t's word: node t sees node j (a node that sees itself has its own
  *             bit set).  Bits at or past the sequence's node count are ignored.
  *  tree_lens  [num_seqs] int32, device: nodes of each sequence, 0 .. tree, or
- *             NULL: `tree` nodes each.  Rows at or past it are neither read nor
- *             written.
+ *             NULL: `tree` nodes each.  Of rows at or past it nothing counts, and
+ *             nothing is written there.
  *  tree       1 .. 64 (else POLAR_ERR_UNSUPPORTED)
  *  seqlens    [num_seqs] int32, device: cached tokens, 0 .. 64 * max_pages
  *             (the drafted nodes are not counted)

@@ -181,7 +181,7 @@ struct SelectArgs {
 // the first block's shared memory (past kSelKeys pages: to the workspace), which
 // selects.  One launch: a kernel for the scores and one for the selection took
 // 25.6 us a call where one sequence has 512 pages and 85 us at 16 sequences of
-// 1024 to 4096, this takes 22.4 and 83.
+// 1024 to 4096, this took 22.4 and 83.
 //
 // A radix selection over keys in the scores' order finds the k-th highest.
 // Scores lie close together, so its digits begin at the highest bit in which

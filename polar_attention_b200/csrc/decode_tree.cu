@@ -273,7 +273,7 @@ size_t tree_workspace_bytes(int num_seqs, int max_pages, int tree, int Hq, int H
     if (uses_tc(num_seqs, max_pages, tree, Hq, Hkv))
         return tree_tc_workspace_bytes(num_seqs, max_pages, tree, Hq, Hkv);
     const TreePlan p = tree_plan(num_seqs, max_pages, tree, Hq, Hkv);
-    if (p.splits == 1) return 16;  // none is used
+    if (p.splits == 1) return 16;  // none of it is touched
     return static_cast<size_t>(num_seqs) * tree * Hq * p.splits * kPartialFloats * sizeof(float);
 }
 

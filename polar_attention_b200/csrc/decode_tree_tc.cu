@@ -19,7 +19,7 @@
 // A CTA's step is one chain; 128 columns (S, O) and two 16 KB stages are all it
 // needs, so four CTAs share an SM and cover each other's waits.
 //
-// What bounds it (64 nodes, 8 sequences of 32K-64K, 216 us): per SM and step of a
+// What bounds it (64 nodes, 8 sequences of 32K-64K, 215-232 us): per SM and step of a
 // full tile about 1100 clocks.  Alone on its SM a chain takes 2100 for a step: 270
 // and 180 to issue the products, about 300 until each is seen, 900 for the weights
 // and sums, of which 512 are exponentials (16 an SM and clock), 200 to reach tensor

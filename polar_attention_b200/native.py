@@ -552,11 +552,15 @@ def _decode_params(Hq, Hkv, D, dtype, s, alpha, L, beta):
     return p, ctypes.pointer(p)
 
 
+def _current(dev):
+    """Whether this is the current CUDA device's index."""
+    return dev >= 0 and dev == torch._C._cuda_getDevice()
+
+
 class _Scope:
-    """A call on the device of `tensor` and on `stream` (None: the device's
-    current stream): what the call allocates belongs to that device and stream.
-    Entering gives the stream's handle; where the device is current and no
-    stream is given, nothing is switched."""
+    """The device of `tensor` and `stream` (None: the device's current stream)
+    made current: what a call in it allocates belongs to that device and
+    stream."""
     __slots__ = ("tensor", "given", "stack")
 
     def __init__(self, tensor, stream):
@@ -566,8 +570,6 @@ class _Scope:
         index = self.tensor.get_device()
         if index < 0:
             raise ValueError("inputs must be contiguous CUDA tensors")
-        if self.given is None and index == torch._C._cuda_getDevice():
-            return torch._C._cuda_getCurrentRawStream(index)
         if self.given is not None and self.given.device.index != index:
             raise ValueError(f"stream of {self.given.device} for tensors on cuda:{index}")
         self.stack = [torch.cuda.device(index)]
@@ -575,10 +577,9 @@ class _Scope:
             self.stack.append(torch.cuda.stream(self.given))
         for c in self.stack:
             c.__enter__()
-        return torch._C._cuda_getCurrentRawStream(index)
 
     def __exit__(self, *exc):
-        for c in reversed(self.stack or ()):
+        for c in reversed(self.stack):
             c.__exit__(*exc)
 
 
@@ -612,6 +613,12 @@ def _pool_shape(kv_pages, D):
     return kv_pages.shape[0], kv_pages.shape[2]
 
 
+@functools.lru_cache(maxsize=64)
+def _untouched(dev, need):
+    """A workspace that no kernel reads or writes: one for all calls."""
+    return torch.empty(need, device=dev, dtype=torch.uint8)
+
+
 @functools.lru_cache(maxsize=256)
 def decode_tree_workspace_size(num_seqs: int, max_pages: int, tree: int, Hq: int, Hkv: int) -> int:
     _, pp = _decode_params(Hq, Hkv, 64, POLAR_BF16, 8.0, 0.3, 2048, 1.0)
@@ -633,25 +640,32 @@ def decode_paged_tree(q, k, v, tree_mask, kv_pages, page_table, seqlens, u, out=
     bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     max_pages = page_table.shape[1]
     dev = q.get_device()
-    with _Scope(q, stream) as st:
-        ptr = (_need("q", q, bf16, (N, M, Hq, D), dev), _need("k", k, bf16, (N, M, Hkv, D), dev),
-               _need("v", v, bf16, (N, M, Hkv, D), dev),
-               _need("tree_mask", tree_mask, torch.int64, (N, M), dev),
-               None if tree_lens is None else _need("tree_lens", tree_lens, i32, (N,), dev), M,
-               _need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, D), dev), P_,
-               _need("page_table", page_table, i32, (N, max_pages), dev), max_pages,
-               _need("seqlens", seqlens, i32, (N,), dev), N, _need("u", u, f32, (Hq, D), dev))
-        _, pp = _decode_params(Hq, Hkv, D, POLAR_BF16, s, alpha, L, beta)
-        if out is None:
-            out = torch.empty_like(q)
-        if neff is None and want_neff:
-            neff = torch.empty((N, M, Hq), device=dev, dtype=f32)
-        workspace, wp, wb = _scratch(
-            workspace, decode_tree_workspace_size(N, max_pages, M, Hq, Hkv), dev)
-        _check(lib().polar_attn_decode_paged_tree(
-            *ptr, pp, _need("out", out, bf16, (N, M, Hq, D), dev),
-            None if neff is None else _need("neff", neff, f32, (N, M, Hq), dev), wp, wb, st),
-            "polar_attn_decode_paged_tree")
+    if stream is not None or not _current(dev):
+        with _Scope(q, stream):
+            return decode_paged_tree(q, k, v, tree_mask, kv_pages, page_table, seqlens, u, out,
+                                     neff, workspace, tree_lens=tree_lens, s=s, alpha=alpha, L=L,
+                                     beta=beta, want_neff=want_neff)
+    st = torch._C._cuda_getCurrentRawStream(dev)
+    ptr = (_need("q", q, bf16, (N, M, Hq, D), dev), _need("k", k, bf16, (N, M, Hkv, D), dev),
+           _need("v", v, bf16, (N, M, Hkv, D), dev),
+           _need("tree_mask", tree_mask, torch.int64, (N, M), dev),
+           None if tree_lens is None else _need("tree_lens", tree_lens, i32, (N,), dev), M,
+           _need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, D), dev), P_,
+           _need("page_table", page_table, i32, (N, max_pages), dev), max_pages,
+           _need("seqlens", seqlens, i32, (N,), dev), N, _need("u", u, f32, (Hq, D), dev))
+    _, pp = _decode_params(Hq, Hkv, D, POLAR_BF16, s, alpha, L, beta)
+    if out is None:
+        out = torch.empty_like(q)
+    if neff is None and want_neff:
+        neff = torch.empty((N, M, Hq), device=dev, dtype=f32)
+    need = decode_tree_workspace_size(N, max_pages, M, Hq, Hkv)
+    if workspace is None and need == 16:  # nothing is split
+        workspace = _untouched(dev, need)
+    workspace, wp, wb = _scratch(workspace, need, dev)
+    _check(lib().polar_attn_decode_paged_tree(
+        *ptr, pp, _need("out", out, bf16, (N, M, Hq, D), dev),
+        None if neff is None else _need("neff", neff, f32, (N, M, Hq), dev), wp, wb, st),
+        "polar_attn_decode_paged_tree")
     return out, neff
 
 
@@ -676,27 +690,34 @@ def decode_paged_sparse(q, kv_pages, bounds, page_table, seqlens, u, keep, out=N
     bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     max_pages = page_table.shape[1]
     dev = q.get_device()
-    with _Scope(q, stream) as st:
-        ptr = (_need("q", q, bf16, (N, Hq, D), dev),
-               _need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, D), dev),
-               _need("bounds", bounds, bf16, (P_, Hkv, 2, D), dev), P_,
-               _need("page_table", page_table, i32, (N, max_pages), dev), max_pages,
-               _need("seqlens", seqlens, i32, (N,), dev), N, keep,
-               _need("u", u, f32, (Hq, D), dev))
-        _, pp = _decode_params(Hq, Hkv, D, POLAR_BF16, s, alpha, L, beta)
-        if out is None:
-            out = torch.empty_like(q)
-        if neff is None and want_neff:
-            neff = torch.empty((N, Hq), device=dev, dtype=f32)
-        if selected is None and want_selected:
-            selected = torch.empty((N, Hkv, max(keep, 0)), device=dev, dtype=i32)
-        workspace, wp, wb = _scratch(
-            workspace, decode_sparse_workspace_size(N, max_pages, keep, Hq, Hkv), dev)
-        _check(lib().polar_attn_decode_paged_sparse(
-            *ptr, pp, _need("out", out, bf16, (N, Hq, D), dev),
-            None if neff is None else _need("neff", neff, f32, (N, Hq), dev),
-            None if selected is None else _need("selected", selected, i32, (N, Hkv, keep), dev), wp,
-            wb, st), "polar_attn_decode_paged_sparse")
+    if stream is not None or not _current(dev):
+        with _Scope(q, stream):
+            return decode_paged_sparse(q, kv_pages, bounds, page_table, seqlens, u, keep, out, neff,
+                                       selected, workspace, s=s, alpha=alpha, L=L, beta=beta,
+                                       want_neff=want_neff, want_selected=want_selected)
+    st = torch._C._cuda_getCurrentRawStream(dev)
+    ptr = (_need("q", q, bf16, (N, Hq, D), dev),
+           _need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, D), dev),
+           _need("bounds", bounds, bf16, (P_, Hkv, 2, D), dev), P_,
+           _need("page_table", page_table, i32, (N, max_pages), dev), max_pages,
+           _need("seqlens", seqlens, i32, (N,), dev), N, keep,
+           _need("u", u, f32, (Hq, D), dev))
+    _, pp = _decode_params(Hq, Hkv, D, POLAR_BF16, s, alpha, L, beta)
+    if out is None:
+        out = torch.empty_like(q)
+    if neff is None and want_neff:
+        neff = torch.empty((N, Hq), device=dev, dtype=f32)
+    if selected is None and want_selected:
+        selected = torch.empty((N, Hkv, max(keep, 0)), device=dev, dtype=i32)
+    need = decode_sparse_workspace_size(N, max_pages, keep, Hq, Hkv)
+    if workspace is None and selected is not None and need <= (N * Hkv * keep * 4 + 15) // 16 * 16:
+        workspace = _untouched(dev, max(need, 16))  # of the list alone, which `selected` takes
+    workspace, wp, wb = _scratch(workspace, need, dev)
+    _check(lib().polar_attn_decode_paged_sparse(
+        *ptr, pp, _need("out", out, bf16, (N, Hq, D), dev),
+        None if neff is None else _need("neff", neff, f32, (N, Hq), dev),
+        None if selected is None else _need("selected", selected, i32, (N, Hkv, keep), dev), wp,
+        wb, st), "polar_attn_decode_paged_sparse")
     return out, neff, selected
 
 
@@ -706,7 +727,7 @@ class PageCache:
     caller with an allocator of its own, who then only appends) and the pages'
     key bounds [P,Hkv,2,64] bf16 (None: not kept).  Holds the tensors; page
     tables and lengths are arguments of each call."""
-    __slots__ = ("kv_pages", "refs", "bounds", "_c", "_p", "_dev")
+    __slots__ = ("kv_pages", "refs", "bounds", "_c", "_p", "_dev", "_pages", "_heads")
 
     def __init__(self, kv_pages, refs=None, bounds=None):
         P_, Hkv = _pool_shape(kv_pages, 64)
@@ -719,7 +740,7 @@ class PageCache:
             None if bounds is None else _need("bounds", bounds, bf16, (P_, Hkv, 2, 64), dev),
             None if refs is None else _need("refs", refs, torch.int32, (P_,), dev), P_, Hkv, 64,
             POLAR_BF16)
-        self._p, self._dev = ctypes.pointer(self._c), dev
+        self._p, self._dev, self._pages, self._heads = ctypes.byref(self._c), dev, P_, Hkv
 
 
 @functools.lru_cache(maxsize=256)
@@ -729,7 +750,7 @@ def _cache_workspace(num_pages, Hkv, num_seqs):
 
 
 def cache_workspace_size(cache: PageCache, num_seqs: int) -> int:
-    return _cache_workspace(cache._c.num_pages, cache._c.Hkv, num_seqs)
+    return _cache_workspace(cache._pages, cache._heads, num_seqs)
 
 
 def _rows(cache, page_table, seqlens):
@@ -747,15 +768,19 @@ def cache_reserve(cache: PageCache, page_table, seqlens, grow, granted=None, wor
     [N] (int32) in place.  Returns granted [N] int32: grow, or 0 from the first
     row on that the pool cannot serve."""
     dev, i32 = cache._dev, torch.int32
-    with _Scope(cache.kv_pages, stream) as st:
-        table, lens, N, max_pages = _rows(cache, page_table, seqlens)
-        g = _need("grow", grow, i32, (N,), dev)
-        if granted is None:
-            granted = torch.empty_like(grow)
-        workspace, wp, wb = _scratch(workspace, cache_workspace_size(cache, N), dev)
-        _check(lib().polar_attn_cache_reserve(cache._p, table, max_pages, lens, g, N,
-                                              _need("granted", granted, i32, (N,), dev), wp, wb,
-                                              st), "polar_attn_cache_reserve")
+    if stream is not None or not _current(dev):
+        with _Scope(cache.kv_pages, stream):
+            return cache_reserve(cache, page_table, seqlens, grow, granted, workspace)
+    st = torch._C._cuda_getCurrentRawStream(dev)
+    table, lens, N, max_pages = _rows(cache, page_table, seqlens)
+    g = _need("grow", grow, i32, (N,), dev)
+    if granted is None:
+        granted = torch.empty_like(grow)
+    workspace, wp, wb = _scratch(
+        workspace, _cache_workspace(cache._pages, cache._heads, N), dev)
+    _check(lib().polar_attn_cache_reserve(cache._p, table, max_pages, lens, g, N,
+                                          _need("granted", granted, i32, (N,), dev), wp, wb,
+                                          st), "polar_attn_cache_reserve")
     return granted
 
 
@@ -765,18 +790,21 @@ def cache_append(cache: PageCache, k, v, page_table, seqlens, counts=None, pick=
     row n, from k, v [N,T,Hkv,64] row t (pick [N,C] int32: row pick[n,t]), to
     position seqlens[n] - counts[n] + t; the touched pages' bounds are kept."""
     dev, bf16, i32 = cache._dev, torch.bfloat16, torch.int32
-    with _Scope(cache.kv_pages, stream) as st:
-        table, lens, N, max_pages = _rows(cache, page_table, seqlens)
-        if k.dim() != 4:
-            raise ValueError(f"k must be [N, T, Hkv, 64], not {tuple(k.shape)}")
-        T, Hkv = k.shape[1], cache._c.Hkv
-        C = T if pick is None else pick.shape[1]
-        _check(lib().polar_attn_cache_append(
-            cache._p, _need("k", k, bf16, (N, T, Hkv, 64), dev),
-            _need("v", v, bf16, (N, T, Hkv, 64), dev), T,
-            None if pick is None else _need("pick", pick, i32, (N, C), dev), C,
-            None if counts is None else _need("counts", counts, i32, (N,), dev), table, max_pages,
-            lens, N, st), "polar_attn_cache_append")
+    if stream is not None or not _current(dev):
+        with _Scope(cache.kv_pages, stream):
+            return cache_append(cache, k, v, page_table, seqlens, counts, pick)
+    st = torch._C._cuda_getCurrentRawStream(dev)
+    table, lens, N, max_pages = _rows(cache, page_table, seqlens)
+    if k.dim() != 4:
+        raise ValueError(f"k must be [N, T, Hkv, 64], not {tuple(k.shape)}")
+    T, Hkv = k.shape[1], cache._heads
+    C = T if pick is None else pick.shape[1]
+    _check(lib().polar_attn_cache_append(
+        cache._p, _need("k", k, bf16, (N, T, Hkv, 64), dev),
+        _need("v", v, bf16, (N, T, Hkv, 64), dev), T,
+        None if pick is None else _need("pick", pick, i32, (N, C), dev), C,
+        None if counts is None else _need("counts", counts, i32, (N,), dev), table, max_pages,
+        lens, N, st), "polar_attn_cache_append")
 
 
 def cache_fork(cache: PageCache, src_table, src_lens, src_rows, dst_table, dst_lens, *,
@@ -785,26 +813,32 @@ def cache_fork(cache: PageCache, src_table, src_lens, src_rows, dst_table, dst_l
     src_table, src_lens that shares its pages; a negative source leaves the row
     alone.  The two tables may not overlap."""
     dev, i32 = cache._dev, torch.int32
-    with _Scope(cache.kv_pages, stream) as st:
-        src, slens, S, width = _rows(cache, src_table, src_lens)
-        dst, dlens, N, max_pages = _rows(cache, dst_table, dst_lens)
-        if width != max_pages:
-            raise ValueError("src_table and dst_table must be equally wide")
-        _check(lib().polar_attn_cache_fork(cache._p, src, slens, S,
-                                           _need("src_rows", src_rows, i32, (N,), dev), N, dst,
-                                           dlens, max_pages, st), "polar_attn_cache_fork")
+    if stream is not None or not _current(dev):
+        with _Scope(cache.kv_pages, stream):
+            return cache_fork(cache, src_table, src_lens, src_rows, dst_table, dst_lens)
+    st = torch._C._cuda_getCurrentRawStream(dev)
+    src, slens, S, width = _rows(cache, src_table, src_lens)
+    dst, dlens, N, max_pages = _rows(cache, dst_table, dst_lens)
+    if width != max_pages:
+        raise ValueError("src_table and dst_table must be equally wide")
+    _check(lib().polar_attn_cache_fork(cache._p, src, slens, S,
+                                       _need("src_rows", src_rows, i32, (N,), dev), N, dst,
+                                       dlens, max_pages, st), "polar_attn_cache_fork")
 
 
 def cache_free(cache: PageCache, page_table, seqlens, keep=None, *, stream=None):
     """Cuts each row to its first keep [N] int32 tokens (None: none; negative:
     the row is left alone) and gives the pages behind them back, in place."""
     dev = cache._dev
-    with _Scope(cache.kv_pages, stream) as st:
-        table, lens, N, max_pages = _rows(cache, page_table, seqlens)
-        _check(lib().polar_attn_cache_free(
-            cache._p, table, max_pages, lens,
-            None if keep is None else _need("keep", keep, torch.int32, (N,), dev), N, st),
-            "polar_attn_cache_free")
+    if stream is not None or not _current(dev):
+        with _Scope(cache.kv_pages, stream):
+            return cache_free(cache, page_table, seqlens, keep)
+    st = torch._C._cuda_getCurrentRawStream(dev)
+    table, lens, N, max_pages = _rows(cache, page_table, seqlens)
+    _check(lib().polar_attn_cache_free(
+        cache._p, table, max_pages, lens,
+        None if keep is None else _need("keep", keep, torch.int32, (N,), dev), N, st),
+        "polar_attn_cache_free")
 
 
 def cache_compact(cache: PageCache, page_table, seqlens, used=None, workspace=None, *,
@@ -813,14 +847,18 @@ def cache_compact(cache: PageCache, page_table, seqlens, used=None, workspace=No
     rows that name pages of this pool) in place.  Returns used [1] int32: the
     number of live pages, which are pages 0 .. used - 1 afterwards."""
     dev, i32 = cache._dev, torch.int32
-    with _Scope(cache.kv_pages, stream) as st:
-        table, lens, N, max_pages = _rows(cache, page_table, seqlens)
-        if used is None:
-            used = torch.empty(1, device=dev, dtype=i32)
-        workspace, wp, wb = _scratch(workspace, cache_workspace_size(cache, N), dev)
-        _check(lib().polar_attn_cache_compact(cache._p, table, max_pages, lens, N,
-                                              _need("used", used, i32, (1,), dev), wp, wb, st),
-               "polar_attn_cache_compact")
+    if stream is not None or not _current(dev):
+        with _Scope(cache.kv_pages, stream):
+            return cache_compact(cache, page_table, seqlens, used, workspace)
+    st = torch._C._cuda_getCurrentRawStream(dev)
+    table, lens, N, max_pages = _rows(cache, page_table, seqlens)
+    if used is None:
+        used = torch.empty(1, device=dev, dtype=i32)
+    workspace, wp, wb = _scratch(
+        workspace, _cache_workspace(cache._pages, cache._heads, N), dev)
+    _check(lib().polar_attn_cache_compact(cache._p, table, max_pages, lens, N,
+                                          _need("used", used, i32, (1,), dev), wp, wb, st),
+           "polar_attn_cache_compact")
     return used
 
 
