@@ -136,6 +136,8 @@ polar_status_t check_decode_tree(const polar_params_t *p, int num_seqs, int max_
     if (p->window != 0) return POLAR_ERR_UNSUPPORTED;
     if (tree < 1) return POLAR_ERR_INVALID_ARG;
     if (tree > kMaxTree) return POLAR_ERR_UNSUPPORTED;
+    // The keys that a node sees are counted in 32 bits.
+    if ((max_pages + 1ll) * kPage > (1ll << 31) - 1) return POLAR_ERR_INVALID_ARG;
     return POLAR_OK;
 }
 

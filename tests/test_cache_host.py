@@ -65,7 +65,8 @@ def test_group_sizes(lib, call):
 @pytest.mark.parametrize("kw,code", [
     ({"tree": 0}, INVALID), ({"tree": 65}, UNSUPPORTED), ({"pages": 0}, INVALID),
     ({"pages": 1 << 24}, INVALID), ({"mp": 0}, INVALID), ({"mp": 1 << 26}, INVALID),
-    ({"n": -1}, INVALID), ({"n": 65536}, INVALID), ({"q": None}, INVALID), ({"k": None}, INVALID),
+    ({"mp": (1 << 25) - 1}, INVALID), ({"n": -1}, INVALID), ({"n": 65536}, INVALID),
+    ({"q": None}, INVALID), ({"k": None}, INVALID),
     ({"v": None}, INVALID), ({"mask": None}, INVALID), ({"kv": None}, INVALID),
     ({"pt": None}, INVALID), ({"sl": None}, INVALID), ({"u": None}, INVALID),
     ({"out": None}, INVALID), ({"ws": None}, INVALID), ({"q": MIS}, INVALID), ({"k": MIS}, INVALID),
