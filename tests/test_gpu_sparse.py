@@ -168,6 +168,20 @@ def test_scores_that_are_not_finite(cuda_ok):
     assert sel[0, 0].tolist() == [7, 9, 19]
 
 
+@pytest.mark.parametrize("keep", [4, 30, 150])
+def test_many_pages_with_scores_that_are_not_finite(cuda_ok, keep):
+    """Every score is in question then: all get exact ones."""
+    x = inputs([64 * 200 + 1, 64 * 90], 8, 2, seed=14)
+    t = x["table"][0].tolist()
+    for p in (3, 11, 150):
+        x["bounds"][t[p], 0, :, 7] = float("nan")
+    for p in (5, 60):
+        x["bounds"][t[p]] = torch.tensor([-float("inf"), float("inf")])[:, None].bfloat16()
+    out, neff, sel = call(cuda(x), keep)
+    assert pa.get_status() == 0
+    check(x, keep, out, neff, sel)
+
+
 def test_stale_rows_do_not_count(cuda_ok):
     x = inputs([64 * 9 + 10], 8, 2, seed=7)
     clean = {k: t.clone() for k, t in x.items()}
