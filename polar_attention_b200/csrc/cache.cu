@@ -43,7 +43,7 @@ __device__ __forceinline__ T block_scan(T x, T *scratch, T *total) {
 
 constexpr int kPlanRows = 1024;   // rows whose plan is held in shared memory
 constexpr int kPlanFresh = 2048;  // and new pages
-constexpr int kFusedRows = 256;   // rows up to which one cluster plans and copies
+constexpr int kFusedRows = 128;   // rows up to which one cluster plans and copies
 constexpr int kFusedCluster = 8;
 
 struct ReserveArgs {
@@ -249,8 +249,11 @@ __device__ __forceinline__ void copy_block(uint4 *kv, uint4 *bounds, int3 c, int
 }
 
 // A growth step of few rows: one cluster, whose first block plans and hands the
-// copies to all.  One launch instead of two: what a step without copies, the
-// common one, spends is the launches (append step of 64 rows: 46 -> 43 us).
+// copies to all.  One launch instead of two, since a loop of such calls spends its
+// time on the launches (append step of 64 rows: 43 us, with two kernels 46).  On
+// the GPU the two kernels are the faster ones, the more so the more rows copy: no
+// copies 4.2 us, this 5.4 to 6.2; half of 64 rows 8.2, this 10.2; of 128 8.2 and
+// 12.4; of 256 8.2 and 14.6.
 __global__ void __launch_bounds__(kPlanThreads)
 cache_reserve_fused_kernel(const ReserveArgs a) {
     __shared__ int3 copies[kFusedRows];

@@ -81,7 +81,8 @@ __device__ __forceinline__ bool elect_one() {
     return one != 0;
 }
 
-// Steps that a share has at least.
+// Steps that a share has at least (4 sequences of 4000-5000 tokens, 128 rows: at
+// least 1 36.8 us, 4 28.8, 12 32.9).
 constexpr int kMinShare = 4;
 constexpr int kMergeThreads = 256;
 
