@@ -126,7 +126,8 @@ __device__ __forceinline__ TileSums tile_pass(const uint32_t (&sr)[32], uint32_t
     return TileSums{fmaxf(mx[0], mx[1]), a1.x + a1.y, a2.x + a2.y, la.x + la.y, l2a.x + l2a.y};
 }
 
-// 16 n columns of fp32 of this thread's lane of tensor memory, times r.
+// 16 n columns of fp32 of this thread's lane of tensor memory, times r.  The stores
+// are complete on return: the second half of a step may load the columns again.
 __device__ __forceinline__ void scale_columns(uint32_t t, int n, float r) {
 #pragma unroll 1
     for (int c = 0; c < n; ++c) {
@@ -137,6 +138,7 @@ __device__ __forceinline__ void scale_columns(uint32_t t, int n, float r) {
         for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
         tmem_st16(t + 16 * c, o);
     }
+    tmem_wait_st();
 }
 
 // The weights of a step's first half (16 columns of bf16 pairs), times a power

@@ -330,3 +330,42 @@ def test_two_graphs_and_eager_calls(cuda_ok):
     assert pa.get_status() == 0
     for w, *others in zip(want, got, again):
         assert all(torch.equal(w[i], o[i]) for o in others for i in (0, 1))
+
+
+def along(axis, dots, rng):
+    """Unit rows with the products `dots` with a unit vector along `axis`."""
+    dots = np.asarray(dots, np.float64)
+    x = rng.standard_normal((*dots.shape, 64))
+    x[..., axis] = 0
+    x *= np.sqrt(1 - dots ** 2)[..., None] / np.linalg.norm(x, axis=-1, keepdims=True)
+    x[..., axis] = dots
+    return torch.from_numpy(x).bfloat16()
+
+
+@pytest.mark.parametrize("G,M", [(4, 20), (1, 40), (8, 64)])
+def test_reference_moves_twice_in_a_page(cuda_ok, G, M):
+    """Weights far above a row's first reference, then a page whose first half
+    moves the reference by more than 2^24 and whose second half moves it as far
+    again: what was summed before has to shrink by both.  At s = 60 a product of
+    0.3 is 26 log2 units; with one of the moves lost, the second page would weigh
+    half as much as the last keys instead of 2^-26 of them."""
+    x = inputs([192, 192, 130], M, 2 * G, 2, seed=15, max_pages=WIDE)
+    rng = np.random.default_rng(15)
+    x["q"].zero_()
+    x["q"][..., 0] = 1
+    for i, n in enumerate((192, 192, 130)):
+        page = x["table"][i].long()
+        dots = np.repeat([-0.6, -0.335, -0.29, 0.0], [64, 64, 32, 32])[:n]
+        if i == 1:  # three moves in one page, and back
+            dots = np.concatenate([np.full(100, -0.9), np.full(60, -0.3), np.full(31, 0.3), [0.9]])
+        keys = along(0, np.broadcast_to(dots, (2, n)), rng)
+        values = torch.zeros((2, n, 64), dtype=torch.bfloat16)
+        for at, d in enumerate(sorted(set(dots.tolist()))):
+            values[:, np.flatnonzero(dots == d), 10 + at] = 1
+        for p in range(n):
+            x["kv"][page[p // 64], 0, :, p % 64] = keys[:, p]
+            x["kv"][page[p // 64], 1, :, p % 64] = values[:, p]
+    x["k"] = along(0, np.full(x["k"].shape[:-1], -0.95), rng)
+    out, neff = call(cuda(x), s=60.0, L=2048)
+    assert pa.get_status() == 0
+    check(x, out, neff, [M, M, M], s=60.0, L=2048)
