@@ -49,6 +49,7 @@ struct RowTile {
     template <bool kAll>
     __device__ __forceinline__ void score(const uint32_t (&kf)[2][2][4],
                                           const uint32_t (&bits)[kHR]) {
+        __syncwarp();  // the products, here and in weigh(), are the whole warp's
         float sc[2][4];
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
@@ -107,6 +108,7 @@ struct RowTile {
             pa[hr][0] = pack_bf16x2(pv[0][0], pv[0][1]);
             pa[hr][1] = pack_bf16x2(pv[1][0], pv[1][1]);
         }
+        __syncwarp();  // quads whose row moved its reference come back
     }
 
     // acc += P V for value columns 16i .. 16i+15 (v: transposed fragments).

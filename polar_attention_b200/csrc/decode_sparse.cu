@@ -131,6 +131,7 @@ __device__ __forceinline__ void score_pages(const uint4 *__restrict__ q,
     for (int step = 0; step < steps; ++step) {  // the same number in every lane: it shuffles
         fetch(step + kScoreRing - 1);
         asm volatile("cp.async.wait_group %0;" ::"n"(kScoreRing - 1) : "memory");
+        __syncwarp();  // lanes without a page or a score to store come back: mma is the warp's
         const uint4 *src = ring + step % kScoreRing * 4 * kThreads + tid;
         float s[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

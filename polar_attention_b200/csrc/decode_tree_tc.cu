@@ -283,6 +283,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
         for (int i = 0; i < kTcThreads / 32; ++i) before += wide[i];
         if (before > first) break;  // uniform
     }
+    __syncwarp();  // instructions on tensor memory are for whole warps
     if (w == 5) tmem_alloc_128(&tmem_base_sh);
     tc_fence_before();
     __syncthreads();
@@ -548,6 +549,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
             const uint64_t extra = s0 + cnt > npg ? odd_nodes & seen : 0ull;
             const __nv_bfloat16 *vrow = a.v + (node0 * a.Hkv + g) * kHeadDim;
             auto column = [&](int c, uint32_t (&o)[16]) {  // O's columns 16c .. 16c + 15
+                __syncwarp();  // lanes that had values to add, or no row to write, come back
                 tmem_ld16(tO + 16 * c, o);
                 tmem_wait_ld();
                 for (uint64_t todo = extra; todo; todo &= todo - 1) {

@@ -18,7 +18,9 @@ __device__ __forceinline__ uint32_t cluster_size() {
     return r;
 }
 // All threads of the cluster; shared-memory writes before it are seen after it.
+// The instructions are for whole warps: a warp comes together first.
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
 }

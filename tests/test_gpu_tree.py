@@ -369,3 +369,26 @@ def test_reference_moves_twice_in_a_page(cuda_ok, G, M):
     out, neff = call(cuda(x), s=60.0, L=2048)
     assert pa.get_status() == 0
     check(x, out, neff, [M, M, M], s=60.0, L=2048)
+
+
+@pytest.mark.parametrize("G,M,lens", [(4, 40, [130, 5]), (8, 9, [130, 5]), (1, 64, [4000, 0])])
+def test_rows_add_different_numbers_of_values(cuda_ok, G, M, lens):
+    """Drafted values that are not finite in columns of their own, seen by none
+    to all of them in the rows of one warp, some of whose lanes have no row: a row
+    has no direction in the columns it sees, and only there."""
+    x = inputs(lens, M, 2 * G, 2, seed=16, max_pages=WIDE)
+    clean = {k: t.clone() for k, t in x.items()}
+    odd = list(range(0, M, 3))
+    for j in odd:
+        x["v"][:, j, :, j % 64] = float("inf")
+    out, neff = call(cuda(x))
+    assert pa.get_status() == 0
+    refs = reference(clean, [M, M], {(i, t, 0) for i in range(2) for t in range(M)})
+    for (i, t, h), (want, n, _, tol) in refs.items():
+        bits = int(x["mask"][i, t]) & (2 ** 64 - 1)
+        seen = [j % 64 for j in odd if bits >> j & 1]
+        row = out[i, t, h].float().cpu().numpy()
+        assert abs(neff[i, t, h].item() - n) <= tol
+        assert np.isnan(row[seen]).all() and np.isfinite(np.delete(row, seen)).all()
+        if not seen:
+            check(clean, out, neff, [M, M], {(i, t, h)})
