@@ -60,6 +60,17 @@ polar_status_t polar_attn_selftest_decode_per_head(const void *q, const void *kv
  */
 int polar_attn_selftest_fwd_host_segments(int T, int *seg_lo, int *seg_hi, int cap);
 
+/*
+ * Host logic only (no device work): the copying thread of the drafted trees'
+ * tensor-core kernel, gone through on counters for a share of `tiles` tiles with
+ * steps[i] steps each (at least one).  fail_at: the number of the wait, from 0,
+ * that runs out (negative: none).  *waits gets the number of waits before the
+ * last copies are waited for.  Returns how many barriers are then left before
+ * their last copy has landed (0 is right), or -1 for bad arguments.  Host
+ * pointers, owned by the caller.
+ */
+int polar_attn_selftest_tree_copies(const int *steps, int tiles, int fail_at, int *waits);
+
 #ifdef __cplusplus
 }
 #endif

@@ -43,6 +43,7 @@
 #include <type_traits>
 
 #include "decode_tree.cuh"
+#include "polar_attn_selftest.h"
 #include "polar_internal.h"
 #include "tc_common.cuh"
 
@@ -205,6 +206,31 @@ struct Walk {
     }
 };
 
+// The copying thread's way through a share: a tile's queries once the tile before
+// has formed its last scores, then its steps, each once its stage is free again.
+// A wait that runs out ends it.  Every copy has landed on return, whichever way it
+// ended: of each barrier, the phase of its last load is waited for.
+#pragma nv_exec_check_disable
+template <typename Share, typename Port>
+__host__ __device__ __forceinline__ void copy_share(Share &share, Port &port) {
+    int tiles = 0, it = 0;  // loads so far
+    bool ok = true;
+    for (; ok && share.left > 0; share.next()) {
+        if (tiles > 0 && !(ok = port.queries_free((tiles - 1) & 1))) break;
+        port.load_queries(share);
+        ++tiles;
+        const int n = share.count();
+        for (int j = 0; j < n; ++j, ++it) {
+            const int st = it % kStagesTc;
+            if (it >= kStagesTc && !(ok = port.stage_free(st, (it / kStagesTc - 1) & 1))) break;
+            port.load_step(share, j, st);
+        }
+    }
+    if (tiles > 0) port.queries_landed((tiles - 1) & 1);
+    for (int j = it > kStagesTc ? it - kStagesTc : 0; j < it; ++j)
+        port.step_landed(j % kStagesTc, (j / kStagesTc) & 1);
+}
+
 template <int G>
 __device__ __forceinline__ long long steps_of(const TreeArgs &a, int seq) {
     const int nodes = tree_nodes(a.seqlens, a.tree_lens, seq, a.tree, a.max_pages);
@@ -316,20 +342,33 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
         if (lane == 0) {
             tma_prefetch_desc(&q_map);
             tma_prefetch_desc(&kv_map);
-            bool ok = true;
-            int tiles = 0;
-            for (; ok && walk.left > 0; walk.next(), ++tiles) {
-                const int npg = walk.per_tile - 1, g = walk.head(), s0 = walk.step;
-                const int n = walk.count();
-                const int32_t *pt = a.page_table + static_cast<size_t>(walk.seq) * a.max_pages + s0;
-                int id = s0 < npg ? pt[0] : 0;
-                // The queries, once the tile before has formed its last scores.
-                if (tiles > 0 && !(ok = mbar_wait(&q_empty, (tiles - 1) & 1, a.status))) break;
-                mbar_arrive_expect_tx(&q_full, kQBytes);
-                tma_load_3d(smem, &q_map, 0, g * G,
-                            walk.seq * a.tree + (walk.row0() - 32 * walk.quarter()) / G, &q_full);
-                for (int j = 0; j < n; ++j, ++it) {
-                    const int st = it % kStagesTc;
+            struct Port {
+                const CUtensorMap &q_map, &kv_map, &k_map, &v_map;
+                const TreeArgs &a;
+                uint8_t *smem, *ring;
+                uint64_t *q_full, *q_empty, *full, *empty;
+                const int32_t *pt;            // the tile's page ids from its first step on
+                int npg, g, seq, s0, n, id;   // id: the next step's page
+
+                __device__ __forceinline__ bool queries_free(uint32_t parity) {
+                    return mbar_wait(q_empty, parity, a.status);
+                }
+                __device__ __forceinline__ void load_queries(const Walk<G> &x) {
+                    npg = x.per_tile - 1;
+                    g = x.head();
+                    seq = x.seq;
+                    s0 = x.step;
+                    n = x.count();
+                    pt = a.page_table + static_cast<size_t>(seq) * a.max_pages + s0;
+                    id = s0 < npg ? pt[0] : 0;
+                    mbar_arrive_expect_tx(q_full, kQBytes);
+                    tma_load_3d(smem, &q_map, 0, g * G,
+                                seq * a.tree + (x.row0() - 32 * x.quarter()) / G, q_full);
+                }
+                __device__ __forceinline__ bool stage_free(int st, uint32_t parity) {
+                    return mbar_wait(&empty[st], parity, a.status);
+                }
+                __device__ __forceinline__ void load_step(const Walk<G> &, int j, int st) {
                     int phys = id;
                     id = j + 1 < n && s0 + j + 1 < npg ? pt[j + 1] : 0;
                     // A page id outside the pool is reported; its step reads page
@@ -338,25 +377,27 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                         record_error(a.status, POLAR_ERR_BAD_PAGE);
                         phys = 0;
                     }
-                    if (it >= kStagesTc &&
-                        !(ok = mbar_wait(&empty[st], (it / kStagesTc - 1) & 1, a.status)))
-                        break;
                     uint8_t *dst = ring + st * kStageBytes;
                     mbar_arrive_expect_tx(&full[st], kStageBytes);
                     if (s0 + j == npg) {
-                        tma_load_3d(dst, &k_map, 0, g, walk.seq * a.tree, &full[st]);
-                        tma_load_3d(dst + kChunkBytes, &v_map, 0, g, walk.seq * a.tree, &full[st]);
+                        tma_load_3d(dst, &k_map, 0, g, seq * a.tree, &full[st]);
+                        tma_load_3d(dst + kChunkBytes, &v_map, 0, g, seq * a.tree, &full[st]);
                     } else {
                         const int at = (phys * 2 * a.Hkv + g) * kPage;  // K block of the kv head
                         tma_load_2d(dst, &kv_map, 0, at, &full[st]);
                         tma_load_2d(dst + kChunkBytes, &kv_map, 0, at + a.Hkv * kPage, &full[st]);
                     }
                 }
-            }
-            // Every copy lands before shared memory is released.
-            if (tiles > 0 || !ok) mbar_wait(&q_full, (tiles - (ok ? 1 : 0)) & 1, a.status);
-            for (int j = max(0, it - kStagesTc); j < it; ++j)
-                mbar_wait(&full[j % kStagesTc], (j / kStagesTc) & 1, a.status);
+                __device__ __forceinline__ void queries_landed(uint32_t parity) {
+                    mbar_wait(q_full, parity, a.status);
+                }
+                __device__ __forceinline__ void step_landed(int st, uint32_t parity) {
+                    mbar_wait(&full[st], parity, a.status);
+                }
+            };
+            Port port{q_map, kv_map, k_map, v_map, a, smem, ring, &q_full, &q_empty, full, empty,
+                      nullptr, 0, 0, 0, 0, 0, 0};
+            copy_share(walk, port);
         }
         __syncwarp();
     } else if (w == 5) {
@@ -733,3 +774,46 @@ cudaError_t launch_tree_tc(const CUtensorMap &kv, const CUtensorMap &k, const CU
 }
 
 }  // namespace polar
+
+namespace {
+
+// copy_share()'s port on the host: counts loads and waits; the wait number
+// `fail_at` runs out.
+struct CountingPort {
+    int fail_at, waits = 0, queries = 0, steps[polar::kStagesTc] = {};
+    int missed = 0;  // waits at the end that are not for a barrier's last load
+
+    bool wait() { return waits++ != fail_at; }
+    bool queries_free(uint32_t) { return wait(); }
+    bool stage_free(int, uint32_t) { return wait(); }
+    template <typename Share> void load_queries(const Share &) { ++queries; }
+    template <typename Share> void load_step(const Share &, int, int st) { ++steps[st]; }
+    void queries_landed(uint32_t parity) { landed(queries, parity); }
+    void step_landed(int st, uint32_t parity) { landed(steps[st], parity); }
+    void landed(int &loads, uint32_t parity) {  // of a barrier: loads 0, 1, .. have parities 0, 1, ..
+        if (loads == 0 || ((loads - 1) & 1u) != parity) ++missed;
+        loads = 0;
+    }
+};
+
+struct CountedShare {
+    const int *steps;
+    int left;  // tiles
+    int count() const { return *steps; }
+    void next() { ++steps, --left; }
+};
+
+}  // namespace
+
+int polar_attn_selftest_tree_copies(const int *steps, int tiles, int fail_at, int *waits) {
+    if (!steps || !waits || tiles < 0) return -1;
+    for (int i = 0; i < tiles; ++i)
+        if (steps[i] < 1) return -1;
+    CountedShare share{steps, tiles};
+    CountingPort port{fail_at};
+    polar::copy_share(share, port);
+    *waits = port.waits;
+    port.missed += port.queries != 0;
+    for (int x : port.steps) port.missed += x != 0;
+    return port.missed;
+}

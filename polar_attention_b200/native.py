@@ -37,7 +37,7 @@ EXPORTS = ["polar_attn_default_params", "polar_attn_fwd_workspace_size", "polar_
            "polar_gdelta_prefill_workspace_size", "polar_gdelta_prefill", "polar_gdelta_step",
            "polar_attn_selftest_timeout", "polar_attn_selftest_decode_per_head",
            "polar_attn_fwd_state_size", "polar_attn_fwd_train", "polar_attn_bwd_from_state",
-           "polar_attn_selftest_fwd_host_segments",
+           "polar_attn_selftest_fwd_host_segments", "polar_attn_selftest_tree_copies",
            "polar_attn_decode_tree_workspace_size", "polar_attn_decode_paged_tree",
            "polar_attn_decode_sparse_workspace_size", "polar_attn_decode_paged_sparse",
            "polar_attn_cache_workspace_size", "polar_attn_cache_reserve",
@@ -124,6 +124,8 @@ def lib() -> ctypes.CDLL:
             IP = ctypes.POINTER(ctypes.c_int)
             L.polar_attn_selftest_fwd_host_segments.argtypes = [I, IP, IP, I]
             L.polar_attn_selftest_fwd_host_segments.restype = I
+            L.polar_attn_selftest_tree_copies.argtypes = [IP, I, I, IP]
+            L.polar_attn_selftest_tree_copies.restype = I
             GP = ctypes.POINTER(GdeltaParams)
             L.polar_gdelta_prefill_workspace_size.argtypes = [GP]
             L.polar_gdelta_prefill_workspace_size.restype = Z
@@ -174,6 +176,19 @@ def fwd_host_segments(T: int, cap: int = 64):
     if n < 0:
         raise ValueError(f"polar_attn_selftest_fwd_host_segments: bad arguments (T={T}, cap={cap})")
     return [(lo[i], hi[i]) for i in range(n)]
+
+
+def tree_copies(steps, fail_at: int = -1):
+    """The copying thread of the drafted trees' tensor-core kernel on counters, for
+    tiles of these numbers of steps, with its wait number fail_at running out
+    (host logic; no device work).  Returns (barriers left before their last copy
+    has landed, waits on the way)."""
+    waits = ctypes.c_int()
+    n = lib().polar_attn_selftest_tree_copies((ctypes.c_int * max(len(steps), 1))(*steps),
+                                              len(steps), int(fail_at), ctypes.byref(waits))
+    if n < 0:
+        raise ValueError(f"polar_attn_selftest_tree_copies: bad arguments (steps={steps})")
+    return n, waits.value
 
 
 def status_string(code: int) -> str:
