@@ -6,8 +6,18 @@
 // mma.sync m16n8k16 (bf16 in, fp32 accumulate): lane (gq, tq) owns row gq and,
 // with two row sets, gq + 8.  Each row keeps the method's state:
 // reference max m_ref (log2 units, moved lazily), l, l2 (rescaled by r and
-// r^2 when it moves), the raw dots' sums S1, S2 and max, and the value
-// accumulator.  The S fragments are the P operand of the second product.
+// r^2 when it moves), the raw dots' number, mean, sum of squared deviations and
+// max, and the value accumulator.  The S fragments are the P operand of the
+// second product.
+//
+// The null floor takes the spread of a row's raw dots.  Where keys are alike it is
+// a small part of their mean, and S2/n - (S1/n)^2 of sums in fp32 loses it (a chain
+// of 65536 dots of 0.77: 0.004 instead of 0, which at a scale of 16 is 0.07 of the
+// gate).  So deviations are summed about means: each step's own, joined to the
+// row's by the number of dots on both sides (Chan, Golub and LeVeque's update), and
+// parts of a row about their common mean: nothing large cancels.  Against the plain
+// sums: 8 nodes of one sequence 12.8 and 12.9 us, 256 selected pages of 16 long
+// sequences 84.3 and 85.4; tcgen05, 26 nodes 65 and 70, 64 nodes 236 and 239.
 #pragma once
 
 #include "launch.cuh"
@@ -15,10 +25,25 @@
 
 namespace polar {
 
+struct Moments {  // of n raw dots: mean, sum of squared deviations from it
+    float n, mean, m2;
+
+    // Joins k more dots (kMaybeNone: possibly none, then of mean 0).
+    template <bool kMaybeNone>
+    __device__ __forceinline__ void join(float k, float k_mean, float k_m2) {
+        const float all = n + k, d = k_mean - mean;
+        const float f = kMaybeNone && k == 0.f ? 0.f : __fdividef(k, all);
+        mean = fmaf(d, f, mean);
+        m2 += fmaf(d * d, n * f, k_m2);
+        n = all;
+    }
+};
+
 template <int kHR>
 struct RowTile {
     uint32_t qa[kHR][4][2];
-    float cl2[kHR], m_ref[kHR], m_raw[kHR], l[kHR], l2[kHR], s1[kHR], s2[kHR];
+    float cl2[kHR], m_ref[kHR], m_raw[kHR], l[kHR], l2[kHR];
+    Moments dots[kHR];
     float acc[8][4];
     uint32_t pa[kHR][2];  // this page's weights, the A operand of P V
 
@@ -26,7 +51,8 @@ struct RowTile {
 #pragma unroll
         for (int hr = 0; hr < kHR; ++hr) {
             m_ref[hr] = m_raw[hr] = -INFINITY;
-            l[hr] = l2[hr] = s1[hr] = s2[hr] = 0.f;
+            l[hr] = l2[hr] = 0.f;
+            dots[hr] = Moments{0.f, 0.f, 0.f};
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
@@ -63,7 +89,7 @@ struct RowTile {
 #pragma unroll
         for (int hr = 0; hr < kHR; ++hr) {
             bool vld[2][2];
-            float tmax = -INFINITY, ts1 = 0.f, ts2 = 0.f;
+            float tmax = -INFINITY, ts1 = 0.f, ts2 = 0.f, seen = 4.f;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -72,12 +98,19 @@ struct RowTile {
                     const float x = vld[nt][e] ? sc[nt][2 * hr + e] : 0.f;
                     tmax = fmaxf(tmax, vld[nt][e] ? x : -INFINITY);
                     ts1 += x;
-                    ts2 = fmaf(x, x, ts2);
                 }
+            if (!kAll) seen = static_cast<float>(__popc(bits[hr] & 15u));
+            const float mean = kAll ? 0.25f * ts1 : seen > 0.f ? __fdividef(ts1, seen) : 0.f;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float d = vld[nt][e] ? sc[nt][2 * hr + e] - mean : 0.f;
+                    ts2 = fmaf(d, d, ts2);
+                }
+            dots[hr].template join<!kAll>(seen, mean, ts2);
             tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
             tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
-            s1[hr] += ts1;
-            s2[hr] += ts2;
             m_raw[hr] = fmaxf(m_raw[hr], tmax);
             const float zmax = tmax * cl2[hr];
             if (zmax > m_ref[hr] + kRescaleThreshold) {  // uniform over the quad of the row
@@ -232,7 +265,8 @@ __device__ __forceinline__ void compute_steps(PageRing &r, int np, int lane, int
 // A row's merged state, spread over eight lanes: lane j of them holds value
 // columns 8j .. 8j + 7; the statistics are the same in all.
 struct RowState {
-    float M, m_raw, l, l2, s1, s2;
+    float M, m_raw, l, l2;
+    Moments dots;
     float4 o[2];
 };
 
@@ -244,16 +278,29 @@ __device__ __forceinline__ RowState merge_parts(int count, Part &&part) {
     const int j = threadIdx.x & 7;
     RowState x;
     x.M = x.m_raw = -INFINITY;
-    x.l = x.l2 = x.s1 = x.s2 = 0.f;
+    x.l = x.l2 = 0.f;
+    x.dots = Moments{0.f, 0.f, 0.f};
     x.o[0] = x.o[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = j; k < count; k += 8) x.M = fmaxf(x.M, part(k)[64]);
+    float sum = 0.f;
+    for (int k = j; k < count; k += 8) {
+        const float *p = part(k);
+        const float2 dots = *reinterpret_cast<const float2 *>(p + 68);
+        x.M = fmaxf(x.M, p[64]);
+        x.dots.n += dots.x;
+        sum = fmaf(dots.x, dots.y, sum);
+    }
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) x.M = fmaxf(x.M, __shfl_xor_sync(~0u, x.M, o));
+    for (int o = 1; o < 8; o <<= 1) {
+        x.M = fmaxf(x.M, __shfl_xor_sync(~0u, x.M, o));
+        x.dots.n += __shfl_xor_sync(~0u, x.dots.n, o);
+        sum += __shfl_xor_sync(~0u, sum, o);
+    }
+    x.dots.mean = x.dots.n > 0.f ? sum / x.dots.n : 0.f;
 #pragma unroll 4
     for (int k = 0; k < count; ++k) {
         const float *p = part(k);
         const float4 st = *reinterpret_cast<const float4 *>(p + 64);
-        const float2 ss = *reinterpret_cast<const float2 *>(p + 68);
+        const float4 dots = *reinterpret_cast<const float4 *>(p + 68);  // n, mean, m2
         const float4 a = *reinterpret_cast<const float4 *>(p + 8 * j);
         const float4 b = *reinterpret_cast<const float4 *>(p + 8 * j + 4);
         const float r = x.M == -INFINITY ? 0.f : exp2f(st.x - x.M);  // st.x: reference max, log2
@@ -263,8 +310,8 @@ __device__ __forceinline__ RowState merge_parts(int count, Part &&part) {
                              fmaf(a.z, r, x.o[0].z), fmaf(a.w, r, x.o[0].w));
         x.o[1] = make_float4(fmaf(b.x, r, x.o[1].x), fmaf(b.y, r, x.o[1].y),
                              fmaf(b.z, r, x.o[1].z), fmaf(b.w, r, x.o[1].w));
-        x.s1 += ss.x;
-        x.s2 += ss.y;
+        const float d = dots.y - x.dots.mean;
+        x.dots.m2 += fmaf(dots.x * d, d, dots.z);
         x.m_raw = fmaxf(x.m_raw, st.y);
     }
     return x;
@@ -276,12 +323,22 @@ __device__ __forceinline__ void store_part(const RowState &x, float *dst, bool r
     *reinterpret_cast<float4 *>(dst + 8 * j) = x.o[0];
     *reinterpret_cast<float4 *>(dst + 8 * j + 4) = x.o[1];
     if (j == 0) *reinterpret_cast<float4 *>(dst + 64) = make_float4(x.M, x.m_raw, x.l, x.l2);
-    if (j == 1) *reinterpret_cast<float2 *>(dst + 68) = make_float2(x.s1, x.s2);
+    if (j == 1)
+        *reinterpret_cast<float4 *>(dst + 68) = make_float4(x.dots.n, x.dots.mean, x.dots.m2, 0.f);
 }
 
 struct Epilogue {  // the method's constants at a row's end
     float s, alpha, L, beta, inv_ln_L;
 };
+
+// The magnitude of a row of n visible keys (n > 0) and its n_eff.  The gate depends
+// on how far the largest dot lies above the mean and on the spread alone, so the
+// mean is taken off first.
+__device__ __forceinline__ float row_magnitude(float l, float l2, float m_raw, const Moments &dots,
+                                               float n, const Epilogue &e, float *neff) {
+    return polar_magnitude(l, l2, m_raw - dots.mean, 0.f, dots.m2,
+                           e.s * length_temperature(n, e.alpha, e.L), n, e.beta, e.inv_ln_L, neff);
+}
 
 // out = content + count and n_eff of a row of n visible keys, by eight lanes
 // (all lanes of the warp are here; rows that are not `real` are not written).
@@ -291,11 +348,7 @@ __device__ __forceinline__ void finish_row(const RowState &x, int n, const Epilo
                                            float *neff_out, bool real) {
     const int j = threadIdx.x & 7;
     float ne = 0.f, mag = 0.f;
-    if (n > 0) {
-        const float nf = static_cast<float>(n);
-        const float c = e.s * length_temperature(nf, e.alpha, e.L);
-        mag = polar_magnitude(x.l, x.l2, x.m_raw, x.s1, x.s2, c, nf, e.beta, e.inv_ln_L, &ne);
-    }
+    if (n > 0) mag = row_magnitude(x.l, x.l2, x.m_raw, x.dots, static_cast<float>(n), e, &ne);
     float o[8] = {x.o[0].x, x.o[0].y, x.o[0].z, x.o[0].w, x.o[1].x, x.o[1].y, x.o[1].z, x.o[1].w};
     float sq = 0.f;
 #pragma unroll
@@ -322,19 +375,24 @@ __device__ __forceinline__ void spill_states(RowTile<kHR> &t, float *parts, int 
     const int gq = lane >> 2, tq = lane & 3;
 #pragma unroll
     for (int hr = 0; hr < kHR; ++hr) {
+        float n = t.dots[hr].n, sum = n * t.dots[hr].mean;
 #pragma unroll
         for (int o = 1; o <= 2; o <<= 1) {
             t.l[hr] += __shfl_xor_sync(0xffffffffu, t.l[hr], o);
             t.l2[hr] += __shfl_xor_sync(0xffffffffu, t.l2[hr], o);
-            t.s1[hr] += __shfl_xor_sync(0xffffffffu, t.s1[hr], o);
-            t.s2[hr] += __shfl_xor_sync(0xffffffffu, t.s2[hr], o);
+            n += __shfl_xor_sync(0xffffffffu, n, o);
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
             t.m_raw[hr] = fmaxf(t.m_raw[hr], __shfl_xor_sync(0xffffffffu, t.m_raw[hr], o));
         }
+        const float mean = n > 0.f ? sum / n : 0.f, d = t.dots[hr].mean - mean;
+        float m2 = fmaf(t.dots[hr].n * d, d, t.dots[hr].m2);
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
         float *p = parts + ((8 * hr + gq) * 4 + w) * kPartialFloats;
         if (tq == 0) {
             *reinterpret_cast<float4 *>(p + 64) =
                 make_float4(t.m_ref[hr], t.m_raw[hr], t.l[hr], t.l2[hr]);
-            *reinterpret_cast<float2 *>(p + 68) = make_float2(t.s1[hr], t.s2[hr]);
+            *reinterpret_cast<float4 *>(p + 68) = make_float4(n, mean, m2, 0.f);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)

@@ -99,9 +99,12 @@ constexpr size_t record_bytes(long long tiles) {
 // One pass over a thread's 32 scores against its reference max: the weights
 // 2^(cl2 S - m_ref) as packed bf16 (operands of the second product, off by at
 // most half a step, 2^-8 of themselves; the sums take them unrounded), their
-// sums, the raw sums and the max.  Scores whose mask bit is clear do not count.
+// sums, the max, and the raw scores' sums about one of them, `from`: the distance of
+// one of 32 scores from their mean is in the sum of squares, too, so that at most
+// five bits of it go when the mean is taken off.  Scores whose mask bit is clear do
+// not count.
 struct TileSums {
-    float top, s1, s2, l, l2;
+    float top, from, s1, s2, l, l2;
 };
 template <bool kAll>
 __device__ __forceinline__ TileSums tile_pass(const uint32_t (&sr)[32], uint32_t mask, float cl2,
@@ -109,12 +112,21 @@ __device__ __forceinline__ TileSums tile_pass(const uint32_t (&sr)[32], uint32_t
     const float2 sc = make_float2(cl2, cl2), nm = make_float2(-m_ref, -m_ref);
     float mx[2] = {-INFINITY, -INFINITY};
     float2 a1 = make_float2(0.f, 0.f), a2 = a1, la = a1, l2a = a1;
+    float from = __uint_as_float(sr[0]);
+    if (!kAll) {
+        from = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            from = fmaxf(from, mask >> e & 1u ? __uint_as_float(sr[e]) : -INFINITY);
+    }
+    const float2 off = make_float2(-from, -from);
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
         float2 v = make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
         const bool v0 = kAll || (mask >> e & 1u), v1 = kAll || (mask >> (e + 1) & 1u);
         const float2 z = f2_fma(v, sc, nm);
         mx[(e >> 1) & 1] = max3(mx[(e >> 1) & 1], v0 ? v.x : -INFINITY, v1 ? v.y : -INFINITY);
+        v = f2_add(v, off);
         if (!kAll) v = make_float2(v0 ? v.x : 0.f, v1 ? v.y : 0.f);
         a1 = f2_add(a1, v);
         a2 = f2_fma(v, v, a2);
@@ -124,7 +136,8 @@ __device__ __forceinline__ TileSums tile_pass(const uint32_t (&sr)[32], uint32_t
         l2a = f2_fma(p, p, l2a);
         pk[e >> 1] = pack_bf16(p.x, p.y);
     }
-    return TileSums{fmaxf(mx[0], mx[1]), a1.x + a1.y, a2.x + a2.y, la.x + la.y, l2a.x + l2a.y};
+    return TileSums{fmaxf(mx[0], mx[1]), from, a1.x + a1.y, a2.x + a2.y, la.x + la.y,
+                    l2a.x + l2a.y};
 }
 
 // 16 n columns of fp32 of this thread's lane of tensor memory, times r.  The stores
@@ -156,7 +169,8 @@ __device__ __forceinline__ void scale_weights(uint32_t t, float r) {
 }
 
 struct RowStats {  // one row's streaming state, in its thread
-    float m_ref, m_raw, l, l2, s1, s2;
+    float m_ref, m_raw, l, l2;
+    Moments dots;
 };
 
 // What the CTA in which a tile begins leaves to the merge.
@@ -480,7 +494,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
             const float cl2 = a.ep.s * length_temperature(static_cast<float>(n), a.ep.alpha,
                                                           a.ep.L) * kLog2e;
             const int32_t *pt = a.page_table + static_cast<size_t>(walk.seq) * a.max_pages;
-            RowStats x{-INFINITY, -INFINITY, 0.f, 0.f, 0.f, 0.f};
+            RowStats x{-INFINITY, -INFINITY, 0.f, 0.f, {0.f, 0.f, 0.f}};
             // Step `it` (`first`: the tile's, O holds nothing yet).  kAll: every row
             // sees all of its keys; else the bits of `mask`.
             auto soft_step = [&](auto kAll, uint64_t mask, bool first) {
@@ -516,8 +530,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                             if (h > 0) scale_weights(tS, r);
                         }
                         x.m_raw = fmaxf(x.m_raw, t.top);
-                        x.s1 += t.s1;
-                        x.s2 += t.s2;
+                        if (decltype(kAll)::value) {
+                            x.dots.template join<false>(32.f, fmaf(t.s1, 1.f / 32, t.from),
+                                                        fmaf(-t.s1, t.s1 * (1.f / 32), t.s2));
+                        } else {
+                            const int k = __popc(static_cast<uint32_t>(mask >> (32 * h)));
+                            const float m = k > 0 ? t.s1 / static_cast<float>(k) : 0.f;
+                            x.dots.template join<true>(static_cast<float>(k), k > 0 ? t.from + m : 0.f,
+                                                       fmaf(-t.s1, m, t.s2));
+                        }
                         x.l += t.l;
                         x.l2 += t.l2;
                         tmem_st16(tS + 16 * h, pk);
@@ -617,7 +638,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                             make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
                 *reinterpret_cast<float4 *>(part + 64) = make_float4(x.m_ref, x.m_raw, x.l, x.l2);
-                *reinterpret_cast<float2 *>(part + 68) = make_float2(x.s1, x.s2);
+                *reinterpret_cast<float4 *>(part + 68) =
+                    make_float4(x.dots.n, x.dots.mean, x.dots.m2, 0.f);
             } else {
                 float sq = 0.f, ne = 0.f, mag = 0.f;
 #pragma unroll 1
@@ -628,12 +650,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                     for (int e = 0; e < 16; ++e)
                         sq = fmaf(__uint_as_float(o[e]), __uint_as_float(o[e]), sq);
                 }
-                if (n > 0) {
-                    const float nf = static_cast<float>(n);
-                    mag = polar_magnitude(x.l, x.l2, x.m_raw, x.s1, x.s2,
-                                          a.ep.s * length_temperature(nf, a.ep.alpha, a.ep.L), nf,
-                                          a.ep.beta, a.ep.inv_ln_L, &ne);
-                }
+                if (n > 0)
+                    mag = row_magnitude(x.l, x.l2, x.m_raw, x.dots, static_cast<float>(n), a.ep,
+                                        &ne);
                 const float inv = n > 0 ? 1.0f / fmaxf(sqrtf(sq), 1e-30f) : 0.f;
                 const int h = g * G + row % G;
                 const size_t out_row = (node0 + row / G) * a.Hq + h;

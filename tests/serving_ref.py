@@ -170,3 +170,28 @@ class HostCache:
             for c in range(-(-lens[i] // PAGE)):
                 table[i, c] = to.get(int(table[i, c]), table[i, c])
         return n
+
+
+# --------------------------------------------------- keys that are alike ---
+
+ALIKE = ["equal", "near", "outliers first", "outlier last"]
+
+
+def alike_keys(kind, key, n, rng):
+    """n keys along `key` (float64 unit vector), up to the kind: the spread of a
+    row's products is then far below their mean, and with it the null floor."""
+    a = np.ones(n)
+    if kind == "near":
+        a -= rng.integers(0, 3, n) / 256
+    elif kind == "outliers first":
+        a[:PAGE] = -1
+    elif kind == "outlier last":
+        a[-1] = -1
+    return torch.from_numpy(a[:, None] * key).bfloat16()
+
+
+def at_angle(key, dot, shape, rng):
+    """Unit vectors (float64) whose product with the unit vector `key` is `dot`."""
+    x = rng.standard_normal((*shape, DIM))
+    x -= (x @ key)[..., None] * key
+    return dot * key + np.sqrt(1 - dot ** 2) * x / np.linalg.norm(x, axis=-1, keepdims=True)

@@ -227,3 +227,26 @@ def test_bad_pages_and_lengths_are_reported(cuda_ok):
                                selected=sel, **ARGS)
         assert pa.get_status() == 7
         assert (out[0] == 7).all() and (sel[0] == 7).all() and (out[1] != 7).any()
+
+
+@pytest.mark.parametrize("kind", R.ALIKE)
+@pytest.mark.parametrize("Hq,keep", [(1, 40), (4, 513), (8, 1100)])
+def test_keys_that_are_alike(cuda_ok, Hq, keep, kind):
+    """Keys and values alike over many selected pages: the null floor's spread is
+    not what sums of squares lose beside the squared mean."""
+    n = 70001
+    x = inputs([n], Hq, 1, seed=15)
+    rng = np.random.default_rng(15)
+    key = R.at_angle(np.eye(64)[0], 0.1, (), rng)
+    x["q"] = torch.from_numpy(R.at_angle(key, 0.77, (1, Hq), rng)).bfloat16()
+    page = x["table"][0].long()
+    keys = torch.zeros((page.numel() * 64, 64), dtype=torch.bfloat16)
+    keys[:n] = R.alike_keys(kind, key, n, rng)
+    keys[n:] = keys[n - 1]
+    x["kv"][page, 0, 0] = keys.view(-1, 64, 64)
+    x["kv"][page, 1, 0] = x["kv"][0, 1, 0, 0].clone()
+    x["bounds"] = torch.stack((x["kv"][:, 0].amin(2), x["kv"][:, 0].amax(2)), 2).contiguous()
+    x["u"] = torch.randn(x["u"].shape, generator=torch.Generator().manual_seed(15))
+    out, neff, sel = call(cuda(x), keep, L=2048)
+    assert pa.get_status() == 0
+    check(x, keep, out, neff, sel, L=2048)

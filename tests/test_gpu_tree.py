@@ -392,3 +392,30 @@ def test_rows_add_different_numbers_of_values(cuda_ok, G, M, lens):
         assert np.isnan(row[seen]).all() and np.isfinite(np.delete(row, seen)).all()
         if not seen:
             check(clean, out, neff, [M, M], {(i, t, h)})
+
+
+@pytest.mark.parametrize("kind", R.ALIKE)
+@pytest.mark.parametrize("G,M,max_pages", [(1, 1, 1025), (4, 4, 1025), (4, 16, WIDE), (8, 64, WIDE)])
+def test_keys_that_are_alike(cuda_ok, G, M, max_pages, kind):
+    """Long caches whose keys are alike: the null floor's spread is not what sums
+    of squares lose beside the squared mean.  Values alike, too, so that the
+    direction is certain, and a count of the direction's size."""
+    lens = [65536, 20011]
+    x = inputs(lens, M, G, 1, seed=17, max_pages=max_pages)
+    rng = np.random.default_rng(17)
+    key = R.at_angle(np.eye(64)[0], 0.1, (), rng)
+    x["q"] = torch.from_numpy(R.at_angle(key, 0.77, x["q"].shape[:-1], rng)).bfloat16()
+    value = along(1, np.float64(0.3), rng)
+    for i, n in enumerate(lens):
+        page = x["table"][i, :-(-n // 64)].long()
+        keys = torch.full((page.numel() * 64, 64), float("nan"), dtype=torch.bfloat16)
+        keys[:n] = R.alike_keys(kind, key, n, rng)
+        x["kv"][page, 0, 0] = keys.view(-1, 64, 64)
+        x["kv"][page, 1, 0] = value
+    x["k"][:] = R.alike_keys("equal", key, 1, rng)[0]
+    x["v"][:] = value
+    x["u"] = torch.randn(x["u"].shape, generator=torch.Generator().manual_seed(17))
+    out, neff = call(cuda(x), L=2048)
+    assert pa.get_status() == 0
+    rows = {(i, t, h) for i in (0, 1) for t in {0, M // 3, M // 2, M - 1} for h in {0, G - 1}}
+    check(x, out, neff, [M, M], rows, L=2048)
