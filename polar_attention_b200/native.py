@@ -740,22 +740,29 @@ class PageCache:
     """A paged KV cache: the pool kv_pages [P,2,Hkv,64,64] bf16, the references
     refs [P] int32 (page-table entries that name a page; 0: free; None for a
     caller with an allocator of its own, who then only appends) and the pages'
-    key bounds [P,Hkv,2,64] bf16 (None: not kept).  Holds the tensors; page
-    tables and lengths are arguments of each call."""
-    __slots__ = ("kv_pages", "refs", "bounds", "_c", "_p", "_dev", "_pages", "_heads")
+    key bounds [P,Hkv,2,64] bf16 (None: not kept).  Holds the tensors, whose
+    contents may change but which stay the same three: another pool, or a smaller
+    one after a compaction, is another PageCache.  Page tables and lengths are
+    arguments of each call."""
+    __slots__ = ("_tensors", "_c", "_p", "_dev", "_pages", "_heads")
 
     def __init__(self, kv_pages, refs=None, bounds=None):
         P_, Hkv = _pool_shape(kv_pages, 64)
         dev, bf16 = kv_pages.get_device(), torch.bfloat16
         if dev < 0:
             raise ValueError("inputs must be contiguous CUDA tensors")
-        self.kv_pages, self.refs, self.bounds = kv_pages, refs, bounds
+        self._tensors = (kv_pages, refs, bounds)
         self._c = Cache(
             _need("kv_pages", kv_pages, bf16, (P_, 2, Hkv, 64, 64), dev),
             None if bounds is None else _need("bounds", bounds, bf16, (P_, Hkv, 2, 64), dev),
             None if refs is None else _need("refs", refs, torch.int32, (P_,), dev), P_, Hkv, 64,
             POLAR_BF16)
         self._p, self._dev, self._pages, self._heads = ctypes.byref(self._c), dev, P_, Hkv
+
+    # Read only: the calls use the addresses that were checked above.
+    kv_pages = property(lambda self: self._tensors[0])
+    refs = property(lambda self: self._tensors[1])
+    bounds = property(lambda self: self._tensors[2])
 
 
 @functools.lru_cache(maxsize=256)

@@ -200,3 +200,12 @@ def test_reference_row_by_hand():
     v[0, 3] = 2.0
     out, neff, _, _ = R.mixing_row(v[0], v, v, np.ones(64), 8.0, 0.3, 128, 1.0)
     assert neff == 1.0 and out[3] == 1.0 and abs(out).sum() == 1.0
+
+
+@pytest.mark.parametrize("name", ["kv_pages", "refs", "bounds"])
+def test_a_cache_keeps_its_tensors(name):
+    """The calls use the addresses that a cache was built with: a tensor put in a
+    cache's place later is turned down, not passed over in silence."""
+    c = N.PageCache.__new__(N.PageCache)
+    with pytest.raises(AttributeError):
+        setattr(c, name, None)

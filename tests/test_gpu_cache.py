@@ -476,3 +476,23 @@ def test_beam_steps_on_a_stream(cuda_ok):
     live = np.arange(6)[None] < -(-p.lens // 64)[:, None]
     p.dtable = torch.where(torch.from_numpy(live).cuda(), p.dtable, -1)
     p.same()
+
+
+def test_a_shrunk_pool_is_another_cache(cuda_ok):
+    """After a compaction the pool's front goes on as a cache of its own; the old
+    cache takes no other tensors and still names its own."""
+    p = Pair(30, 2, 3, 8, seed=15)
+    p.grow([200, 300, 64])
+    p.free([0, -1, -1])
+    p.compact()
+    n = int((p.host.refs > 0).sum()) + 4
+    old = p.dev
+    with pytest.raises(AttributeError):
+        old.refs = old.refs[:n].clone()
+    p.dev = pa.PageCache(*(t[:n].clone() for t in (old.kv_pages, old.refs, old.bounds)))
+    p.host = R.HostCache(p.host.kv[:n], p.host.refs[:n], p.host.bounds[:n])
+    before = [t.clone() for t in (old.kv_pages, old.refs, old.bounds)]
+    p.grow([70, 20, 64])
+    assert p.reserve([128, 64, 0], status=NO_PAGES).tolist() == [0, 0, 0]
+    for a, b in zip(before, (old.kv_pages, old.refs, old.bounds)):
+        assert torch.equal(a, b)
