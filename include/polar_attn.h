@@ -63,7 +63,9 @@ typedef enum {
     POLAR_ERR_BAD_PAGE = 4,    /* device: page id outside [0, num_pages) */
     POLAR_ERR_TIMEOUT = 5,     /* device: a bounded wait ran out */
     POLAR_ERR_CUDA = 6,        /* a CUDA runtime call failed */
-    POLAR_ERR_BAD_SEQLEN = 7,  /* device: seqlen outside [1, max_pages*64] */
+    POLAR_ERR_BAD_SEQLEN = 7,  /* device: a sequence's length (1 .. max_pages*64, or from 0 on
+                                  where a call says so), node count, growth or token count
+                                  out of range */
     POLAR_ERR_BAD_SLOT = 8,    /* device: memory state slot >= num_slots (polar_gdelta.h), or
                                   a source row out of range (polar_cache.h) */
     POLAR_ERR_NO_PAGES = 9     /* device: the page pool ran out (polar_cache.h) */

@@ -919,7 +919,8 @@ const char *polar_attn_status_string(polar_status_t s) {
         case POLAR_ERR_BAD_PAGE: return "page id outside the page pool";
         case POLAR_ERR_TIMEOUT: return "a bounded device wait timed out";
         case POLAR_ERR_CUDA: return "CUDA runtime error";
-        case POLAR_ERR_BAD_SEQLEN: return "sequence length outside [1, 64*max_pages]";
+        case POLAR_ERR_BAD_SEQLEN:
+            return "sequence length, node count, growth or token count out of range";
         case POLAR_ERR_BAD_SLOT: return "memory state slot or source row out of range";
         case POLAR_ERR_NO_PAGES: return "no free page left in the page pool";
     }

@@ -209,3 +209,9 @@ def test_a_cache_keeps_its_tensors(name):
     c = N.PageCache.__new__(N.PageCache)
     with pytest.raises(AttributeError):
         setattr(c, name, None)
+
+
+def test_status_string_names_what_is_out_of_range(lib):
+    """Code 7 stands for lengths and for the counts of the tree and the cache."""
+    text = lib.polar_attn_status_string(7).decode()
+    assert all(word in text for word in ("length", "node", "growth", "count", "out of range"))
