@@ -382,8 +382,14 @@ polar_status_t polar_attn_decode_paged_tree(const void *q, const void *k, const 
  * others by score, the lower page first on a tie, a NaN score above all
  * others.  A sequence of at most `keep` pages is read whole and the row equals
  * polar_attn_decode_paged's.  The row is the mixing step over the positions of
- * the selected pages: n, and with it the length temperature and the null
- * floor, is their number.  params->window must be 0 (POLAR_ERR_UNSUPPORTED).
+ * the selected pages, as if the sequence were these pages: n, and with it the
+ * length temperature and the null floor, is their number.  Past `keep` pages it
+ * is therefore no estimate of the whole sequence's row: the direction follows a
+ * key that stands out, the temperature and the count do not.  (512 pages, 32
+ * kept, one planted key that is among them, in 64 bits, mean over draws: scale
+ * 8.0 where the whole sequence has 14.7, n_eff 8.5 and 1.16, the count's amount
+ * 0.26 and 0.02, cosine of the two directions 0.998.)  params->window must be 0
+ * (POLAR_ERR_UNSUPPORTED).
  * Errors as polar_attn_decode_paged (a sequence out of range leaves its
  * selected pages unwritten too).
  */

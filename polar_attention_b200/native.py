@@ -696,7 +696,10 @@ def decode_paged_sparse(q, kv_pages, bounds, page_table, seqlens, u, keep, out=N
                         stream=None, want_neff=True, want_selected=True):
     """Decode over at most `keep` pages per (sequence, kv head), chosen by a
     score on the pages' key bounds [P,Hkv,2,64] bf16 (smallest and largest key;
-    cache_append keeps them).  Other arguments as decode_paged.  Returns (out
+    cache_append keeps them).  A row is that of a sequence of the selected pages
+    alone: their number of positions is n in the length temperature and the null
+    floor (include/polar_attn.h says how far that is from the whole sequence's
+    row).  Other arguments as decode_paged.  Returns (out
     [N,Hq,64], neff [N,Hq], selected [N,Hkv,keep] int32: the logical pages
     read, ascending, then -1)."""
     N, Hq, D = q.shape

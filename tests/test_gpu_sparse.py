@@ -250,3 +250,23 @@ def test_keys_that_are_alike(cuda_ok, Hq, keep, kind):
     out, neff, sel = call(cuda(x), keep, L=2048)
     assert pa.get_status() == 0
     check(x, keep, out, neff, sel, L=2048)
+
+
+def test_row_is_that_of_the_selected_pages(cuda_ok):
+    """The plain decode over tables of the selected pages gives the same rows: n is
+    the number of selected positions, not the sequence's."""
+    x = inputs([64 * 90 + 7, 64 * 40, 64 * 300 + 64], 8, 2, seed=16)
+    d, keep = cuda(x), 20
+    out, neff, sel = call(d, keep)
+    for g in range(2):
+        table = d["table"].gather(1, sel[:, g].long())
+        lens = (keep - 1) * 64 + (d["lens"] - 1) % 64 + 1
+        want, nwant = pa.decode_paged(d["q"], d["kv"], table.contiguous(), lens.int(), d["u"], **ARGS)
+        heads = slice(4 * g, 4 * g + 4)
+        for i in range(3):  # both against 64 bits, over the same pages
+            keys, values = R.cached(R.f64(x["kv"]), table[i].cpu().numpy(), g, int(lens[i]))
+            refs = [R.mixing_row(R.f64(x["q"])[i, h], keys, values, R.f64(x["u"])[h], **ARGS)
+                    for h in range(4 * g, 4 * g + 4)]
+            R.check_rows(out[i, heads], neff[i, heads], refs)
+            R.check_rows(want[i, heads], nwant[i, heads], refs)
+    assert pa.get_status() == 0
