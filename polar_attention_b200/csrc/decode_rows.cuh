@@ -15,9 +15,10 @@
 // of 65536 dots of 0.77: 0.004 instead of 0, which at a scale of 16 is 0.07 of the
 // gate).  So deviations are summed about means: each step's own, joined to the
 // row's by the number of dots on both sides (Chan, Golub and LeVeque's update), and
-// parts of a row about their common mean: nothing large cancels.  Against the plain
-// sums: 8 nodes of one sequence 12.8 and 12.9 us, 256 selected pages of 16 long
-// sequences 84.3 and 85.4; tcgen05, 26 nodes 65 and 70, 64 nodes 236 and 239.
+// parts of a row about their common mean: nothing large cancels.  Replayed from a
+// graph, with the plain sums and with these: 8 nodes of one sequence 9.0 and 9.6 us,
+// 32 pages of one long sequence 16.0 and 16.4, 256 of 16 sequences 85.7 and 86.2;
+// tcgen05 with 26 nodes 66.4 and 70.3, with 64 nodes 216 and 224.
 #pragma once
 
 #include "launch.cuh"
@@ -295,7 +296,7 @@ __device__ __forceinline__ RowState merge_parts(int count, Part &&part) {
         x.dots.n += __shfl_xor_sync(~0u, x.dots.n, o);
         sum += __shfl_xor_sync(~0u, sum, o);
     }
-    x.dots.mean = x.dots.n > 0.f ? sum / x.dots.n : 0.f;
+    x.dots.mean = x.dots.n > 0.f ? __fdividef(sum, x.dots.n) : 0.f;
 #pragma unroll 4
     for (int k = 0; k < count; ++k) {
         const float *p = part(k);
@@ -384,7 +385,7 @@ __device__ __forceinline__ void spill_states(RowTile<kHR> &t, float *parts, int 
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
             t.m_raw[hr] = fmaxf(t.m_raw[hr], __shfl_xor_sync(0xffffffffu, t.m_raw[hr], o));
         }
-        const float mean = n > 0.f ? sum / n : 0.f, d = t.dots[hr].mean - mean;
+        const float mean = n > 0.f ? __fdividef(sum, n) : 0.f, d = t.dots[hr].mean - mean;
         float m2 = fmaf(t.dots[hr].n * d, d, t.dots[hr].m2);
 #pragma unroll
         for (int o = 1; o <= 2; o <<= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
