@@ -251,9 +251,10 @@ __device__ __forceinline__ void copy_block(uint4 *kv, uint4 *bounds, int3 c, int
 // A growth step of few rows: one cluster, whose first block plans and hands the
 // copies to all.  One launch instead of two, since a loop of such calls spends its
 // time on the launches (append step of 64 rows: 43 us, with two kernels 46).  On
-// the GPU the two kernels are the faster ones, the more so the more rows copy: no
-// copies 4.2 us, this 5.4 to 6.2; half of 64 rows 8.2, this 10.2; of 128 8.2 and
-// 12.4; of 256 8.2 and 14.6.
+// the GPU the two kernels are the faster ones, the more so the more rows copy.
+// Replayed from a graph, two kernels and this, for 1, 16, 64 and 128 rows: without
+// copies 5.2, 4.7, 4.6, 4.9 us and 5.1, 5.5, 5.2, 5.2; where every row copies its
+// tail 10.2, 10.4, 10.2, 10.6 and 10.9, 12.6, 15.5, 21.8.
 __global__ void __launch_bounds__(kPlanThreads)
 cache_reserve_fused_kernel(const ReserveArgs a) {
     __shared__ int3 copies[kFusedRows];
@@ -630,8 +631,8 @@ cudaError_t launch_cache_reserve(const CacheLaunch &a, const int32_t *grow, int3
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     count_launches(2);
-    return launch_ex(cache_reserve_copy_kernel, dim3(std::min(a.num_seqs, 148 * 8)), 128, 0, 1, true,
-                     a.stream, r);
+    return launch_ex(cache_reserve_copy_kernel, dim3(std::min(a.num_seqs, 148 * 8)), 128, 0, 1,
+                     true, a.stream, r);
 }
 
 cudaError_t launch_cache_append(const CacheLaunch &a, const void *k, const void *v, int src_tokens,
@@ -643,7 +644,8 @@ cudaError_t launch_cache_append(const CacheLaunch &a, const void *k, const void 
     p.src_tokens = src_tokens; p.tokens = tokens; p.num_pages = a.num_pages;
     p.max_pages = a.max_pages; p.Hkv = a.Hkv; p.status = a.status;
     // Pages that `tokens` new tokens can touch, from any offset in a page.
-    const long long touched = std::min<long long>(a.max_pages, (tokens - 1ll + kPage - 1) / kPage + 1);
+    const long long touched =
+        std::min<long long>(a.max_pages, (tokens - 1ll + kPage - 1) / kPage + 1);
     if (touched * a.Hkv > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     count_launches(1);
     return launch_ex(cache_append_kernel, dim3(static_cast<unsigned>(touched * a.Hkv), a.num_seqs),
@@ -654,8 +656,8 @@ cudaError_t launch_cache_fork(const CacheLaunch &a, const int32_t *src_table,
                               const int32_t *src_lens, int num_src, const int32_t *src_rows) {
     const int blocks = std::min((a.max_pages + 255) / 256, 64);
     count_launches(1);
-    return launch_ex(cache_fork_kernel, dim3(blocks, a.num_seqs), 256, 0, 1, false, a.stream, a.refs,
-                     a.num_pages, src_table, src_lens, num_src, src_rows, a.table, a.lens,
+    return launch_ex(cache_fork_kernel, dim3(blocks, a.num_seqs), 256, 0, 1, false, a.stream,
+                     a.refs, a.num_pages, src_table, src_lens, num_src, src_rows, a.table, a.lens,
                      a.max_pages, a.status);
 }
 

@@ -136,9 +136,9 @@ struct RowTile {
                     l[hr] += p;
                     l2[hr] = fmaf(p, p, l2[hr]);
                 }
-            // bf16 operand of the second product: half a step (2^-9 relative)
-            // per weight, as in the other decode kernels; l and l2 sum the
-            // unrounded weights.
+            // bf16 operand of the second product: at most half a step (2^-8
+            // relative) per weight, as in the other decode kernels; l and l2
+            // sum the unrounded weights.
             pa[hr][0] = pack_bf16x2(pv[0][0], pv[0][1]);
             pa[hr][1] = pack_bf16x2(pv[1][0], pv[1][1]);
         }
@@ -431,7 +431,8 @@ __device__ __forceinline__ void reduce_rows(RowTile<kHR> &tile, float *parts, in
     for (int r0 = w < kRowWarps ? 4 * (w * C + rank) : nrows; r0 < nrows; r0 += 4 * kRowWarps * C) {
         const int r = min(r0 + (lane >> 3), nrows - 1);
         const bool real = r0 + (lane >> 3) < nrows;
-        fin(r, real, merge_parts(C, [&](int k) { return cluster_map(own + r * kPartialFloats, k); }));
+        fin(r, real,
+            merge_parts(C, [&](int k) { return cluster_map(own + r * kPartialFloats, k); }));
     }
     cluster_sync();  // no CTA leaves while its states are read
 }

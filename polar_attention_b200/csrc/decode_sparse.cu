@@ -383,8 +383,9 @@ __global__ void __launch_bounds__(kSelThreads) sparse_select_kernel(const Select
         __syncthreads();
         for (int i = w; i < mid; i += kWarps) {
             const int phys = pt[few[i].x];
-            const uint32_t k = phys >= 0 && phys < a.num_pages
-                ? exact_key<G>(q, a.bounds + (static_cast<size_t>(phys) * a.Hkv + g) * 16, lane) : 0u;
+            const bool ok = phys >= 0 && phys < a.num_pages;
+            const size_t at = (static_cast<size_t>(ok ? phys : 0) * a.Hkv + g) * 16;
+            const uint32_t k = ok ? exact_key<G>(q, a.bounds + at, lane) : 0u;
             if (lane == 0) few[i].y = static_cast<int>(k);
         }
         __syncthreads();
@@ -606,8 +607,8 @@ cudaError_t launch_all(const SparseLaunch &a, const CUtensorMap &map, const Layo
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(configured.load() & bit)) {
-        e = cudaFuncSetAttribute(sparse_split_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSmem);
+        e = cudaFuncSetAttribute(sparse_split_kernel<G>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(sparse_select_kernel<G>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -617,7 +618,8 @@ cudaError_t launch_all(const SparseLaunch &a, const CUtensorMap &map, const Layo
     }
     char *ws = static_cast<char *>(a.workspace);
     int32_t *sel = a.selected ? a.selected : reinterpret_cast<int32_t *>(ws + l.selected);
-    const uint4 *q = static_cast<const uint4 *>(a.q), *bounds = static_cast<const uint4 *>(a.bounds);
+    const uint4 *q = static_cast<const uint4 *>(a.q);
+    const uint4 *bounds = static_cast<const uint4 *>(a.bounds);
     SelectArgs s{q, bounds, a.page_table, a.seqlens, sel, reinterpret_cast<uint32_t *>(ws),
                  a.num_pages, a.max_pages, a.Hkv, a.keep, a.status};
     // Blocks of a row, with two steps of the scores each (one block a row: 512 pages
@@ -639,8 +641,8 @@ cudaError_t launch_all(const SparseLaunch &a, const CUtensorMap &map, const Layo
     p.Hq = a.Hq; p.Hkv = a.Hkv; p.keep = a.keep; p.splits = l.splits;
     const float L = static_cast<float>(a.L);
     p.ep = Epilogue{a.s, a.alpha, L, a.beta, 1.0f / logf(L)};
-    e = launch_ex(sparse_split_kernel<G>, dim3(l.cluster * l.splits, a.Hkv, a.num_seqs), kRowThreads,
-                  kSmem, l.cluster, true, a.stream, map, p);
+    e = launch_ex(sparse_split_kernel<G>, dim3(l.cluster * l.splits, a.Hkv, a.num_seqs),
+                  kRowThreads, kSmem, l.cluster, true, a.stream, map, p);
     if (e != cudaSuccess) return e;
     count_launches(2);
     if (l.splits > 1) {

@@ -58,7 +58,8 @@ tree_split_kernel(const __grid_constant__ CUtensorMap kv_map,
     if (row0 >= R) return;
     const int len = a.seqlens[seq];
     const int npg = (len + kPage - 1) / kPage;
-    const int per = (npg + a.splits * C) / (a.splits * C);  // of npg + 1 steps: the drafted rows last
+    // Of npg + 1 steps: the drafted rows last.
+    const int per = (npg + a.splits * C) / (a.splits * C);
     const int p0 = min(part * per, npg + 1);
     const int np = min(npg + 1, p0 + per) - p0;
     const int32_t *pt = a.page_table + static_cast<size_t>(seq) * a.max_pages + p0;

@@ -21,7 +21,7 @@ struct TreeArgs {
 };
 
 struct TreePlan {  // the mma.sync kernel's grid
-    int tile_rows;  // 8, 16 or 32
+    int tile_rows;  // 8 or 16
     int row_tiles, cluster, splits;
 };
 

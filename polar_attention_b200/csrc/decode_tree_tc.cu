@@ -19,19 +19,19 @@
 // A CTA's step is one chain; 128 columns (S, O) and two 16 KB stages are all it
 // needs, so four CTAs share an SM and cover each other's waits.
 //
-// What bounds it (64 nodes, 8 sequences of 32K-64K, 215-232 us): per SM and step of a
-// full tile about 1100 clocks.  Alone on its SM a chain takes 2100 for a step: 270
-// and 180 to issue the products, about 300 until each is seen, 900 for the weights
-// and sums, of which 512 are exponentials (16 an SM and clock), 200 to reach tensor
-// memory and back.  Four chains come to 1100, not to a quarter of 2100: the
-// products' pipe is busy for 36 % of the time, exponentials 46 %, issue slots 47 %,
-// and they wait for one another.  Loads do not bound it (half of them left out, or all from one page: the
-// same time).  Measured besides: two threads a row in clusters of eight CTAs, two an
-// SM, 310-330 us; equal shares with a 64-key buffer and one thread for copies and
-// products 268 us, with two 32-key buffers 255 us, with 128-key steps and two CTAs
-// an SM 283 us; two 64-key buffers and two CTAs an SM 235 us; three chains with the
-// next scores formed during a step's weights (160 columns a chain, one CTA of 480
-// threads) 230-240 us.
+// What bounds it (64 nodes, 8 sequences of 32K-64K, 221-250 us): the four chains of an
+// SM wait for one another.  The products' pipe is busy for 34 % of the time,
+// exponentials 45 %, issue slots 48 %.  Measured while the raw scores were summed
+// without means (215-232 us): per SM and step of a full tile about 1100 clocks; a
+// chain alone on its SM 2100 for a step, 270 and 180 of them to issue the products,
+// about 300 until each is seen, 900 for the weights and sums, of which 512 are
+// exponentials (16 an SM and clock), 200 to reach tensor memory and back.  Loads do
+// not bound it (half of them left out, or all from one page: the same time).  Tried
+// then: two threads a row in clusters of eight CTAs, two an SM, 310-330 us; equal
+// shares with a 64-key buffer and one thread for copies and products 268 us, with
+// two 32-key buffers 255 us, with 128-key steps and two CTAs an SM 283 us; two
+// 64-key buffers and two CTAs an SM 235 us; three chains with the next scores formed
+// during a step's weights (160 columns a chain, one CTA of 480 threads) 230-240 us.
 //
 // The reference max of a row moves only when a logit exceeds it by more than
 // 2^24 (kTcThreshold), and then to a whole number of log2 units: weights are
@@ -129,7 +129,8 @@ __device__ __forceinline__ TileSums tile_pass(const uint32_t (&sr)[32], uint32_t
 }
 
 // Sum of squares of a thread's 32 scores about `mean`, of those that count.
-__device__ __forceinline__ float squares_about(const uint32_t (&sr)[32], uint32_t mask, float mean) {
+__device__ __forceinline__ float squares_about(const uint32_t (&sr)[32], uint32_t mask,
+                                               float mean) {
     const float2 off = make_float2(-mean, -mean);
     float2 a = make_float2(0.f, 0.f);
 #pragma unroll
@@ -256,8 +257,10 @@ __device__ __forceinline__ long long steps_of(const TreeArgs &a, int seq) {
 
 template <int G>
 __global__ void __launch_bounds__(kTcThreads, kTcPerSm)
-tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
-               const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
+               const __grid_constant__ CUtensorMap kv_map,
+               const __grid_constant__ CUtensorMap k_map,
+               const __grid_constant__ CUtensorMap v_map,
                const TreeArgs a, SharedTile *__restrict__ shared_tiles) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -299,7 +302,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
     __syncthreads();
     all = 0;
     for (int i = 0; i < kTcThreads / 32; ++i) all += wide[i];
-    const long long share = max((all + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinShare));
+    const long long share =
+        max((all + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinShare));
     const long long first = min(cta * share, all), count = min(share, all - first);
     if (count == 0) return;
     long long before = 0;
@@ -649,8 +653,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                 }
             };
             if (s0 > 0 || s0 + cnt <= npg) {  // a shared tile: its state for the merge
-                float *part = a.partials + static_cast<size_t>(2 * cta + (segment > 0)) * kSlotFloats +
-                              r_tile * kPartialFloats;
+                const size_t slot = 2 * cta + (segment > 0);
+                float *part = a.partials + slot * kSlotFloats + r_tile * kPartialFloats;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[16];
@@ -689,9 +693,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                     for (int e = 0; e < 16; e += 2) {
                         const float2 uu = *reinterpret_cast<const float2 *>(a.u + h * kHeadDim +
                                                                             16 * c + e);
-                        y[e >> 1] = n > 0 ? pack_bf16(fmaf(mag, uu.x, __uint_as_float(o[e]) * inv),
-                                                      fmaf(mag, uu.y, __uint_as_float(o[e + 1]) * inv))
-                                          : 0u;
+                        const float y0 = fmaf(mag, uu.x, __uint_as_float(o[e]) * inv);
+                        const float y1 = fmaf(mag, uu.y, __uint_as_float(o[e + 1]) * inv);
+                        y[e >> 1] = n > 0 ? pack_bf16(y0, y1) : 0u;
                     }
                     uint4 *dst = reinterpret_cast<uint4 *>(a.out + out_row * kHeadDim + 16 * c);
                     dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
@@ -803,8 +807,8 @@ cudaError_t launch_tree_tc(const CUtensorMap &kv, const CUtensorMap &k, const CU
     const uint64_t strides[2] = {kHeadDim * 2, static_cast<uint64_t>(t.Hq) * kHeadDim * 2};
     const uint32_t box[3] = {kHeadDim, static_cast<uint32_t>(G),
                              static_cast<uint32_t>(kTileRows / G)};
-    if (encode_tiled(&q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16 *>(t.q), dims,
-                     strides, box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    if (encode_tiled(&q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16 *>(t.q),
+                     dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     switch (G) {
         case 1: return launch_tc<1>(q, kv, k, v, t, ctas, stream);
@@ -832,7 +836,7 @@ struct CountingPort {
     template <typename Share> void load_step(const Share &, int, int st) { ++steps[st]; }
     void queries_landed(uint32_t parity) { landed(queries, parity); }
     void step_landed(int st, uint32_t parity) { landed(steps[st], parity); }
-    void landed(int &loads, uint32_t parity) {  // of a barrier: loads 0, 1, .. have parities 0, 1, ..
+    void landed(int &loads, uint32_t parity) {  // a barrier's loads have parities 0, 1, 0, ..
         if (loads == 0 || ((loads - 1) & 1u) != parity) ++missed;
         loads = 0;
     }

@@ -21,8 +21,9 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // The instructions are for whole warps: a warp comes together first.
 __device__ __forceinline__ void cluster_sync() {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
+    asm volatile(
+        "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+            : "memory");
 }
 // The same shared-memory address in the cluster's CTA `rank` (generic).
 template <typename T>
