@@ -270,3 +270,17 @@ def test_row_is_that_of_the_selected_pages(cuda_ok):
             R.check_rows(out[i, heads], neff[i, heads], refs)
             R.check_rows(want[i, heads], nwant[i, heads], refs)
     assert pa.get_status() == 0
+
+
+@pytest.mark.parametrize("G,keep", [(1, 3), (4, 8), (8, 20)])
+def test_counts_of_the_directions_size(cuda_ok, G, keep):
+    """Values alike and u of order one: mean, spread and n_eff are seen in the
+    outputs, from one key to all of the selected pages."""
+    x = inputs([1, 2, 17, 64, 65, 700, 64 * keep, 3000], 2 * G, 2, seed=17)
+    rng = np.random.default_rng(17)
+    key = R.at_angle(np.eye(64)[0], 0.2, (), rng)
+    x["kv"][:, 1] = torch.from_numpy(R.at_angle(key, 0.99, x["kv"][:, 1].shape[:-1], rng)).bfloat16()
+    x["u"] = torch.from_numpy(rng.choice([-1.0, 1.0], x["u"].shape)).float()
+    out, neff, sel = call(cuda(x), keep)
+    assert pa.get_status() == 0
+    check(x, keep, out, neff, sel)

@@ -419,3 +419,22 @@ def test_keys_that_are_alike(cuda_ok, G, M, max_pages, kind):
     assert pa.get_status() == 0
     rows = {(i, t, h) for i in (0, 1) for t in {0, M // 3, M // 2, M - 1} for h in {0, G - 1}}
     check(x, out, neff, [M, M], rows, L=2048)
+
+
+@pytest.mark.parametrize("max_pages", [13, WIDE])
+@pytest.mark.parametrize("G,M", [(1, 2), (4, 5), (8, 1), (8, 3), (2, 31), (4, 64)])
+def test_counts_of_the_directions_size(cuda_ok, G, M, max_pages):
+    """Few keys and many, with values alike and u of order one: the outputs' size
+    is the count's, so that mean, spread and n_eff are seen in them."""
+    lens = [0, 1, 2, 3, 17, 63, 64, 65, 130, 700]
+    x = inputs(lens, M, 2 * G, 2, seed=18, max_pages=max_pages)
+    rng = np.random.default_rng(18)
+    key = R.at_angle(np.eye(64)[0], 0.2, (), rng)
+    x["kv"][:, 1] = torch.from_numpy(R.at_angle(key, 0.99, x["kv"][:, 1].shape[:-1], rng)).bfloat16()
+    x["v"] = torch.from_numpy(R.at_angle(key, 0.99, x["v"].shape[:-1], rng)).bfloat16()
+    near = x["kv"][:, 0].float() + 0.5 * x["kv"][:, 0, :, :1].float()  # a page's keys alike
+    x["kv"][:, 0] = (near / near.norm(dim=-1, keepdim=True)).bfloat16()
+    x["u"] = torch.from_numpy(rng.choice([-1.0, 1.0], x["u"].shape)).float()
+    out, neff = call(cuda(x))
+    assert pa.get_status() == 0
+    check(x, out, neff, [M] * len(lens), what=f"G={G} M={M}")
